@@ -29,7 +29,9 @@ STATUS = {0: "FP4Q_OK", 1: "FP4Q_E_NULL", 2: "FP4Q_E_SHAPE", 3: "FP4Q_E_ALIGN", 
 EXPORTS = ["fp4q_workspace_create", "fp4q_workspace_destroy", "fp4q_workspace_set_wait", "fp4q_workspace_fallbacks",
            "fp4q_quantize_nvfp4", "fp4q_quantize_nvfp4_noalloc", "fp4q_quantize_nvfp4_2d", "fp4q_quantize_mxfp4", "fp4q_quantize_mxfp6",
            "fp4q_quantize_if4", "fp4q_quantize_variant", "fp4q_dequantize_variant", "fp4q_rht", "fp4q_gemm_mxfp4", "fp4q_gemm_nvfp4", "fp4q_dequantize", "fp4q_amax",
-           "fp4q_rht_signs_from_seed", "fp4q_status_string", "fp4q_abi_version"]
+           "fp4q_rht_signs_from_seed", "fp4q_status_string", "fp4q_abi_version",
+           "fp4q_quantize_mxfp8", "fp4q_dequantize_mxfp8", "fp4q_rmsnorm_mxfp8", "fp4q_rmsnorm_backward",
+           "fp4q_rmsnorm_backward_scratch"]
 
 
 class Fp4qError(RuntimeError):
@@ -40,6 +42,7 @@ class Fp4qError(RuntimeError):
 
 _lib = None
 _P, _I64, _U64, _I, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_int, ctypes.c_uint
+_F = ctypes.c_float
 
 
 def lib() -> ctypes.CDLL:
@@ -71,12 +74,18 @@ def lib() -> ctypes.CDLL:
             "fp4q_rht_signs_from_seed": [_U64, _P],
             "fp4q_status_string": [_I],
             "fp4q_abi_version": [],
+            "fp4q_quantize_mxfp8": [_P, _I, _I64, _I64, _P, _P, _P],
+            "fp4q_dequantize_mxfp8": [_P, _P, _I64, _I64, _I, _P, _P],
+            "fp4q_rmsnorm_mxfp8": [_P, _P, _I, _I64, _I64, _P, _F, _P, _P, _P, _P, _P, _P],
+            "fp4q_rmsnorm_backward": [_P, _P, _P, _I, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P],
+            "fp4q_rmsnorm_backward_scratch": [_I64, _I64],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
             fn.restype = _I
         L.fp4q_rht_signs_from_seed.restype = None
+        L.fp4q_rmsnorm_backward_scratch.restype = _I64
         L.fp4q_status_string.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -254,6 +263,33 @@ def fp4q_abi_version() -> int:
     return lib().fp4q_abi_version()
 
 
+def fp4q_quantize_mxfp8(x, dt, rows, cols, codes, scales, stream=None) -> int:
+    return _check("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
+        _p(x), dt, rows, cols, _p(codes), _p(scales), _s(stream)))
+
+
+def fp4q_dequantize_mxfp8(codes, scales, rows, cols, out_dt, y, stream=None) -> int:
+    return _check("fp4q_dequantize_mxfp8", lib().fp4q_dequantize_mxfp8(
+        _p(codes), _p(scales), rows, cols, out_dt, _p(y), _s(stream)))
+
+
+def fp4q_rmsnorm_mxfp8(x, residual, dt, rows, cols, gain, eps, codes, scales, sum, rstd, y, stream=None) -> int:
+    return _check("fp4q_rmsnorm_mxfp8", lib().fp4q_rmsnorm_mxfp8(
+        _p(x), _p(residual), dt, rows, cols, _p(gain), eps, _p(codes), _p(scales), _p(sum), _p(rstd), _p(y),
+        _s(stream)))
+
+
+def fp4q_rmsnorm_backward_scratch(rows: int, cols: int) -> int:
+    return lib().fp4q_rmsnorm_backward_scratch(rows, cols)
+
+
+def fp4q_rmsnorm_backward(dy, s, dsum, dt, rows, cols, gain, rstd, dx, dgain, scratch, scratch_bytes,
+                          stream=None) -> int:
+    return _check("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
+        _p(dy), _p(s), _p(dsum), dt, rows, cols, _p(gain), _p(rstd), _p(dx), _p(dgain), _p(scratch), scratch_bytes,
+        _s(stream)))
+
+
 # --- allocation helpers --------------------------------------------------------------
 
 def _dt(x: torch.Tensor) -> int:
@@ -407,3 +443,107 @@ def dequantize_variant(var: int, codes, scales, tensor_scale, rows: int, cols: i
     y = torch.empty(rows, cols, dtype=out_dtype, device=codes.device)
     fp4q_dequantize_variant(var, codes, scales, tensor_scale, rows, cols, _dt(y), y, stream)
     return y
+
+
+# --- MXFP8 activations -------------------------------------------------------------------
+#
+# These helpers check what the C entry points cannot see (the tensors' types, shapes, devices
+# and strides) before any address is passed on.
+
+_NAMES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _need(name: str, t, dtype, shape, device) -> None:
+    """`t` is a dense tensor of this type (one of them), shape and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor is needed, got {type(t).__name__}")
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{name}: {dtype} is needed, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: is on {t.device}, the call's other tensors on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a dense row-major tensor is needed (call .contiguous())")
+
+
+def _on_current(t: torch.Tensor) -> None:
+    """Kernels are launched on the current device: the tensors have to be there."""
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors on {t.device}, but device {torch.cuda.current_device()} is current "
+                         "(use torch.cuda.device)")
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Device memory for one call on `stream`; the allocator does not hand it out again before
+    the stream has passed the call, also when that is not the current stream."""
+    t = _u8(nbytes, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return t
+
+
+def _rows_of(name: str, x) -> tuple[int, int, int, torch.device]:
+    """(fp4q dtype, rows, cols, device) of a dense 2-D bf16 or fp32 device tensor."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _NAMES:
+        raise TypeError(f"{name}: a bfloat16 or float32 tensor is needed")
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name}: a dense row-major [rows][cols] tensor on the GPU is needed")
+    _on_current(x)
+    return _NAMES[x.dtype], x.shape[0], x.shape[1], x.device
+
+
+def quantize_mxfp8(x: torch.Tensor, stream=None) -> dict:
+    """MXFP8: codes [rows][cols] (E4M3), E8M0 scales [rows][cols/32]."""
+    dt, rows, cols, dev = _rows_of("x", x)
+    out = {"codes": _u8(rows, cols, device=dev), "scales": _u8(rows, cols // 32, device=dev)}
+    fp4q_quantize_mxfp8(x, dt, rows, cols, out["codes"], out["scales"], stream)
+    return out
+
+
+def dequantize_mxfp8(q: dict, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """The values of MXFP8 codes and scales as quantize_mxfp8 returns them."""
+    codes, scales = q["codes"], q["scales"]
+    rows, cols = codes.shape
+    _need("codes", codes, torch.uint8, (rows, cols), codes.device)
+    _need("scales", scales, torch.uint8, (rows, cols // 32), codes.device)
+    y = torch.empty(rows, cols, dtype=out_dtype, device=codes.device)
+    fp4q_dequantize_mxfp8(codes, scales, rows, cols, _dt(y), y, stream)
+    return y
+
+
+def rmsnorm_mxfp8(x: torch.Tensor, gain: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                  with_y: bool = False, in_place: bool = False, stream=None) -> dict:
+    """RMS norm of x + residual with `gain` (float32) into MXFP8.
+
+    Returns codes, scales, rstd, sum (x + residual in x's type; x itself without a residual)
+    and, with ``with_y``, the unquantized y.  ``in_place`` writes the sum over `residual`."""
+    dt, rows, cols, dev = _rows_of("x", x)
+    _need("gain", gain, torch.float32, (cols,), dev)
+    if residual is not None:
+        _need("residual", residual, x.dtype, x.shape, dev)
+    out = {"codes": _u8(rows, cols, device=dev), "scales": _u8(rows, cols // 32, device=dev),
+           "rstd": torch.empty(rows, dtype=torch.float32, device=dev)}
+    out["sum"] = x if residual is None else residual if in_place else torch.empty_like(x)
+    if with_y:
+        out["y"] = torch.empty_like(x)
+    fp4q_rmsnorm_mxfp8(x, residual, dt, rows, cols, gain, eps, out["codes"], out["scales"],
+                       None if residual is None else out["sum"], out["rstd"], out.get("y"), stream)
+    return out
+
+
+def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gain: torch.Tensor, rstd: torch.Tensor,
+                     dsum: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dgain) of rmsnorm_mxfp8 from its `sum` and `rstd`; `dsum` is the gradient that reaches
+    the sum from elsewhere, added to dx."""
+    dt, rows, cols, dev = _rows_of("dy", dy)
+    _need("s", s, dy.dtype, dy.shape, dev)
+    _need("gain", gain, torch.float32, (cols,), dev)
+    _need("rstd", rstd, torch.float32, (rows,), dev)
+    if dsum is not None:
+        _need("dsum", dsum, dy.dtype, dy.shape, dev)
+    dx, dgain = torch.empty_like(dy), torch.empty(cols, dtype=torch.float32, device=dev)
+    need = fp4q_rmsnorm_backward_scratch(rows, cols)
+    scratch = _scratch(need, dev, stream)
+    fp4q_rmsnorm_backward(dy, s, dsum, dt, rows, cols, gain, rstd, dx, dgain, scratch, need, stream)
+    return dx, dgain

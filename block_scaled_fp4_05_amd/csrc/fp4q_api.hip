@@ -4,6 +4,7 @@
 #include "../../include/fp4q.h"
 #include "fp4q_internal.hpp"
 
+#include <float.h>
 #include <mutex>
 #include <new>
 #include <stdint.h>
@@ -24,6 +25,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool valid_dtype(int d) { return d == FP4Q_F32 || d == FP4Q_BF16; }
 bool valid_round(int r) { return r == FP4Q_RTN || r == FP4Q_SR; }
+
+// Shape of an MXFP8 tensor: whole blocks, and few enough elements (2^36, 64 GiB of codes) that a
+// launch's thread count stays within 32 bits.
+bool mx_shape(int64_t rows, int64_t cols) {
+  return rows > 0 && cols > 0 && cols % 32 == 0 && rows <= INT32_MAX && cols <= INT32_MAX &&
+         rows <= ((int64_t)1 << 36) / cols;
+}
 
 // Sink of a two-pass call's amax pass and the matching source for its quantizer: the
 // workspace's two-pass state when there is one, else the caller's float (which the
@@ -374,6 +382,58 @@ fp4q_status fp4q_dequantize(fp4q_format fmt, const uint8_t* codes, const uint8_t
   if (!aligned16(codes) || !aligned16(scales) || !aligned16(y) || (tensor_scale && !aligned4(tensor_scale)))
     return FP4Q_E_ALIGN;
   fp4q::launch_dequant(fmt, codes, scales, tensor_scale, rows, cols, out_dt, y, stream);
+  return after_launch();
+}
+
+fp4q_status fp4q_quantize_mxfp8(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, uint8_t* codes,
+                                uint8_t* scales, hipStream_t stream) {
+  if (!x || !codes || !scales) return FP4Q_E_NULL;
+  if (!valid_dtype(dt)) return FP4Q_E_ARG;
+  if (!mx_shape(rows, cols)) return FP4Q_E_SHAPE;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return FP4Q_E_ALIGN;
+  fp4q::launch_mxfp8(x, dt, rows, cols, codes, scales, stream);
+  return after_launch();
+}
+
+fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                  fp4q_dtype out_dt, void* y, hipStream_t stream) {
+  if (!codes || !scales || !y) return FP4Q_E_NULL;
+  if (!valid_dtype(out_dt)) return FP4Q_E_ARG;
+  if (!mx_shape(rows, cols)) return FP4Q_E_SHAPE;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return FP4Q_E_ALIGN;
+  fp4q::launch_dequant_mxfp8(codes, scales, rows, cols, out_dt, y, stream);
+  return after_launch();
+}
+
+fp4q_status fp4q_rmsnorm_mxfp8(const void* x, const void* residual, fp4q_dtype dt, int64_t rows, int64_t cols,
+                               const float* gain, float eps, uint8_t* codes, uint8_t* scales, void* sum,
+                               float* rstd, void* y, hipStream_t stream) {
+  if (!x || !gain || !codes || !scales) return FP4Q_E_NULL;
+  if (!valid_dtype(dt) || !(eps >= 0.0f) || eps > FLT_MAX) return FP4Q_E_ARG;
+  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return FP4Q_E_SHAPE;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(codes) || !aligned16(scales) ||
+      !aligned16(sum) || !aligned4(rstd) || !aligned16(y))
+    return FP4Q_E_ALIGN;
+  fp4q::launch_rmsnorm(x, residual, dt, rows, cols, gain, eps, codes, scales, sum, rstd, y, stream);
+  return after_launch();
+}
+
+int64_t fp4q_rmsnorm_backward_scratch(int64_t rows, int64_t cols) {
+  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return 0;
+  return fp4q::rmsnorm_backward_scratch(rows, cols);
+}
+
+fp4q_status fp4q_rmsnorm_backward(const void* dy, const void* s, const void* dsum, fp4q_dtype dt, int64_t rows,
+                                  int64_t cols, const float* gain, const float* rstd, void* dx, float* dgain,
+                                  void* scratch, int64_t scratch_bytes, hipStream_t stream) {
+  if (!dy || !s || !gain || !rstd || !dx || !dgain || !scratch) return FP4Q_E_NULL;
+  if (!valid_dtype(dt)) return FP4Q_E_ARG;
+  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return FP4Q_E_SHAPE;
+  if (scratch_bytes < fp4q::rmsnorm_backward_scratch(rows, cols)) return FP4Q_E_ARG;
+  if (!aligned16(dy) || !aligned16(s) || !aligned16(dsum) || !aligned16(gain) || !aligned4(rstd) || !aligned16(dx) ||
+      !aligned16(dgain) || !aligned16(scratch))
+    return FP4Q_E_ALIGN;
+  fp4q::launch_rmsnorm_backward(dy, s, dsum, dt, rows, cols, gain, rstd, dx, dgain, scratch, stream);
   return after_launch();
 }
 

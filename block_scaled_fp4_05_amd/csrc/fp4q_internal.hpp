@@ -121,4 +121,16 @@ bool launch_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* a_scales, const fl
                        const uint8_t* b_scales, const float* b_ts, int64_t m, int64_t n, int64_t k, bool bf16_out,
                        void* c, float* amax, unsigned flags, hipStream_t st);
 
+// MXFP8 quantize, dequantize; the RMS norm into MXFP8 and its gradient -- fp4q_mxfp8.hip.
+void launch_mxfp8(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                  hipStream_t st);
+void launch_dequant_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int out_dtype,
+                          void* y, hipStream_t st);
+void launch_rmsnorm(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const float* gain,
+                    float eps, uint8_t* codes, uint8_t* scales, void* sum, float* rstd, void* y, hipStream_t st);
+int64_t rmsnorm_backward_scratch(int64_t rows, int64_t cols);
+void launch_rmsnorm_backward(const void* dy, const void* s, const void* dsum, int dtype, int64_t rows, int64_t cols,
+                             const float* gain, const float* rstd, void* dx, float* dgain, void* scratch,
+                             hipStream_t st);
+
 }  // namespace fp4q

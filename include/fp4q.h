@@ -367,6 +367,67 @@ fp4q_status fp4q_dequantize(fp4q_format fmt, const uint8_t* codes, const uint8_t
                             const float* tensor_scale, int64_t rows, int64_t cols,
                             fp4q_dtype out_dt, void* y, hipStream_t stream);
 
+/*
+ * MXFP8: 32 elements + one E8M0 scale, elements OCP E4M3 (e4m3fn: largest 448, smallest
+ * step 2^-9, one NaN magnitude 0x7F) [GL "FP4の仕組み" for the 32 + E8M0 block; F6].  The
+ * activation operand of a product with MXFP4 weights (fp4q_gemm_mxfp8_mxfp4,
+ * fp4q_moe_mxfp4).  Per block, with b the largest finite magnitude, the scale code is the
+ * smallest c >= 0 with b <= 448 * 2^(c - 127), so no element saturates (the 4- and 6-bit
+ * formats round the scale to nearest and clip up to a third of the block maximum; with
+ * E4M3's 18 binades the one binade this costs at the bottom is worth less than the
+ * clipping); elements are x * 2^(127 - c) rounded to nearest, ties to the even code, sign
+ * copied.  NaN and infinite inputs give a NaN code (0x7F or 0xFF) and leave the block's
+ * scale to its finite elements.  RTN only.
+ *   codes [rows][cols], scales [rows][cols/32].   Shapes: cols % 32 == 0.
+ */
+fp4q_status fp4q_quantize_mxfp8(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, uint8_t* codes,
+                                uint8_t* scales, hipStream_t stream);
+
+/* x_hat = e4m3(code) * 2^(scale - 127) (scale 255: NaN); out_dt FP4Q_F32, or FP4Q_BF16
+ * (RNE of the float value).  Shapes as fp4q_quantize_mxfp8; y [rows][cols]. */
+fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                  fp4q_dtype out_dt, void* y, hipStream_t stream);
+
+/*
+ * Residual addition, root-mean-square norm and MXFP8 in one read of x:
+ *   s = x + residual (x without one),  r = 1 / sqrt(mean(s^2) + eps),  n = (s r) gain,
+ *   codes, scales = MXFP8(n) as fp4q_quantize_mxfp8 writes it.
+ * All of it in fp32 from the unrounded s; what is stored is rounded once.
+ *   x, residual  [rows][cols] of type dt; residual may be NULL.
+ *   gain         device float [cols].        eps >= 0, finite.
+ *   sum          s in type dt, or NULL.  It may be x itself or residual itself (in place);
+ *                no other overlap.
+ *   rstd         device float [rows] or NULL: r, for fp4q_rmsnorm_backward.
+ *   y            n in type dt, or NULL (e.g. a router's input).
+ * A row with a NaN gives NaN codes throughout; a row whose sum of squares overflows gives
+ * r = 0 (its finite elements 0, its infinite ones NaN), as the formula does.
+ * Shapes: cols % 32 == 0, cols <= 32768, rows < 2^31.  Alignment: 16 bytes (rstd 4).
+ */
+#define FP4Q_NORM_MAX_COLS 32768
+fp4q_status fp4q_rmsnorm_mxfp8(const void* x, const void* residual, fp4q_dtype dt, int64_t rows, int64_t cols,
+                               const float* gain, float eps, uint8_t* codes, uint8_t* scales, void* sum,
+                               float* rstd, void* y, hipStream_t stream);
+
+/*
+ * Gradient of the norm (straight through the rounding to MXFP8), from the stored s and r:
+ *   a = dy gain,   dx = r a - s r^3 mean(a s) + dsum,   dgain = sum over rows of dy s r.
+ * dx is the gradient of x and of the residual alike.
+ *   dy, s  [rows][cols] of type dt (s: the forward call's sum, or its x without a residual).
+ *   rstd   device float [rows];  gain device float [cols].
+ *   dsum   [rows][cols] of type dt or NULL: the gradient that reaches s from elsewhere (the
+ *          residual stream).
+ *   dx     [rows][cols] of type dt; may be dy or dsum itself (in place).
+ *   dgain  device float [cols].  Summed in a fixed order: the same inputs give the same bits.
+ *   scratch  device memory of at least fp4q_rmsnorm_backward_scratch(rows, cols) bytes, 16-byte
+ *          aligned; its contents before and after the call mean nothing.
+ * Shapes and alignment as fp4q_rmsnorm_mxfp8.
+ */
+fp4q_status fp4q_rmsnorm_backward(const void* dy, const void* s, const void* dsum, fp4q_dtype dt, int64_t rows,
+                                  int64_t cols, const float* gain, const float* rstd, void* dx, float* dgain,
+                                  void* scratch, int64_t scratch_bytes, hipStream_t stream);
+/* Bytes of scratch for that call (0 for a shape it refuses).  Host only. */
+int64_t fp4q_rmsnorm_backward_scratch(int64_t rows, int64_t cols);
+
 /* max |x| over the whole matrix, written to device float *amax. */
 fp4q_status fp4q_amax(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, float* amax,
                       hipStream_t stream);

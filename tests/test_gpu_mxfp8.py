@@ -1,0 +1,230 @@
+"""MXFP8 quantizer and its inverse, the RMS norm into MXFP8 and its gradient (GPU), against
+binary64.
+
+Rounding bounds, in units u = 2^-24 of one fp32 rounding:
+ - rstd: a thread adds at most 32 squares, then 6 + 16 partial sums: 54 u on the sum of squares,
+   half of it on the root, and 5 u for the mean, eps, the root and the division: 32 u.
+ - y = (s r) gain: 32 u, one for s, two products: 35 u; 40 u is allowed.
+ - dot products of the gradient: 54 u of the sum of magnitudes, and up to 8 roundings around it.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_ref as ref
+from block_scaled_fp4_05_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+VAL = ref.e4m3_values()
+
+
+def _rand(rows, cols, dtype, seed, gain=1.0, outliers=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * gain
+    if outliers:
+        x[:, ::37] *= 20.0
+    return x.to(DTYPES[dtype]).to(DEV)
+
+
+def _np(t):
+    return t.float().cpu().numpy().astype(np.float64) if t.is_floating_point() else t.cpu().numpy()
+
+
+def _check_codes(q, y, delta):
+    """codes and scales are MXFP8 of values within a relative `delta` of y."""
+    codes, scales = _np(q["codes"]), _np(q["scales"]).astype(np.int64)
+    bmax = np.abs(y).reshape(y.shape[0], -1, 32).max(-1)
+    assert np.all(scales >= ref.scale_code(bmax * (1 - delta))) and np.all(scales <= ref.scale_code(bmax * (1 + delta)))
+    k = np.repeat(np.ldexp(1.0, (127 - scales).astype(np.int32)), 32, axis=-1)
+    lo, hi = np.sort([ref.e4m3_round(np.clip(y * k * f, -448, 448)) for f in (1 - delta, 1 + delta)], axis=0)
+    v = VAL[codes]
+    assert np.all((v >= lo) & (v <= hi))
+    assert np.array_equal(codes >> 7, np.signbit(y).astype(np.uint8))
+
+
+SHAPES = [(1, 32), (1, 64), (3, 96), (2, 4096), (1021, 160), (65, 2080), (257, 1056)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_quantize_is_exact(shape, dtype):
+    x = _rand(*shape, dtype, seed=sum(shape))
+    print("mxfp8", shape, dtype, flush=True)
+    q = B.quantize_mxfp8(x)
+    v, c = ref.quantize(_np(x))
+    assert np.array_equal(_np(q["scales"]), c)
+    assert np.array_equal(VAL[_np(q["codes"])], v)
+    for out in (torch.float32, torch.bfloat16):   # E4M3 times a power of two is exact in both
+        assert np.array_equal(_np(B.dequantize_mxfp8(q, out)), ref.dequantize(_np(q["codes"]), _np(q["scales"])))
+
+
+def test_quantize_edges():
+    x = np.zeros((6, 128), np.float32)
+    x[0, :32] = -0.0
+    x[0, 32:64] = np.float32(1e-45) * np.arange(32)           # subnormal inputs, scale 0
+    x[0, 64] = 2.0 ** -119 * 1.75                             # the largest block of scale code 0
+    x[0, 96] = np.nextafter(np.float32(2.0 ** -119 * 1.75), np.float32(1))
+    x[1] = 3.4028235e38 * np.linspace(-1, 1, 128)
+    x[2, ::2] = 448.0                                          # the largest element: exactly 448
+    x[3, 0], x[3, 32], x[3, 64] = 448.0, np.nextafter(np.float32(448), np.float32(1e9)), 449.0
+    x[4] = np.ldexp(17.0 + (np.arange(128) % 2), np.arange(128) % 12 - 12)   # ties of the significand
+    x[5] = np.ldexp(np.arange(128) - 64.0, -10)                # ties among subnormal codes ...
+    x[5, ::32] = 448.0                                         # ... of scale 1
+    d = torch.from_numpy(x).to(DEV)
+    q = B.quantize_mxfp8(d)
+    v, c = ref.quantize(x)
+    assert np.array_equal(_np(q["scales"]), c)
+    assert np.array_equal(VAL[_np(q["codes"])], v)
+    assert np.array_equal(_np(q["codes"]) >> 7, np.signbit(x).astype(np.uint8))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_quantize_not_finite(dtype):
+    x = _rand(5, 96, dtype, 3)
+    x[0, 5], x[1, 40], x[2, 70] = float("inf"), float("-inf"), float("nan")
+    x[3, 0:32] = float("nan")
+    x[4, 32:64] = float("inf")
+    q = B.quantize_mxfp8(x)
+    v, c = ref.quantize(_np(x))
+    assert np.array_equal(_np(q["scales"]), c)
+    assert np.array_equal(VAL[_np(q["codes"])], v, equal_nan=True)
+
+
+def test_dequantize_every_code_and_scale():
+    codes = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    scales = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 8).contiguous()
+    q = {"codes": codes.to(DEV), "scales": scales.to(DEV)}
+    with np.errstate(all="ignore"):
+        exact = ref.e4m3_values()[None] * np.ldexp(1.0, np.arange(256) - 127)[:, None]
+        exact[255] = np.nan
+        want = exact.astype(np.float32)
+    got = B.dequantize_mxfp8(q).cpu().numpy()
+    assert np.array_equal(got, want, equal_nan=True)
+    half = B.dequantize_mxfp8(q, torch.bfloat16).float().cpu().numpy()
+    assert np.array_equal(half, torch.from_numpy(want).to(torch.bfloat16).float().numpy(), equal_nan=True)
+
+
+NORM = [(1, 32), (1, 4096), (7, 96), (600, 160), (511, 4096), (2053, 288), (5, 2080), (3, 16384), (2, 32768),
+        (530, 8192), (515, 20000)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("shape", NORM)
+def test_rmsnorm(shape, residual, dtype):
+    rows, cols = shape
+    x = _rand(rows, cols, dtype, rows + cols)
+    res = _rand(rows, cols, dtype, rows + cols + 1) if residual else None
+    gain = (torch.randn(cols, generator=torch.Generator().manual_seed(5)) * 0.2 + 1).to(DEV)
+    print("rmsnorm", shape, residual, dtype, flush=True)
+    o = B.rmsnorm_mxfp8(x, gain, residual=res, eps=1e-5, with_y=True)
+    s, r, y = ref.rmsnorm(_np(x), _np(gain), None if res is None else _np(res), 1e-5)
+    assert np.all(np.abs(_np(o["rstd"]) - r) <= 32 * U * r)
+    half = 2.0 ** -8 if dtype == "bf16" else U          # unit roundoff of the stored type (8 and 24 bits)
+    assert np.all(np.abs(_np(o["sum"]) - s) <= 1.01 * half * np.abs(s) + 1e-45)
+    assert np.all(np.abs(_np(o["y"]) - y) <= (1.01 * half + 40 * U) * np.abs(y) + 1e-45)
+    _check_codes(o, y, 40 * U)
+    if res is not None:                                  # in place over the residual: the same bits
+        again = B.rmsnorm_mxfp8(x, gain, residual=res, eps=1e-5, in_place=True)
+        assert again["sum"] is res and torch.equal(res, o["sum"])
+        assert torch.equal(again["codes"], o["codes"]) and torch.equal(again["scales"], o["scales"])
+
+
+def test_rmsnorm_special_rows():
+    x = torch.randn(5, 512, device=DEV)
+    x[0] = 0.0                          # r = 1/sqrt(eps), codes zero
+    x[1, 7] = float("nan")              # the whole row
+    x[2, 9] = float("inf")              # r = 0
+    x[3] = 1e30                         # the sum of squares overflows: r = 0
+    gain = torch.ones(512, device=DEV)
+    o = B.rmsnorm_mxfp8(x, gain, with_y=True)
+    v = VAL[_np(o["codes"])]
+    assert np.all(v[0] == 0) and abs(float(o["rstd"][0]) - 1e3) < 1e-3
+    assert np.all(np.isnan(v[1])) and torch.isnan(o["y"][1]).all()
+    assert float(o["rstd"][2]) == 0 and np.isnan(v[2, 9]) and np.all(np.delete(v[2], 9) == 0)
+    assert float(o["rstd"][3]) == 0 and np.all(v[3] == 0)
+    alone = B.rmsnorm_mxfp8(x[4:].contiguous(), gain)
+    assert torch.equal(alone["codes"], o["codes"][4:])      # a row does not depend on its neighbours
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("up", [False, True])
+@pytest.mark.parametrize("shape", [(1, 32), (1, 4096), (7, 96), (77, 1056), (600, 160), (2053, 288), (3, 16384),
+                                   (2, 32768), (1100, 4096), (515, 20000)])
+def test_rmsnorm_backward(shape, up, dtype):
+    rows, cols = shape
+    s, dy = _rand(rows, cols, dtype, rows), _rand(rows, cols, dtype, rows + 1, gain=0.1)
+    du = _rand(rows, cols, dtype, rows + 2, gain=0.1) if up else None
+    gain = (torch.randn(cols, generator=torch.Generator().manual_seed(6)) * 0.2 + 1).to(DEV)
+    rstd = (1.0 / torch.sqrt(s.float().square().mean(-1) + 1e-5)).contiguous()
+    print("rmsnorm backward", shape, up, dtype, flush=True)
+    dx, dg = B.rmsnorm_backward(dy, s, gain, rstd, dsum=du)
+    wx, wg, mx, mg = ref.rmsnorm_backward(_np(dy), _np(s), _np(gain), _np(rstd), None if du is None else _np(du))
+    half = 2.0 ** -8 if dtype == "bf16" else U
+    assert np.all(np.abs(_np(dx) - wx) <= 1.01 * half * np.abs(wx) + 64 * U * mx + 1e-45)
+    # a workgroup adds up to ceil(rows / 512) rows one after another, then at most 32 + 5 partial sums
+    assert np.all(np.abs(_np(dg) - wg) <= (rows / 512 + 42) * U * mg + 1e-45)
+    again = B.rmsnorm_backward(dy, s, gain, rstd, dsum=du)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dg)
+
+
+def test_rmsnorm_backward_against_differences():
+    """Along random directions: the gradient's slope against central differences of the binary64 norm."""
+    rng = np.random.default_rng(0)
+    x, gain, w = rng.standard_normal((5, 96)), rng.standard_normal(96), rng.standard_normal((5, 96))
+    x32, g32, w32 = (torch.from_numpy(v.astype(np.float32)).to(DEV) for v in (x, gain, w))
+    x, gain, w = _np(x32), _np(g32), _np(w32)
+    o = B.rmsnorm_mxfp8(x32, g32, eps=1e-5)
+    dx, dg = B.rmsnorm_backward(w32, o["sum"], g32, o["rstd"])
+    loss = lambda x, g: float((ref.rmsnorm(x, g, eps=1e-5)[2] * w).sum())
+    h = 1e-5
+    for _ in range(8):
+        v, u = rng.standard_normal(x.shape), rng.standard_normal(gain.shape)
+        slope = (loss(x + h * v, gain) - loss(x - h * v, gain)) / (2 * h)
+        size = np.abs(_np(dx) * v).sum()
+        assert abs(slope - (_np(dx) * v).sum()) <= 1e-5 * size     # 64 u and h^2 are far below
+        slope = (loss(x, gain + h * u) - loss(x, gain - h * u)) / (2 * h)
+        assert abs(slope - (_np(dg) * u).sum()) <= 1e-5 * np.abs(_np(dg) * u).sum()
+
+
+def test_backward_in_place_and_another_stream():
+    s, dy, du = (_rand(300, 1056, "bf16", k, gain=0.1) for k in range(3))
+    gain = torch.ones(1056, device=DEV)
+    rstd = (1.0 / torch.sqrt(s.float().square().mean(-1) + 1e-6)).contiguous()
+    dx, dg = B.rmsnorm_backward(dy, s, gain, rstd, dsum=du)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = B.rmsnorm_backward(dy, s, gain, rstd, dsum=du, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0], dx) and torch.equal(got[1], dg)
+    need = B.fp4q_rmsnorm_backward_scratch(300, 1056)
+    for target in (dy, du):
+        keep, a = target.clone(), torch.empty(1056, device=DEV)
+        scratch = torch.empty(need, dtype=torch.uint8, device=DEV)
+        B.fp4q_rmsnorm_backward(dy, s, du, B.BF16, 300, 1056, gain, rstd, target, a, scratch, need)
+        assert torch.equal(target, dx) and torch.equal(a, dg)
+        target.copy_(keep)
+
+
+def test_norm_and_quantizer_in_a_graph():
+    x, res = _rand(70, 2080, "bf16", 1), _rand(70, 2080, "bf16", 2)
+    gain = torch.ones(2080, device=DEV)
+    B.rmsnorm_mxfp8(x, gain, residual=res)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = B.rmsnorm_mxfp8(x, gain, residual=res)
+        q = B.quantize_mxfp8(x)
+        dx, dg = B.rmsnorm_backward(x, o["sum"], gain, o["rstd"], dsum=res)
+    for k in range(4):
+        x.copy_(_rand(70, 2080, "bf16", 10 + k))
+        g.replay()
+        torch.cuda.synchronize()
+        e = B.rmsnorm_mxfp8(x, gain, residual=res)
+        ex, eg = B.rmsnorm_backward(x, e["sum"], gain, e["rstd"], dsum=res)
+        torch.cuda.synchronize()
+        for a, b in ((o["codes"], e["codes"]), (o["scales"], e["scales"]), (o["sum"], e["sum"]),
+                     (q["codes"], B.quantize_mxfp8(x)["codes"]), (dx, ex), (dg, eg)):
+            assert torch.equal(a, b)
