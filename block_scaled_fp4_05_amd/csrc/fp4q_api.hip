@@ -437,6 +437,21 @@ fp4q_status fp4q_rmsnorm_backward(const void* dy, const void* s, const void* dsu
   return after_launch();
 }
 
+fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                                  const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, fp4q_dtype out_dt,
+                                  void* c, hipStream_t stream) {
+  if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return FP4Q_E_NULL;
+  if (!valid_dtype(out_dt)) return FP4Q_E_ARG;
+  const int64_t lim = (int64_t)1 << 31;
+  if (m <= 0 || n <= 0 || k < 128 || k % 128 != 0 || m >= lim || n >= lim || k > ((int64_t)1 << 25))
+    return FP4Q_E_SHAPE;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(c))
+    return FP4Q_E_ALIGN;
+  if (!fp4q::launch_gemm_mxfp8_mxfp4(a_codes, a_scales, b_codes, b_scales, m, n, k, out_dt == FP4Q_BF16, c, stream))
+    return FP4Q_E_SHAPE;
+  return after_launch();
+}
+
 // ---------------------------------------------------------------------------------------
 // Allocation-free NVFP4 entry point.  Its workspace is this file-scope device array (one
 // copy per GPU, alive until the process ends), found once per device by

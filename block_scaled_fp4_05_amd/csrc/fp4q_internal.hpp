@@ -133,4 +133,10 @@ void launch_rmsnorm_backward(const void* dy, const void* s, const void* dsum, in
                              const float* gain, const float* rstd, void* dx, float* dgain, void* scratch,
                              hipStream_t st);
 
+// MXFP8 x MXFP4 product -- fp4q_gemm8.hip.  k % 128 == 0.  False (nothing enqueued) where the
+// grid would be too large.
+bool launch_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
+                             const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, bool bf16_out, void* c,
+                             hipStream_t st);
+
 }  // namespace fp4q

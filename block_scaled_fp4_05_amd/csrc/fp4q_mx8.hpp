@@ -1,0 +1,58 @@
+// fp4q_mx8.hpp -- device pieces shared by the products of MXFP8 activations and MXFP4
+// weights (fp4q_gemm8.hip, fp4q_moe.hip).
+//
+// v_mfma_scale_f32_{16x16x128,32x32x64}_f8f6f4 takes one operand in E4M3 and the other in
+// E2M1.  Lane layout (checked with an in-bounds probe, both operand orders), for R = 16 or 32
+// rows per operand, lane l holding row l % R of its operand and q = l / R:
+//  - E2M1: 16 bytes, K elements 32 q .. 32 q + 31;
+//  - E4M3: 32 bytes, the first 16 at K = 16 q .., the last 16 at K = (instruction's K) / 2 + 16 q ..;
+//  - the scale byte of lane l is that of K block q (32 elements) of its row, for both.
+// The E4M3 products of one small group are aligned to the group's largest and cut about 13
+// bits below it, groups are joined in fp32: on Gaussian operands a result is about 5e-6
+// (2-norm) from the exact one, against 2.6e-2 for rounding an operand to E4M3.
+#pragma once
+#include "fp4q_internal.hpp"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp4q {
+
+typedef int v8i_m __attribute__((ext_vector_type(8)));
+typedef float v4f_m __attribute__((ext_vector_type(4)));
+typedef float v16f_m __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_m __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_m __attribute__((ext_vector_type(2)));
+typedef float f32x2_m __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_m __attribute__((ext_vector_type(2)));
+
+// Operand registers of the builtin: 16 bytes of E2M1 (the upper half is not read), or two
+// 16-byte pieces of E4M3.
+__device__ __forceinline__ v8i_m frag4(u32x4_m w) {
+  return v8i_m{(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
+}
+__device__ __forceinline__ v8i_m frag8(u32x4_m lo, u32x4_m hi) {
+  return v8i_m{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+}
+
+// acc[row of w][row of x] += w (16 rows, E2M1) x^T (16 rows, E4M3) over 128 K elements; sw / sx
+// hold the lane's scale byte in byte 0.  Register r of lane l is row 4 (l / 16) + r, column l % 16.
+__device__ __forceinline__ v4f_m mma_w4x8(v8i_m w, v8i_m x, v4f_m acc, uint32_t sw, uint32_t sx) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, acc, 4, 0, 0, (int)sw, 0, (int)sx);
+}
+
+// acc += x (32 rows, E4M3) w^T (32 rows, E2M1) over 64 K elements; the lane's scale byte is byte 0
+// (_lo) or byte 2 (_hi) of its word.  Register t is row 8 (t / 4) + 4 (l / 32) + t % 4, column l % 32.
+__device__ __forceinline__ v16f_m mma_x8w4_lo(v8i_m x, v8i_m w, v16f_m acc, uint32_t sx, uint32_t sw) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, w, acc, 0, 4, 0, (int)sx, 0, (int)sw);
+}
+__device__ __forceinline__ v16f_m mma_x8w4_hi(v8i_m x, v8i_m w, v16f_m acc, uint32_t sx, uint32_t sw) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, w, acc, 0, 4, 2, (int)sx, 2, (int)sw);
+}
+
+// Two fp32 values to packed bf16, nearest even (v_cvt_pk_bf16_f32; NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_m{a, b}), bf16x2_m));
+}
+
+}  // namespace fp4q

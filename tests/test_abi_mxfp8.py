@@ -80,3 +80,15 @@ def test_helpers_refuse_what_the_library_cannot_see():
         with pytest.raises(err):
             B._need("t", bad, torch.float32, (8, 64), dev)
     B._need("t", x, torch.float32, (8, 64), dev)
+
+
+GEMM = dict(ac=A, asc=A, bc=A, bsc=A, m=4, n=8, k=256, dt=B.F32, c=A, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(ac=None), 1), (dict(asc=None), 1), (dict(bc=None), 1), (dict(bsc=None), 1), (dict(c=None), 1),
+    (dict(dt=2), 4), (dict(m=0), 2), (dict(n=-1), 2), (dict(k=0), 2), (dict(k=192), 2), (dict(k=(1 << 25) + 128), 2),
+    (dict(m=1 << 31), 2), (dict(n=1 << 31), 2), (dict(m=(1 << 31) - 1, n=(1 << 31) - 1), 2), (dict(ac=MIS), 3),
+    (dict(asc=MIS), 3), (dict(bc=MIS), 3), (dict(bsc=MIS), 3), (dict(c=MIS), 3)])
+def test_gemm(kw, status):
+    assert _with("fp4q_gemm_mxfp8_mxfp4", GEMM)(**kw) == status
