@@ -31,7 +31,8 @@ EXPORTS = ["fp4q_workspace_create", "fp4q_workspace_destroy", "fp4q_workspace_se
            "fp4q_quantize_if4", "fp4q_quantize_variant", "fp4q_dequantize_variant", "fp4q_rht", "fp4q_gemm_mxfp4", "fp4q_gemm_nvfp4", "fp4q_dequantize", "fp4q_amax",
            "fp4q_rht_signs_from_seed", "fp4q_status_string", "fp4q_abi_version",
            "fp4q_quantize_mxfp8", "fp4q_dequantize_mxfp8", "fp4q_rmsnorm_mxfp8", "fp4q_rmsnorm_backward",
-           "fp4q_rmsnorm_backward_scratch", "fp4q_gemm_mxfp8_mxfp4"]
+           "fp4q_rmsnorm_backward_scratch", "fp4q_gemm_mxfp8_mxfp4", "fp4q_moe_mxfp4",
+           "fp4q_moe_scratch"]
 
 
 class Fp4qError(RuntimeError):
@@ -80,6 +81,9 @@ def lib() -> ctypes.CDLL:
             "fp4q_rmsnorm_backward": [_P, _P, _P, _I, _I64, _I64, _P, _P, _P, _P, _P, _I64, _P],
             "fp4q_rmsnorm_backward_scratch": [_I64, _I64],
             "fp4q_gemm_mxfp8_mxfp4": [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P],
+            "fp4q_moe_mxfp4": [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _U, _P, _P, _I, _P,
+                               _P, _I64, _P],
+            "fp4q_moe_scratch": [_I64, _I64, _I64, _I64],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -87,6 +91,7 @@ def lib() -> ctypes.CDLL:
             fn.restype = _I
         L.fp4q_rht_signs_from_seed.restype = None
         L.fp4q_rmsnorm_backward_scratch.restype = _I64
+        L.fp4q_moe_scratch.restype = _I64
         L.fp4q_status_string.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -294,6 +299,22 @@ def fp4q_rmsnorm_backward(dy, s, dsum, dt, rows, cols, gain, rstd, dx, dgain, sc
 def fp4q_gemm_mxfp8_mxfp4(a_codes, a_scales, b_codes, b_scales, m, n, k, out_dt, c, stream=None) -> int:
     return _check("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
         _p(a_codes), _p(a_scales), _p(b_codes), _p(b_scales), m, n, k, out_dt, _p(c), _s(stream)))
+
+
+ROUTE_COMPUTE, ROUTE_GIVEN = 0, 1
+
+
+def fp4q_moe_mxfp4(x_codes, x_scales, router_x, router_w, router_dt, w13_codes, w13_scales, w2_codes, w2_scales,
+                   tokens, d, hidden, experts, topk, route_mode, ids, weights, out_dt, y, scratch, scratch_bytes,
+                   stream=None) -> int:
+    return _check("fp4q_moe_mxfp4", lib().fp4q_moe_mxfp4(
+        _p(x_codes), _p(x_scales), _p(router_x), _p(router_w), router_dt, _p(w13_codes), _p(w13_scales),
+        _p(w2_codes), _p(w2_scales), tokens, d, hidden, experts, topk, route_mode, _p(ids), _p(weights), out_dt,
+        _p(y), _p(scratch), scratch_bytes, _s(stream)))
+
+
+def fp4q_moe_scratch(tokens: int, hidden: int, experts: int, topk: int) -> int:
+    return lib().fp4q_moe_scratch(tokens, hidden, experts, topk)
 
 
 # --- allocation helpers --------------------------------------------------------------
@@ -575,3 +596,45 @@ def gemm_mxfp8_mxfp4(a: dict, b: dict, out_dtype=torch.float32, stream=None) -> 
     c = torch.empty(m, n, dtype=out_dtype, device=dev)
     fp4q_gemm_mxfp8_mxfp4(ac, asc, bc, bsc, m, n, k, _dt(c), c, stream)
     return c
+
+
+def moe_mxfp4(x: dict, w13: dict, w2: dict, topk: int, router_x: torch.Tensor | None = None,
+              router_w: torch.Tensor | None = None, ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None, out_dtype=torch.bfloat16, stream=None) -> dict:
+    """A mixture-of-experts layer for up to 64 tokens.
+
+    x: MXFP8 tokens (rmsnorm_mxfp8); w13, w2: MXFP4 experts, codes [experts][2 hidden][d/2] and
+    [experts][d][hidden/2] with their scales [..][/32].  Either `router_x` [tokens][d] and
+    `router_w` [experts][d] (bfloat16 or float32): the layer routes; or `ids` (int32) and
+    `weights` (float32) [tokens][topk], as another router chose them.  Returns y, ids, weights."""
+    xc, xsc, w13c, w13s, w2c, w2s = x["codes"], x["scales"], w13["codes"], w13["scales"], w2["codes"], w2["scales"]
+    _matrix("x", xc)
+    if not isinstance(w2c, torch.Tensor) or w2c.dim() != 3:
+        raise ValueError("w2 codes: a tensor [experts][d][hidden/2] is needed")
+    (tokens, d), experts, hidden, dev = xc.shape, w2c.shape[0], w2c.shape[2] * 2, xc.device
+    _on_current(xc)
+    _need("x codes", xc, torch.uint8, (tokens, d), dev)
+    _need("x scales", xsc, torch.uint8, (tokens, d // 32), dev)
+    _need("w13 codes", w13c, torch.uint8, (experts, 2 * hidden, d // 2), dev)
+    _need("w13 scales", w13s, torch.uint8, (experts, 2 * hidden, d // 32), dev)
+    _need("w2 codes", w2c, torch.uint8, (experts, d, hidden // 2), dev)
+    _need("w2 scales", w2s, torch.uint8, (experts, d, hidden // 32), dev)
+    if (router_x is None) != (router_w is None) or (ids is None) != (weights is None) or \
+            (router_x is None) == (ids is None):
+        raise ValueError("either router_x and router_w or ids and weights are needed")
+    if router_x is not None:
+        mode, rdt = ROUTE_COMPUTE, _dt(router_x)
+        _need("router_x", router_x, router_x.dtype, (tokens, d), dev)
+        _need("router_w", router_w, router_x.dtype, (experts, d), dev)
+        ids = torch.empty(tokens, topk, dtype=torch.int32, device=dev)
+        weights = torch.empty(tokens, topk, dtype=torch.float32, device=dev)
+    else:
+        mode, rdt = ROUTE_GIVEN, F32
+        _need("ids", ids, torch.int32, (tokens, topk), dev)
+        _need("weights", weights, torch.float32, (tokens, topk), dev)
+    y = torch.empty(tokens, d, dtype=out_dtype, device=dev)
+    need = fp4q_moe_scratch(tokens, hidden, experts, topk)
+    scratch = _scratch(need, dev, stream)
+    fp4q_moe_mxfp4(xc, xsc, router_x, router_w, rdt, w13c, w13s, w2c, w2s, tokens, d, hidden, experts, topk, mode,
+                   ids, weights, _dt(y), y, scratch, need, stream)
+    return {"y": y, "ids": ids, "weights": weights}

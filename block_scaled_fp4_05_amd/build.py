@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp4q.so")
 SOURCES = ["fp4q_api.hip", "fp4q_quant.hip", "fp4q_rht.hip", "fp4q_gemm.hip", "fp4q_variant.hip", "fp4q_mxfp8.hip",
-           "fp4q_gemm8.hip"]
+           "fp4q_gemm8.hip", "fp4q_moe.hip"]
 
 ARCH = "gfx950"
 CXXFLAGS = [

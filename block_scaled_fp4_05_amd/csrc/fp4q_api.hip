@@ -33,6 +33,12 @@ bool mx_shape(int64_t rows, int64_t cols) {
          rows <= ((int64_t)1 << 36) / cols;
 }
 
+bool moe_shape(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
+  return tokens >= 1 && tokens <= FP4Q_MOE_MAX_TOKENS && d >= 128 && d % 128 == 0 && d <= 65536 && hidden >= 128 &&
+         hidden % 128 == 0 && hidden <= 65536 && experts >= 1 && experts <= FP4Q_MOE_MAX_EXPERTS && topk >= 1 &&
+         topk <= FP4Q_MOE_MAX_TOPK && topk <= experts;
+}
+
 // Sink of a two-pass call's amax pass and the matching source for its quantizer: the
 // workspace's two-pass state when there is one, else the caller's float (which the
 // amax pass zeroes first).
@@ -449,6 +455,36 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scale
     return FP4Q_E_ALIGN;
   if (!fp4q::launch_gemm_mxfp8_mxfp4(a_codes, a_scales, b_codes, b_scales, m, n, k, out_dt == FP4Q_BF16, c, stream))
     return FP4Q_E_SHAPE;
+  return after_launch();
+}
+
+int64_t fp4q_moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk) {
+  return moe_shape(tokens, 128, hidden, experts, topk) ? fp4q::moe_scratch(tokens, hidden, experts, topk) : 0;
+}
+
+fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, const void* router_x,
+                           const void* router_w, fp4q_dtype router_dt, const uint8_t* w13_codes,
+                           const uint8_t* w13_scales, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                           int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk,
+                           unsigned route_mode, int32_t* ids, float* weights, fp4q_dtype out_dt, void* y,
+                           void* scratch, int64_t scratch_bytes, hipStream_t stream) {
+  const bool route = route_mode == FP4Q_ROUTE_COMPUTE;
+  if (!x_codes || !x_scales || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !ids || !weights || !y ||
+      !scratch || (route && (!router_x || !router_w)))
+    return FP4Q_E_NULL;
+  if (!valid_dtype(out_dt) || (!route && route_mode != FP4Q_ROUTE_GIVEN) || (route && !valid_dtype(router_dt)))
+    return FP4Q_E_ARG;
+  if (!moe_shape(tokens, d, hidden, experts, topk)) return FP4Q_E_SHAPE;
+  if (scratch_bytes < fp4q::moe_scratch(tokens, hidden, experts, topk)) return FP4Q_E_ARG;
+  if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w13_codes) || !aligned16(w13_scales) ||
+      !aligned16(w2_codes) || !aligned16(w2_scales) || !aligned4(ids) || !aligned4(weights) || !aligned16(y) ||
+      !aligned16(scratch) || (route && (!aligned16(router_x) || !aligned16(router_w))))
+    return FP4Q_E_ALIGN;
+  fp4q::launch_moe(fp4q::MoeArgs{x_codes, x_scales, route ? router_x : nullptr, route ? router_w : nullptr,
+                                 router_dt == FP4Q_BF16, w13_codes, w13_scales, w2_codes, w2_scales, (int)tokens,
+                                 (int)d, (int)hidden, (int)experts, (int)topk, ids, weights, out_dt == FP4Q_BF16, y,
+                                 scratch},
+                   stream);
   return after_launch();
 }
 

@@ -139,4 +139,20 @@ bool launch_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, co
                              const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, bool bf16_out, void* c,
                              hipStream_t st);
 
+// Mixture-of-experts layer -- fp4q_moe.hip.  router_w NULL: ids and weights are given.
+struct MoeArgs {
+  const uint8_t *x_codes, *x_scales;
+  const void *router_x, *router_w;
+  bool router_bf16;
+  const uint8_t *w13_codes, *w13_scales, *w2_codes, *w2_scales;
+  int tokens, d, hidden, experts, topk;
+  int32_t* ids;
+  float* weights;
+  bool bf16_out;
+  void* y;
+  void* scratch;
+};
+int64_t moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk);
+void launch_moe(const MoeArgs& a, hipStream_t st);
+
 }  // namespace fp4q

@@ -447,6 +447,48 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scale
                                   const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, fp4q_dtype out_dt,
                                   void* c, hipStream_t stream);
 
+/*
+ * A mixture-of-experts layer for a few tokens (a decode step) over MXFP4 expert weights, bound by
+ * reading each used expert's weights once.  Per token t with MXFP8 activation x_t:
+ *   route   l = router_x[t] . router_w[e]; the topk largest logits (ties to the lower expert), in
+ *           falling order, and their softmax as weights
+ *   expert  g, u = x_t W13[e]^T (rows 0 .. hidden-1 of W13[e] are the gate, the next hidden the up
+ *           projection);  h = MXFP8(g / (1 + exp(-g)) * u);  o_e = h W2[e]^T
+ *   y_t     = sum_j weights[t][j] o_{ids[t][j]}
+ * Products as in fp4q_gemm_mxfp8_mxfp4, sums in fp32 in a fixed order; h is rounded to MXFP8 so
+ * that the down product too runs on 8-bit times 4-bit operands.
+ *   x_codes, x_scales      MXFP8 [tokens][d]  (fp4q_rmsnorm_mxfp8)
+ *   router_x               [tokens][d] of router_dt (e.g. that norm's y), router_w [experts][d]
+ *                          of router_dt; read only with FP4Q_ROUTE_COMPUTE
+ *   w13_codes, w13_scales  MXFP4 [experts][2 hidden][d]: codes [..][d/2], scales [..][d/32]
+ *   w2_codes, w2_scales    MXFP4 [experts][d][hidden]
+ *   route_mode  FP4Q_ROUTE_COMPUTE: the call routes and writes ids and weights.
+ *               FP4Q_ROUTE_GIVEN: ids and weights are read.  An id outside 0 .. experts-1 is a
+ *               choice that takes no part (an expert held elsewhere, a dropped token); a token
+ *               without any gets y = 0.  An expert that a token names twice gets both weights.
+ *   ids      device int32 [tokens][topk];  weights  device float [tokens][topk]
+ *   y        [tokens][d]: float, or bf16 (RNE of the fp32 sum)
+ *   scratch  device memory of at least fp4q_moe_scratch(tokens, hidden, experts, topk) bytes,
+ *            16-byte aligned; its contents before and after the call mean nothing.
+ * A NaN logit ranks above every number, so it is chosen and makes its token's weights NaN; so does
+ * a chosen +infinity.
+ * Shapes: 1 <= tokens <= 64; d, hidden multiples of 128 up to 65536; 1 <= experts <= 512;
+ * 1 <= topk <= min(16, experts).  Tensors 16-byte aligned, ids and weights 4.
+ */
+#define FP4Q_ROUTE_COMPUTE 0u
+#define FP4Q_ROUTE_GIVEN 1u
+#define FP4Q_MOE_MAX_TOKENS 64
+#define FP4Q_MOE_MAX_EXPERTS 512
+#define FP4Q_MOE_MAX_TOPK 16
+fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, const void* router_x,
+                           const void* router_w, fp4q_dtype router_dt, const uint8_t* w13_codes,
+                           const uint8_t* w13_scales, const uint8_t* w2_codes, const uint8_t* w2_scales,
+                           int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk,
+                           unsigned route_mode, int32_t* ids, float* weights, fp4q_dtype out_dt, void* y,
+                           void* scratch, int64_t scratch_bytes, hipStream_t stream);
+/* Bytes of scratch for that call (0 for a shape it refuses).  Host only. */
+int64_t fp4q_moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk);
+
 /* max |x| over the whole matrix, written to device float *amax. */
 fp4q_status fp4q_amax(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, float* amax,
                       hipStream_t stream);

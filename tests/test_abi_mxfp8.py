@@ -92,3 +92,27 @@ GEMM = dict(ac=A, asc=A, bc=A, bsc=A, m=4, n=8, k=256, dt=B.F32, c=A, stream=0)
     (dict(asc=MIS), 3), (dict(bc=MIS), 3), (dict(bsc=MIS), 3), (dict(c=MIS), 3)])
 def test_gemm(kw, status):
     assert _with("fp4q_gemm_mxfp8_mxfp4", GEMM)(**kw) == status
+
+
+MOE = dict(xc=A, xs=A, rx=A, rw=A, rdt=B.BF16, w13c=A, w13s=A, w2c=A, w2s=A, tokens=4, d=256, hidden=128, experts=8, topk=2,
+           mode=B.ROUTE_COMPUTE, ids=A, weights=A, dt=B.BF16, y=A, scratch=A, scratch_bytes=1 << 30, stream=0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(xc=None), 1), (dict(xs=None), 1), (dict(rx=None), 1), (dict(rw=None), 1), (dict(w13c=None), 1),
+    (dict(w13s=None), 1), (dict(w2c=None), 1), (dict(w2s=None), 1), (dict(ids=None), 1), (dict(weights=None), 1),
+    (dict(y=None), 1), (dict(scratch=None), 1), (dict(rdt=3), 4), (dict(dt=2), 4), (dict(mode=2), 4),
+    (dict(tokens=0), 2), (dict(tokens=65), 2), (dict(d=192), 2), (dict(d=0), 2), (dict(d=65664), 2),
+    (dict(hidden=64), 2), (dict(hidden=65664), 2), (dict(experts=0), 2), (dict(experts=513), 2), (dict(topk=0), 2),
+    (dict(topk=9), 2), (dict(experts=64, topk=17), 2),
+    (dict(scratch_bytes=B.fp4q_moe_scratch(4, 128, 8, 2) - 1), 4), (dict(xc=MIS), 3), (dict(rx=MIS), 3),
+    (dict(w13c=MIS), 3), (dict(w2s=MIS), 3), (dict(ids=A + 2), 3), (dict(weights=A + 1), 3), (dict(y=MIS), 3),
+    (dict(scratch=MIS), 3),
+    (dict(mode=B.ROUTE_GIVEN, rx=None, rw=None, y=None), 1), (dict(mode=B.ROUTE_GIVEN, rx=None, rw=None, xs=MIS), 3)])
+def test_moe(kw, status):
+    assert _with("fp4q_moe_mxfp4", MOE)(**kw) == status
+
+
+def test_moe_scratch():
+    assert B.fp4q_moe_scratch(65, 128, 8, 2) == 0 and B.fp4q_moe_scratch(4, 100, 8, 2) == 0
+    assert B.fp4q_moe_scratch(64, 65536, 512, 16) >= 64 * 16 * 65536
