@@ -83,7 +83,7 @@ def lib() -> ctypes.CDLL:
             "fp4q_gemm_mxfp8_mxfp4": [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P],
             "fp4q_moe_mxfp4": [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _U, _P, _P, _I, _P,
                                _P, _I64, _P],
-            "fp4q_moe_scratch": [_I64, _I64, _I64, _I64],
+            "fp4q_moe_scratch": [_I64, _I64, _I64, _I64, _I64],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -313,8 +313,8 @@ def fp4q_moe_mxfp4(x_codes, x_scales, router_x, router_w, router_dt, w13_codes, 
         _p(y), _p(scratch), scratch_bytes, _s(stream)))
 
 
-def fp4q_moe_scratch(tokens: int, hidden: int, experts: int, topk: int) -> int:
-    return lib().fp4q_moe_scratch(tokens, hidden, experts, topk)
+def fp4q_moe_scratch(tokens: int, d: int, hidden: int, experts: int, topk: int) -> int:
+    return lib().fp4q_moe_scratch(tokens, d, hidden, experts, topk)
 
 
 # --- allocation helpers --------------------------------------------------------------
@@ -475,67 +475,79 @@ def dequantize_variant(var: int, codes, scales, tensor_scale, rows: int, cols: i
 # --- MXFP8 activations -------------------------------------------------------------------
 #
 # These helpers check what the C entry points cannot see (the tensors' types, shapes, devices
-# and strides) before any address is passed on.
+# and strides) before any address is passed on.  A decode step makes several such calls in a few
+# microseconds each, so they call the library directly and each check has a short way through.
 
 _NAMES = {torch.float32: F32, torch.bfloat16: BF16}
+_U8, _F32 = torch.uint8, torch.float32
 
 
-def _need(name: str, t, dtype, shape, device) -> None:
-    """`t` is a dense tensor of this type (one of them), shape and device."""
+def _need(name: str, t, dtype, shape, device: int) -> int:
+    """The address of `t`, a dense tensor of this type, shape and device (index, -1: the CPU)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == device \
+            and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: a tensor is needed, got {type(t).__name__}")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+    if t.dtype != dtype:
         raise TypeError(f"{name}: {dtype} is needed, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} is needed, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: is on {t.device}, the call's other tensors on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: a dense row-major tensor is needed (call .contiguous())")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: is on {t.device}, the call's other tensors on device {device}")
+    raise ValueError(f"{name}: a dense row-major tensor is needed (call .contiguous())")
 
 
-def _on_current(t: torch.Tensor) -> None:
-    """Kernels are launched on the current device: the tensors have to be there."""
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors on {t.device}, but device {torch.cuda.current_device()} is current "
-                         "(use torch.cuda.device)")
-
-
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Device memory for one call on `stream`; the allocator does not hand it out again before
-    the stream has passed the call, also when that is not the current stream."""
-    t = _u8(nbytes, device=device)
-    if stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return t
-
-
-def _rows_of(name: str, x) -> tuple[int, int, int, torch.device]:
-    """(fp4q dtype, rows, cols, device) of a dense 2-D bf16 or fp32 device tensor."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _NAMES:
-        raise TypeError(f"{name}: a bfloat16 or float32 tensor is needed")
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+def _matrix(name: str, t, dtypes) -> tuple[int, int, int]:
+    """(rows, cols, device index) of a dense 2-D tensor of one of `dtypes` on the current device."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name}: a tensor of {' or '.join(str(d) for d in dtypes)} is needed")
+    if t.dim() != 2 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: a dense row-major [rows][cols] tensor on the GPU is needed")
-    _on_current(x)
-    return _NAMES[x.dtype], x.shape[0], x.shape[1], x.device
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():   # kernels are launched on the current device
+        raise ValueError(f"{name}: is on {t.device}, but device {torch.cuda.current_device()} is current "
+                         "(use torch.cuda.device)")
+    rows, cols = t.shape
+    return rows, cols, dev
+
+
+def _at(stream, dev: int, *made) -> int:
+    """The stream's handle.  Memory `made` for a call on a stream that is not the current one is
+    not handed out again by the allocator before that stream has passed the call."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    for t in made:
+        if t is not None:
+            t.record_stream(s)
+    return s.cuda_stream
+
+
+def _done(fn: str, status: int) -> None:
+    if status:
+        raise Fp4qError(fn, status)
 
 
 def quantize_mxfp8(x: torch.Tensor, stream=None) -> dict:
     """MXFP8: codes [rows][cols] (E4M3), E8M0 scales [rows][cols/32]."""
-    dt, rows, cols, dev = _rows_of("x", x)
-    out = {"codes": _u8(rows, cols, device=dev), "scales": _u8(rows, cols // 32, device=dev)}
-    fp4q_quantize_mxfp8(x, dt, rows, cols, out["codes"], out["scales"], stream)
-    return out
+    rows, cols, dev = _matrix("x", x, _NAMES)
+    codes = torch.empty_like(x, dtype=_U8)
+    scales = codes.new_empty(rows, cols // 32)
+    _done("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
+        x.data_ptr(), _NAMES[x.dtype], rows, cols, codes.data_ptr(), scales.data_ptr(),
+        _at(stream, dev, codes, scales)))
+    return {"codes": codes, "scales": scales}
 
 
 def dequantize_mxfp8(q: dict, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """The values of MXFP8 codes and scales as quantize_mxfp8 returns them."""
-    codes, scales = q["codes"], q["scales"]
-    rows, cols = codes.shape
-    _need("codes", codes, torch.uint8, (rows, cols), codes.device)
-    _need("scales", scales, torch.uint8, (rows, cols // 32), codes.device)
-    y = torch.empty(rows, cols, dtype=out_dtype, device=codes.device)
-    fp4q_dequantize_mxfp8(codes, scales, rows, cols, _dt(y), y, stream)
+    codes = q["codes"]
+    rows, cols, dev = _matrix("codes", codes, (_U8,))
+    scales = _need("scales", q["scales"], _U8, (rows, cols // 32), dev)
+    y = torch.empty_like(codes, dtype=out_dtype)
+    _done("fp4q_dequantize_mxfp8", lib().fp4q_dequantize_mxfp8(
+        codes.data_ptr(), scales, rows, cols, _dt(y), y.data_ptr(), _at(stream, dev, y)))
     return y
 
 
@@ -545,17 +557,21 @@ def rmsnorm_mxfp8(x: torch.Tensor, gain: torch.Tensor, residual: torch.Tensor | 
 
     Returns codes, scales, rstd, sum (x + residual in x's type; x itself without a residual)
     and, with ``with_y``, the unquantized y.  ``in_place`` writes the sum over `residual`."""
-    dt, rows, cols, dev = _rows_of("x", x)
-    _need("gain", gain, torch.float32, (cols,), dev)
-    if residual is not None:
-        _need("residual", residual, x.dtype, x.shape, dev)
-    out = {"codes": _u8(rows, cols, device=dev), "scales": _u8(rows, cols // 32, device=dev),
-           "rstd": torch.empty(rows, dtype=torch.float32, device=dev)}
-    out["sum"] = x if residual is None else residual if in_place else torch.empty_like(x)
+    rows, cols, dev = _matrix("x", x, _NAMES)
+    gp = _need("gain", gain, _F32, (cols,), dev)
+    rp = None if residual is None else _need("residual", residual, x.dtype, x.shape, dev)
+    codes = torch.empty_like(x, dtype=_U8)
+    scales = codes.new_empty(rows, cols // 32)
+    rstd = gain.new_empty(rows)
+    total = x if residual is None else residual if in_place else torch.empty_like(x)
+    y = torch.empty_like(x) if with_y else None
+    _done("fp4q_rmsnorm_mxfp8", lib().fp4q_rmsnorm_mxfp8(
+        x.data_ptr(), rp, _NAMES[x.dtype], rows, cols, gp, eps, codes.data_ptr(), scales.data_ptr(),
+        None if rp is None else total.data_ptr(), rstd.data_ptr(), None if y is None else y.data_ptr(),
+        _at(stream, dev, codes, scales, rstd, total, y)))
+    out = {"codes": codes, "scales": scales, "rstd": rstd, "sum": total}
     if with_y:
-        out["y"] = torch.empty_like(x)
-    fp4q_rmsnorm_mxfp8(x, residual, dt, rows, cols, gain, eps, out["codes"], out["scales"],
-                       None if residual is None else out["sum"], out["rstd"], out.get("y"), stream)
+        out["y"] = y
     return out
 
 
@@ -563,38 +579,32 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gain: torch.Tensor, rstd
                      dsum: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """(dx, dgain) of rmsnorm_mxfp8 from its `sum` and `rstd`; `dsum` is the gradient that reaches
     the sum from elsewhere, added to dx."""
-    dt, rows, cols, dev = _rows_of("dy", dy)
-    _need("s", s, dy.dtype, dy.shape, dev)
-    _need("gain", gain, torch.float32, (cols,), dev)
-    _need("rstd", rstd, torch.float32, (rows,), dev)
-    if dsum is not None:
-        _need("dsum", dsum, dy.dtype, dy.shape, dev)
-    dx, dgain = torch.empty_like(dy), torch.empty(cols, dtype=torch.float32, device=dev)
-    need = fp4q_rmsnorm_backward_scratch(rows, cols)
-    scratch = _scratch(need, dev, stream)
-    fp4q_rmsnorm_backward(dy, s, dsum, dt, rows, cols, gain, rstd, dx, dgain, scratch, need, stream)
+    rows, cols, dev = _matrix("dy", dy, _NAMES)
+    sp = _need("s", s, dy.dtype, dy.shape, dev)
+    gp = _need("gain", gain, _F32, (cols,), dev)
+    rp = _need("rstd", rstd, _F32, (rows,), dev)
+    up = None if dsum is None else _need("dsum", dsum, dy.dtype, dy.shape, dev)
+    dx, dgain = torch.empty_like(dy), torch.empty_like(gain)
+    need = lib().fp4q_rmsnorm_backward_scratch(rows, cols)
+    scratch = gain.new_empty(need // 4)
+    _done("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
+        dy.data_ptr(), sp, up, _NAMES[dy.dtype], rows, cols, gp, rp, dx.data_ptr(), dgain.data_ptr(),
+        scratch.data_ptr(), need, _at(stream, dev, dx, dgain, scratch)))
     return dx, dgain
-
-
-def _matrix(name: str, codes) -> None:
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 2 or not codes.is_cuda:
-        raise ValueError(f"{name}: a 2-D tensor of codes on the GPU is needed")
 
 
 def gemm_mxfp8_mxfp4(a: dict, b: dict, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """C = A B^T for an MXFP8 operand (quantize_mxfp8, rmsnorm_mxfp8) and a row-wise MXFP4 one
     (quantize_mxfp4); k (a multiple of 128) is the columns of both."""
-    ac, asc, bc, bsc = a["codes"], a["scales"], b["codes"], b["scales"]
-    _matrix("a", ac)
-    _matrix("b", bc)
-    (m, k), n, dev = ac.shape, bc.shape[0], ac.device
-    _on_current(ac)
-    _need("a codes", ac, torch.uint8, (m, k), dev)
-    _need("a scales", asc, torch.uint8, (m, k // 32), dev)
-    _need("b codes", bc, torch.uint8, (n, k // 2), dev)
-    _need("b scales", bsc, torch.uint8, (n, k // 32), dev)
-    c = torch.empty(m, n, dtype=out_dtype, device=dev)
-    fp4q_gemm_mxfp8_mxfp4(ac, asc, bc, bsc, m, n, k, _dt(c), c, stream)
+    ac, bc = a["codes"], b["codes"]
+    m, k, dev = _matrix("a codes", ac, (_U8,))
+    n = bc.shape[0] if isinstance(bc, torch.Tensor) and bc.dim() == 2 else 0
+    asp = _need("a scales", a["scales"], _U8, (m, k // 32), dev)
+    bcp = _need("b codes", bc, _U8, (n, k // 2), dev)
+    bsp = _need("b scales", b["scales"], _U8, (n, k // 32), dev)
+    c = torch.empty(m, n, dtype=out_dtype, device=ac.device)
+    _done("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
+        ac.data_ptr(), asp, bcp, bsp, m, n, k, _dt(c), c.data_ptr(), _at(stream, dev, c)))
     return c
 
 
@@ -607,34 +617,34 @@ def moe_mxfp4(x: dict, w13: dict, w2: dict, topk: int, router_x: torch.Tensor | 
     [experts][d][hidden/2] with their scales [..][/32].  Either `router_x` [tokens][d] and
     `router_w` [experts][d] (bfloat16 or float32): the layer routes; or `ids` (int32) and
     `weights` (float32) [tokens][topk], as another router chose them.  Returns y, ids, weights."""
-    xc, xsc, w13c, w13s, w2c, w2s = x["codes"], x["scales"], w13["codes"], w13["scales"], w2["codes"], w2["scales"]
-    _matrix("x", xc)
+    xc, w2c = x["codes"], w2["codes"]
+    tokens, d, dev = _matrix("x codes", xc, (_U8,))
     if not isinstance(w2c, torch.Tensor) or w2c.dim() != 3:
         raise ValueError("w2 codes: a tensor [experts][d][hidden/2] is needed")
-    (tokens, d), experts, hidden, dev = xc.shape, w2c.shape[0], w2c.shape[2] * 2, xc.device
-    _on_current(xc)
-    _need("x codes", xc, torch.uint8, (tokens, d), dev)
-    _need("x scales", xsc, torch.uint8, (tokens, d // 32), dev)
-    _need("w13 codes", w13c, torch.uint8, (experts, 2 * hidden, d // 2), dev)
-    _need("w13 scales", w13s, torch.uint8, (experts, 2 * hidden, d // 32), dev)
-    _need("w2 codes", w2c, torch.uint8, (experts, d, hidden // 2), dev)
-    _need("w2 scales", w2s, torch.uint8, (experts, d, hidden // 32), dev)
+    experts, hidden = w2c.shape[0], w2c.shape[2] * 2
+    xsp = _need("x scales", x["scales"], _U8, (tokens, d // 32), dev)
+    w13p = _need("w13 codes", w13["codes"], _U8, (experts, 2 * hidden, d // 2), dev)
+    w13sp = _need("w13 scales", w13["scales"], _U8, (experts, 2 * hidden, d // 32), dev)
+    w2p = _need("w2 codes", w2c, _U8, (experts, d, hidden // 2), dev)
+    w2sp = _need("w2 scales", w2["scales"], _U8, (experts, d, hidden // 32), dev)
     if (router_x is None) != (router_w is None) or (ids is None) != (weights is None) or \
             (router_x is None) == (ids is None):
         raise ValueError("either router_x and router_w or ids and weights are needed")
+    where = xc.device
+    rxp = rwp = None
+    mode, rdt = ROUTE_GIVEN, F32
     if router_x is not None:
         mode, rdt = ROUTE_COMPUTE, _dt(router_x)
-        _need("router_x", router_x, router_x.dtype, (tokens, d), dev)
-        _need("router_w", router_w, router_x.dtype, (experts, d), dev)
-        ids = torch.empty(tokens, topk, dtype=torch.int32, device=dev)
-        weights = torch.empty(tokens, topk, dtype=torch.float32, device=dev)
-    else:
-        mode, rdt = ROUTE_GIVEN, F32
-        _need("ids", ids, torch.int32, (tokens, topk), dev)
-        _need("weights", weights, torch.float32, (tokens, topk), dev)
-    y = torch.empty(tokens, d, dtype=out_dtype, device=dev)
-    need = fp4q_moe_scratch(tokens, hidden, experts, topk)
-    scratch = _scratch(need, dev, stream)
-    fp4q_moe_mxfp4(xc, xsc, router_x, router_w, rdt, w13c, w13s, w2c, w2s, tokens, d, hidden, experts, topk, mode,
-                   ids, weights, _dt(y), y, scratch, need, stream)
+        rxp = _need("router_x", router_x, router_x.dtype, (tokens, d), dev)
+        rwp = _need("router_w", router_w, router_x.dtype, (experts, d), dev)
+        ids = torch.empty(tokens, topk, dtype=torch.int32, device=where)
+        weights = torch.empty(tokens, topk, dtype=_F32, device=where)
+    ip = _need("ids", ids, torch.int32, (tokens, topk), dev)
+    wp = _need("weights", weights, _F32, (tokens, topk), dev)
+    y = torch.empty(tokens, d, dtype=out_dtype, device=where)
+    need = lib().fp4q_moe_scratch(tokens, d, hidden, experts, topk)
+    scratch = xc.new_empty(need)
+    _done("fp4q_moe_mxfp4", lib().fp4q_moe_mxfp4(
+        xc.data_ptr(), xsp, rxp, rwp, rdt, w13p, w13sp, w2p, w2sp, tokens, d, hidden, experts, topk, mode, ip, wp,
+        _dt(y), y.data_ptr(), scratch.data_ptr(), need, _at(stream, dev, y, ids, weights, scratch)))
     return {"y": y, "ids": ids, "weights": weights}

@@ -458,8 +458,8 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scale
   return after_launch();
 }
 
-int64_t fp4q_moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk) {
-  return moe_shape(tokens, 128, hidden, experts, topk) ? fp4q::moe_scratch(tokens, hidden, experts, topk) : 0;
+int64_t fp4q_moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
+  return moe_shape(tokens, d, hidden, experts, topk) ? fp4q::moe_scratch(tokens, d, hidden, experts, topk) : 0;
 }
 
 fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, const void* router_x,
@@ -475,7 +475,7 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
   if (!valid_dtype(out_dt) || (!route && route_mode != FP4Q_ROUTE_GIVEN) || (route && !valid_dtype(router_dt)))
     return FP4Q_E_ARG;
   if (!moe_shape(tokens, d, hidden, experts, topk)) return FP4Q_E_SHAPE;
-  if (scratch_bytes < fp4q::moe_scratch(tokens, hidden, experts, topk)) return FP4Q_E_ARG;
+  if (scratch_bytes < fp4q::moe_scratch(tokens, d, hidden, experts, topk)) return FP4Q_E_ARG;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w13_codes) || !aligned16(w13_scales) ||
       !aligned16(w2_codes) || !aligned16(w2_scales) || !aligned4(ids) || !aligned4(weights) || !aligned16(y) ||
       !aligned16(scratch) || (route && (!aligned16(router_x) || !aligned16(router_w))))

@@ -6,82 +6,101 @@
 // Two forms: few rows of A (k_gemm8_rows, bound by reading B once) and tiles in LDS
 // (k_gemm8_tile, bound by the matrix cores).
 #include "fp4q_mx8.hpp"
+#include <type_traits>
 
 namespace fp4q {
 namespace {
 
 // -----------------------------------------------------------------------------------------
-// Few rows.  A workgroup takes 16 rows of B and every row of A (G groups of 16); its waves
+// Few rows.  A workgroup takes 16 NT rows of B and every row of A (G groups of 16); its waves
 // split k into contiguous ranges and join their sums in LDS, in wave order.  B's codes go from
 // memory to the matrix core's registers without a stop, since no two waves want the same ones.
 // -----------------------------------------------------------------------------------------
-template <int G, int WAVES, bool BF16OUT>
+template <int G, int NT, int WAVES, bool BF16OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_gemm8_rows(const uint8_t* __restrict__ ac,
                                                            const uint8_t* __restrict__ as,
                                                            const uint8_t* __restrict__ bc,
                                                            const uint8_t* __restrict__ bs, int M, int N, int K,
                                                            void* __restrict__ cout) {
-  __shared__ v4f_m sums[WAVES][G][64];
+  __shared__ v4f_m sums[WAVES][NT * G][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16;
+  const int n0 = blockIdx.x * (16 * NT);
   const int nk = K / 128;
   const int first = (int)((int64_t)nk * wave / WAVES), last = (int)((int64_t)nk * (wave + 1) / WAVES);
   // rows past an operand's end read its last row; their results are not stored
-  const int64_t brow = min(n0 + r, N - 1);
-  const uint8_t* bcp = bc + brow * (K / 2) + 16 * q;
-  const uint8_t* bsp = bs + brow * (K / 32);
+  const uint8_t* bcp[NT];
+  const uint8_t* bsp[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int64_t row = min(n0 + 16 * t + r, N - 1);
+    bcp[t] = bc + row * (K / 2) + 16 * q;
+    bsp[t] = bs + row * (K / 32);
+  }
   const uint8_t* acp[G];
   const uint8_t* asp[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t arow = min(16 * g + r, M - 1);
-    acp[g] = ac + arow * K + 16 * q;
-    asp[g] = as + arow * (K / 32);
+    const int64_t row = min(16 * g + r, M - 1);
+    acp[g] = ac + row * K + 16 * q;
+    asp[g] = as + row * (K / 32);
   }
-  v4f_m acc[G];
+  v4f_m acc[NT][G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) acc[g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = 4;   // steps whose loads are in flight together
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int g = 0; g < G; ++g) acc[t][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
+  // Four steps at a time, their B codes in flight together and a row's four scale words in one
+  // load: a load of one word per row costs the address unit as much as one of 16 bytes per lane.
+  constexpr int U = 4;
   int s = first;
   for (; s + U <= last; s += U) {
-    u32x4_m b[U];
-    uint32_t sb[U];
+    u32x4_m b[NT][U];
+    u32x4_w sb[NT], sa[G];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      b[u] = *reinterpret_cast<const u32x4_m*>(bcp + (int64_t)(s + u) * 64);
-      sb[u] = *reinterpret_cast<const uint32_t*>(bsp + (s + u) * 4);
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) b[t][u] = *reinterpret_cast<const u32x4_m*>(bcp[t] + (int64_t)(s + u) * 64);
+      sb[t] = *reinterpret_cast<const u32x4_w*>(bsp[t] + s * 4);
     }
+#pragma unroll
+    for (int g = 0; g < G; ++g) sa[g] = *reinterpret_cast<const u32x4_w*>(asp[g] + s * 4);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const uint8_t* p = acp[g] + (int64_t)(s + u) * 128;
         const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
-        const uint32_t sa = *reinterpret_cast<const uint32_t*>(asp[g] + (s + u) * 4);
-        acc[g] = mma_w4x8(frag4(b[u]), frag8(lo, hi), acc[g], sb[u] >> (8 * q), sa >> (8 * q));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[t][g] = mma_w4x8(frag4(b[t][u]), frag8(lo, hi), acc[t][g], sb[t][u] >> (8 * q), sa[g][u] >> (8 * q));
       }
   }
   for (; s < last; ++s) {
-    const u32x4_m b = *reinterpret_cast<const u32x4_m*>(bcp + (int64_t)s * 64);
-    const uint32_t sb = *reinterpret_cast<const uint32_t*>(bsp + s * 4);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint8_t* p = acp[g] + (int64_t)s * 128;
       const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
       const uint32_t sa = *reinterpret_cast<const uint32_t*>(asp[g] + s * 4);
-      acc[g] = mma_w4x8(frag4(b), frag8(lo, hi), acc[g], sb >> (8 * q), sa >> (8 * q));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const u32x4_m b = *reinterpret_cast<const u32x4_m*>(bcp[t] + (int64_t)s * 64);
+        const uint32_t sb = *reinterpret_cast<const uint32_t*>(bsp[t] + s * 4);
+        acc[t][g] = mma_w4x8(frag4(b), frag8(lo, hi), acc[t][g], sb >> (8 * q), sa >> (8 * q));
+      }
     }
   }
 #pragma unroll
-  for (int g = 0; g < G; ++g) sums[wave][g][lane] = acc[g];
-  __syncthreads();
-  for (int t = threadIdx.x; t < G * 64; t += 64 * WAVES) {
-    const int g = t >> 6, l = t & 63;
-    v4f_m v = sums[0][g][l];
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) v += sums[w][g][l];
-    const int row = 16 * g + (l & 15), col = n0 + 4 * (l >> 4);
+    for (int g = 0; g < G; ++g) sums[wave][t * G + g][lane] = acc[t][g];
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * G * 64; i += 64 * WAVES) {
+    const int tg = i >> 6, l = i & 63;
+    v4f_m v = sums[0][tg][l];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += sums[w][tg][l];
+    const int row = 16 * (tg % G) + (l & 15), col = n0 + 16 * (tg / G) + 4 * (l >> 4);
     if (row >= M || col >= N) continue;
     const int64_t at = (int64_t)row * N + col;
     const bool whole = (N & 3) == 0;   // then col + 4 <= N and the address is a multiple of four elements
@@ -121,16 +140,18 @@ __device__ __forceinline__ uint32_t swz_a(uint32_t r) {
   return ((r >> 1) & 1u) | (((r >> 2) & 1u) << 1) | (((r ^ (r >> 3)) & 1u) << 2);
 }
 __device__ __forceinline__ uint32_t swz_b(uint32_t r) { return ((r >> 2) & 1u) | ((((r >> 1) ^ (r >> 3)) & 1u) << 1); }
-// Word d of a row's 16 scale bytes (four steps) sits at position d ^ swz_s(row).
-__device__ __forceinline__ uint32_t swz_s(uint32_t r) { return (r >> 3) & 3u; }
 
 // One wave's copy of 64 pieces of 16 (4) bytes into 64 consecutive ones of LDS.
 __device__ __forceinline__ void copy16(const void* from, void* lds) {
   __builtin_amdgcn_global_load_lds(from, lds, 16, 0, 0);
 }
+
 __device__ __forceinline__ void copy4(const void* from, void* lds) {
   __builtin_amdgcn_global_load_lds(from, lds, 4, 0, 0);
 }
+
+// Word d of a row's 16 scale bytes sits at position d ^ swz_s(row) where they are copied as words.
+__device__ __forceinline__ uint32_t swz_s(uint32_t r) { return (r >> 3) & 3u; }
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -155,45 +176,71 @@ __device__ __forceinline__ void tile_of(int b, int tiles_m, int tiles_n, int& tm
   tm = first + rem % gh;
 }
 
-template <int MI, int NJ, int S>
+template <int MI, int NJ, int S, bool WIDE>
 struct TileLds {
   static constexpr int BM = 64 * MI, BN = 64 * NJ;
   struct Stage {
     u32x4_m a[BM * 8];
     u32x4_m b[BN * 4];
   };
-  struct Scales {   // four steps: 16 bytes per row, A's rows, then B's
-    uint32_t w[(BM + BN) * 4];
-  };
+  // Scales come in chunks of four steps, one 16-byte piece per row (A's rows, then B's), in slices of
+  // 64 rows that travel with the codes of the four steps before, S steps ahead of use; a buffer is
+  // written again once its chunk has been read: 2 + (S - 1) / 4 of them, rounded up.  Where k / 32 is
+  // a multiple of 16 (WIDE) a slice is one wave's copy of 16 bytes per row.  Else a row starts at a
+  // multiple of four bytes only, and it is four waves' copies of words; an instruction of either
+  // kind costs about the same (8192^3: 387 us with pieces, 445 with words).  Loading unaligned pieces
+  // into registers and writing them on took longer than the words (256 x 4096 x 4224: 15.3 against
+  // 11.2 us), since the compiler waits for every copy in flight before the write.
+  static constexpr int kBuffers = 2 + (S + 2) / 4;
   struct Loop {
     Stage st[S];
-    Scales sc[3];
+    u32x4_m sc[kBuffers][BM + BN];
   };
   union {
     Loop loop;
     uint16_t out[4][32 * MI * 32 * NJ];   // each wave's block of C on its way out, bf16
   };
-  // loads per wave and step: codes, and the next scale chunk's slices of 64 rows dealt over its
-  // four steps (a chunk of only two slices is loaded twice)
-  static constexpr int kSlices = (MI + NJ) >= 4 ? (MI + NJ) / 4 : 1;
-  static constexpr int kLoads = 2 * MI + NJ + kSlices;
+  static constexpr int kSlices = (MI + NJ + 3) / 4;                            // words: slices per step
+  static constexpr int kLoads = 2 * MI + NJ + (WIDE ? 0 : kSlices);            // at least so many copies per wave and step
 };
+
+template <int P>
+using Phase = std::integral_constant<int, P>;
+
+// The first S steps' copies.
+template <int S, int I = 0, typename Issue>
+__device__ __forceinline__ void issue_first(Issue& issue) {
+  if constexpr (I < S) {
+    issue(I, Phase<(I & 3)>{});
+    issue_first<S, I + 1>(issue);
+  }
+}
 
 template <int MI, int NJ>
 struct Frags {
   v8i_m a[MI], b[NJ];
 };
 
-template <int MI, int NJ, int S, bool BF16OUT>
+// Scheduling groups: one MFMA, then up to V copies and D LDS reads, N times.
+template <int N, int V, int D>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int g = 0; g < N; ++g) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (V > 0) __builtin_amdgcn_sched_group_barrier(0x020, V, 0);
+    if constexpr (D > 0) __builtin_amdgcn_sched_group_barrier(0x100, D, 0);
+  }
+}
+
+template <int MI, int NJ, int S, bool WIDE, bool BF16OUT>
 __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ ac, const uint8_t* __restrict__ as,
                                                     const uint8_t* __restrict__ bc, const uint8_t* __restrict__ bs,
                                                     int M, int N, int K, int tiles_m, int tiles_n,
                                                     void* __restrict__ cout) {
-  using Lds = TileLds<MI, NJ, S>;
-  static_assert((MI + NJ) % 4 == 0 || (MI == 1 && NJ == 1), "scale slices per step");
+  using Lds = TileLds<MI, NJ, S, WIDE>;
   __shared__ Lds lds_;
   auto* st = lds_.loop.st;
-  auto* sc = lds_.loop.sc;
+  auto& sc = lds_.loop.sc;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int tm, tn;
@@ -214,18 +261,24 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
 #pragma unroll
   for (int j = 0; j < NJ; ++j)
     ob[j] = (uint32_t)((min(n0 + 64 * j + rb, N - 1) - min(n0 + 64 * j, N - 1)) * (int)ldb);
-  // Scale slice i of a chunk: 64 rows of A (i < MI) or of B; this lane fetches row 16 wave +
-  // lane / 4 of it, word 4 chunk + ((lane % 4) ^ swz_s(row)), clamped to the row's last.
-  const int srow = 16 * wave + (lane >> 2);
-  const int sword = (lane & 3) ^ (int)swz_s((uint32_t)srow);
+  // Slice i of a chunk is 64 rows of A (i < MI) or of B.  WIDE: lane l copies row l's 16 bytes.
+  // Words: wave w copies rows 16 w .., lane l word l % 4 of row l / 4 of those, to word
+  // (l % 4) ^ swz_s(row) of the row's piece.  Clamped to the row's last piece or word.
+  const int srow = WIDE ? lane : 16 * wave + (lane >> 2);
+  const int sword = WIDE ? 0 : (lane & 3) ^ (int)swz_s((uint32_t)srow);
   auto issue_scales = [&](int chunk, int i) {
     const bool of_a = i < MI;   // uniform selects: a branch here would cut the step into pieces
     const uint8_t* from = of_a ? as : bs;
     const int row = (of_a ? m0 + 64 * i : n0 + 64 * (i - MI)) + srow, end = of_a ? M : N;
-    copy4(from + (int64_t)min(row, end - 1) * lds + 4 * min(4 * chunk + sword, nk - 1),
-          &sc[chunk % 3].w[(64 * i + 16 * wave) * 4]);
+    const uint8_t* at = from + (int64_t)min(row, end - 1) * lds;
+    uint32_t* to = reinterpret_cast<uint32_t*>(&sc[chunk % Lds::kBuffers][64 * i + (WIDE ? 0 : 16 * wave)]);
+    if constexpr (WIDE) copy16(at + 16 * min(chunk, nk / 4 - 1), to);
+    else copy4(at + 4 * min(4 * chunk + sword, nk - 1), to);
   };
-  auto issue = [&](int ks) {
+  // Copies of step ks; PHASE = ks % 4 where the loop knows it (the copies of pieces need no branch
+  // then, which would make the compiler move the accumulators about), else -1.
+  auto issue = [&](int ks, auto phase) {
+    constexpr int PHASE = decltype(phase)::value;
     auto& s = st[ks % S];
     const int kc = min(ks, nk - 1);
 #pragma unroll
@@ -236,19 +289,20 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
     for (int j = 0; j < NJ; ++j)
       copy16(bc + (int64_t)min(n0 + 64 * j, N - 1) * ldb + (ob[j] + (uint32_t)(kc * 64 + cb * 16)),
              &s.b[j * 256 + wave * 64]);
-    const int chunk = (ks >> 2) + 1, part = ks & 3;
-    if constexpr (MI + NJ >= 4) {
+    const int chunk = (ks >> 2) + 1;   // (the last slice again where there is room for more)
+    if constexpr (!WIDE) {
 #pragma unroll
-      for (int i = 0; i < Lds::kSlices; ++i) issue_scales(chunk, part * Lds::kSlices + i);
-    } else {
-      issue_scales(chunk, part & 1);
+      for (int i = 0; i < Lds::kSlices; ++i) issue_scales(chunk, min((ks & 3) * Lds::kSlices + i, MI + NJ - 1));
+    } else if constexpr (4 * PHASE < MI + NJ) {
+      issue_scales(chunk, min(4 * PHASE + wave, MI + NJ - 1));
     }
   };
 
   // Fragment addresses: row (wave's first + 32 i + fr); sub-step u (64 K elements) takes A's
   // chunks 4 u + fh and 4 u + 2 + fh and B's chunk 2 u + fh.
   const int wm = wave & 1, wn = wave >> 1, fr = lane & 31, fh = lane >> 5;
-  const uint32_t za = swz_a((uint32_t)fr), zb = swz_b((uint32_t)fr), zs = swz_s((uint32_t)fr);
+  const uint32_t za = swz_a((uint32_t)fr), zb = swz_b((uint32_t)fr);
+  const uint32_t zs = WIDE ? 0u : swz_s((uint32_t)fr);
   const int rowA = wm * 32 * MI + fr, rowB = wn * 32 * NJ + fr;
   auto read = [&](int ks, int u, Frags<MI, NJ>& f) {
     const auto& s = st[ks % S];
@@ -262,12 +316,11 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
   };
   // Scale words of a step, shifted so that byte 2 u is the lane's block of sub-step u.
   auto read_scales = [&](int ks, uint32_t* wa, uint32_t* wb) {
-    const auto& c = sc[(ks >> 2) % 3];
-    const uint32_t d = (uint32_t)(ks & 3) ^ zs;
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(sc[(ks >> 2) % Lds::kBuffers]) + ((uint32_t)(ks & 3) ^ zs);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) wa[i] = c.w[(rowA + 32 * i) * 4 + d] >> (8 * fh);
+    for (int i = 0; i < MI; ++i) wa[i] = c[(rowA + 32 * i) * 4] >> (8 * fh);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) wb[j] = c.w[(Lds::BM + rowB + 32 * j) * 4 + d] >> (8 * fh);
+    for (int j = 0; j < NJ; ++j) wb[j] = c[(Lds::BM + rowB + 32 * j) * 4] >> (8 * fh);
   };
 
   v16f_m acc[MI][NJ];
@@ -276,44 +329,106 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = v16f_m{};
 
-  // While one sub-step's MFMAs run, the next one's fragments are read.  The barrier that
-  // publishes step ks + 1 sits between the two sub-steps of step ks, when all of step ks is in
-  // registers; its stage then takes step ks + S.  Step ks + 1 has landed once only the loads of
-  // the S - 2 steps after it are outstanding.
+  // Step ks + 1 has landed once only the copies of the S - 2 steps after it are outstanding; the
+  // barrier then publishes it, and the stage of step ks, all of it in registers by then, takes
+  // step ks + S.
+  if constexpr (WIDE) {
 #pragma unroll
-  for (int i = 0; i < MI + NJ; ++i) issue_scales(0, i);
+    for (int i = 0; i < MI + NJ; i += 4) issue_scales(0, min(i + wave, MI + NJ - 1));
+  } else {
 #pragma unroll
-  for (int s = 0; s < S; ++s) issue(s);
+    for (int i = 0; i < MI + NJ; ++i) issue_scales(0, i);
+  }
+  issue_first<S>(issue);
   wait_loads<(S - 1) * Lds::kLoads>();
   tile_barrier();
-  Frags<MI, NJ> f0, f1;
-  uint32_t wa[MI], wb[NJ];
-  read(0, 0, f0);
-  read_scales(0, wa, wb);
-  for (int ks = 0; ks < nk; ++ks) {
-    read(ks, 1, f1);
+  if constexpr (MI * NJ < 16) {
+    // small tiles: a whole step's fragments are read while the one before is multiplied, so a step
+    // has one barrier and one LDS latency
+    struct Step {
+      Frags<MI, NJ> f0, f1;
+      uint32_t wa[MI], wb[NJ];
+    } even, odd;
+    const auto fetch = [&](int ks, Step& t) {
+      read(ks, 0, t.f0);
+      read(ks, 1, t.f1);
+      read_scales(ks, t.wa, t.wb);
+    };
+    const auto turn = [&](int ks, auto phase, Step& t, Step& next) {
+      wait_loads<(S - 2) * Lds::kLoads>();
+      tile_barrier();
+      issue(ks + S, phase);
+      fetch(ks + 1, next);
+      __builtin_amdgcn_sched_barrier(0);   // the reads go out before the MFMAs that cover them
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        acc[i][j] = mma_x8w4_lo(f0.a[i], f0.b[j], acc[i][j], wa[i], wb[j]);
-    __builtin_amdgcn_sched_barrier(0);
-    uint32_t va[MI], vb[NJ];
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mma_x8w4_lo(t.f0.a[i], t.f0.b[j], acc[i][j], t.wa[i], t.wb[j]);
 #pragma unroll
-    for (int i = 0; i < MI; ++i) va[i] = wa[i];
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) vb[j] = wb[j];
-    wait_loads<(S - 2) * Lds::kLoads>();
-    tile_barrier();
-    issue(ks + S);
-    read_scales(ks + 1, wa, wb);
-    read(ks + 1, 0, f0);
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mma_x8w4_hi(t.f1.a[i], t.f1.b[j], acc[i][j], t.wa[i], t.wb[j]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    fetch(0, even);
+    if constexpr (WIDE) {   // nk is a multiple of four
+      for (int ks = 0; ks < nk; ks += 4) {
+        turn(ks, Phase<S & 3>{}, even, odd);
+        turn(ks + 1, Phase<(S + 1) & 3>{}, odd, even);
+        turn(ks + 2, Phase<(S + 2) & 3>{}, even, odd);
+        turn(ks + 3, Phase<(S + 3) & 3>{}, odd, even);
+      }
+    } else {
+      for (int ks = 0; ks < nk; ks += 2) {
+        turn(ks, Phase<-1>{}, even, odd);
+        if (ks + 1 < nk) turn(ks + 1, Phase<-1>{}, odd, even);
+      }
+    }
+  } else {
+    // large tiles have no registers for that: while one sub-step's MFMAs run, the next one's
+    // fragments are read, with the barrier between the two sub-steps of a step, and reads and
+    // copies are dealt one by one between the MFMAs
+    Frags<MI, NJ> f0, f1;
+    uint32_t wa[MI], wb[NJ];
+    read(0, 0, f0);
+    read_scales(0, wa, wb);
+    const auto turn = [&](int ks, auto phase) {
+      read(ks, 1, f1);
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        acc[i][j] = mma_x8w4_hi(f1.a[i], f1.b[j], acc[i][j], va[i], vb[j]);
-    __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mma_x8w4_lo(f0.a[i], f0.b[j], acc[i][j], wa[i], wb[j]);
+      interleave<12, 0, 1>();
+      interleave<4, 0, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      uint32_t va[MI], vb[NJ];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) va[i] = wa[i];
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) vb[j] = wb[j];
+      wait_loads<(S - 2) * Lds::kLoads>();
+      tile_barrier();
+      issue(ks + S, phase);
+      read_scales(ks + 1, wa, wb);
+      read(ks + 1, 0, f0);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = mma_x8w4_hi(f1.a[i], f1.b[j], acc[i][j], va[i], vb[j]);
+      interleave<12, 1, 2>();
+      interleave<4, 1, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (WIDE) {
+      for (int ks = 0; ks < nk; ks += 4) {
+        turn(ks, Phase<S & 3>{});
+        turn(ks + 1, Phase<(S + 1) & 3>{});
+        turn(ks + 2, Phase<(S + 2) & 3>{});
+        turn(ks + 3, Phase<(S + 3) & 3>{});
+      }
+    } else {
+      for (int ks = 0; ks < nk; ++ks) turn(ks, Phase<-1>{});
+    }
   }
   wait_loads<0>();   // the loads past k land before LDS is used again
 
@@ -367,6 +482,8 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
   }
 }
 
+constexpr int kCus = 256;   // compute units of the GPU
+
 struct Gemm8 {
   const uint8_t *ac, *as, *bc, *bs;
   int m, n, k;
@@ -378,30 +495,48 @@ template <int MI, int NJ, int S, bool BF16OUT>
 bool run_tile(const Gemm8& g) {
   const int64_t tm = (g.m + (int64_t)64 * MI - 1) / (64 * MI), tn = (g.n + (int64_t)64 * NJ - 1) / (64 * NJ);
   if (tm * tn > (1 << 24) - 1) return false;   // a launch has at most 2^32 threads
-  k_gemm8_tile<MI, NJ, S, BF16OUT><<<(unsigned)(tm * tn), 256, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k,
-                                                                          (int)tm, (int)tn, g.c);
+  auto kern = g.k % 512 == 0 ? k_gemm8_tile<MI, NJ, S, true, BF16OUT> : k_gemm8_tile<MI, NJ, S, false, BF16OUT>;
+  kern<<<(unsigned)(tm * tn), 256, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k, (int)tm, (int)tn, g.c);
   return true;
 }
 
-template <int G, bool BF16OUT>
+template <int G, int NT, int WAVES, bool BF16OUT>
 void run_rows(const Gemm8& g) {
-  const unsigned grid = (unsigned)((g.n + (int64_t)15) / 16);
-  k_gemm8_rows<G, 8, BF16OUT><<<grid, 512, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k, g.c);
+  const unsigned grid = (unsigned)((g.n + (int64_t)16 * NT - 1) / (16 * NT));
+  k_gemm8_rows<G, NT, WAVES, BF16OUT><<<grid, 64 * WAVES, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k, g.c);
 }
 
 template <bool BF16OUT>
 bool run(const Gemm8& g) {
-  if (g.m <= 64) {
-    if ((g.n + (int64_t)15) / 16 > (1 << 22)) return false;
-    if (g.m <= 16) run_rows<1, BF16OUT>(g);
-    else if (g.m <= 32) run_rows<2, BF16OUT>(g);
-    else run_rows<4, BF16OUT>(g);
+  if (g.m <= 32 && g.n <= 1 << 26) {   // (a launch has at most 2^32 threads)
+    // Rows of B per workgroup: 16, or more where that leaves a workgroup per CU and the longer
+    // stream per wave pays (us at 16 / 32 / 64: one row of A, n 4096, k 4096 3.6 / 5.4 / 7.6;
+    // n 32768, k 8192 33.7 / 31.4 / 27.9; 16 rows, n 8192, k 8192 14.8 / 12.0 / 15.4).
+    const bool two = g.n >= 32 * kCus, four = g.n >= 128 * kCus && g.m <= 16;
+    if (g.m <= 16) {
+      if (four) run_rows<1, 4, 8, BF16OUT>(g);
+      else if (two) run_rows<1, 2, 8, BF16OUT>(g);
+      else run_rows<1, 1, 8, BF16OUT>(g);
+    } else {
+      if (two) run_rows<2, 2, 8, BF16OUT>(g);
+      else run_rows<2, 1, 8, BF16OUT>(g);
+    }
     return true;
   }
-  const auto tiles = [&](int t) { return ((g.m + (int64_t)t - 1) / t) * ((g.n + (int64_t)t - 1) / t); };
-  if (tiles(256) >= 192) return run_tile<4, 4, 2, BF16OUT>(g);
-  if (tiles(128) >= 192) return run_tile<2, 2, 2, BF16OUT>(g);
-  return run_tile<1, 1, 4, BF16OUT>(g);
+  // The tile by what a round of one tile per CU takes, in units of a 64 x 64 tile's (measured at
+  // k = 4096, us for one round: 64 x 64 8.7, 64 x 128 12.0, 128 x 128 19.7 alone and 18.0 each in
+  // pairs, 256 x 256 41.7), times the rounds.
+  const auto cost = [&](int bm, int bn, float round) {
+    const int64_t t = ((g.m + (int64_t)bm - 1) / bm) * ((g.n + (int64_t)bn - 1) / bn);
+    return round * (float)((t + kCus - 1) / kCus);
+  };
+  const float c[4] = {cost(64, 64, 1.0f), cost(64, 128, 1.35f), cost(128, 128, 2.0f), cost(256, 256, 4.6f)};
+  const bool largest = c[3] <= c[0] && c[3] <= c[1] && c[3] <= c[2];
+  if (!largest && (c[2] <= c[0] && c[2] <= c[1] ? run_tile<2, 2, 2, BF16OUT>(g)
+                   : c[1] <= c[0]               ? run_tile<1, 2, 4, BF16OUT>(g)
+                                                : run_tile<1, 1, 4, BF16OUT>(g)))
+    return true;
+  return run_tile<4, 4, 2, BF16OUT>(g);   // also where the launch cannot hold the smaller tiles
 }
 
 }  // namespace

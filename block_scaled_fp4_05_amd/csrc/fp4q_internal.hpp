@@ -152,7 +152,7 @@ struct MoeArgs {
   void* y;
   void* scratch;
 };
-int64_t moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk);
+int64_t moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk);
 void launch_moe(const MoeArgs& a, hipStream_t st);
 
 }  // namespace fp4q

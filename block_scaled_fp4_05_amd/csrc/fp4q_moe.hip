@@ -15,6 +15,7 @@
 namespace fp4q {
 namespace {
 
+constexpr int kCus = 256;   // compute units of the GPU
 constexpr int kMaxTokens = 64;
 constexpr int kMaxPairs = kMaxTokens * 16;   // tokens x top-k
 
@@ -92,86 +93,122 @@ struct Moe {
   float* weights;               // [tokens][topk]; read, or written by k_moe_down when routing
   const float* logits;          // [tokens][experts], routing only
   uint8_t *hc, *hs;             // scratch: MXFP8 hidden rows [tokens * topk][hidden]
+  int splits;                   // workgroups per row tile of k_moe_down
+  float* partial;               // scratch: their sums [d / 16][splits][64][16]
+  int* arrived;                 // scratch: how many of a row tile's have finished; k_moe_up clears it
   void* y;
 };
 
-// The choice of expert `e` by each token as pair indices (token * topk + rank) in `list`, in
-// order; returns how many.  Whole workgroup; ends with a barrier.
+// Which pairs (token * topk + place) chose expert `e`, in order, in `list`; returns how many.  Whole
+// workgroup; ends with a barrier.
 //
 // With given ids: a token that names an expert twice counts once (its first place; k_moe_down
-// adds the weights up).  When routing: the rank of e among a token's logits is the number of
-// larger ones, ties to the lower index, so no sort is needed.
+// adds the weights up).  When routing: the place of e among a token's logits is the number of
+// larger ones, ties to the lower index, so no sort is needed; each wave takes eight tokens at a
+// time, whose logits are loaded together.
+struct RouteLds {
+  union {
+    int16_t id[kMaxPairs];
+    uint32_t key[512];
+    uint8_t place[kMaxTokens];
+  };
+  uint16_t list[kMaxTokens];
+  int count, found;
+};
+
 template <bool ROUTE>
-__device__ int pairs_of_expert(const Moe& a, int e, uint16_t* list, int* count, bool publish) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+__device__ int pairs_of_expert(const Moe& a, int e, RouteLds& r, bool publish) {
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint64_t below = (1ull << lane) - 1ull;
   if constexpr (!ROUTE) {
+    const int pairs = a.tokens * a.topk;
+    for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
+      const int v = a.ids[p];
+      r.id[p] = v >= 0 && v < a.experts ? (int16_t)v : (int16_t)-1;
+    }
+    __syncthreads();
     if (wave == 0) {
       int n = 0;
-      const int pairs = a.tokens * a.topk;
       for (int p0 = 0; p0 < pairs; p0 += 64) {
         const int p = p0 + lane;
-        bool hit = p < pairs && a.ids[p] == e;
+        bool hit = p < pairs && r.id[p] == e;
         if (hit)
-          for (int f = p - p % a.topk; f < p; ++f) hit = hit && a.ids[f] != e;
+          for (int f = p - p % a.topk; f < p; ++f) hit = hit && r.id[f] != e;
         const uint64_t m = __ballot(hit);
-        if (hit) list[n + __popcll(m & ((1ull << lane) - 1ull))] = (uint16_t)p;
+        if (hit) r.list[n + __popcll(m & below)] = (uint16_t)p;
         n += __popcll(m);
       }
-      if (lane == 0) *count = n;
+      if (lane == 0) r.count = n;
     }
   } else {
-    // bit t of `chosen`: token t's place for e, found by one wave per token
-    __shared__ uint8_t place[kMaxTokens];
-    for (int t = wave; t < a.tokens; t += waves) {
-      const float* l = a.logits + (int64_t)t * a.experts;
-      const uint32_t own = logit_key(l[e]);
-      int rank = 0;
-      for (int f0 = 0; f0 < a.experts; f0 += 64) {
-        const int f = f0 + lane;
-        const uint32_t k = f < a.experts ? logit_key(l[f]) : 0u;
-        rank += __popcll(__ballot(f < a.experts && (k > own || (k == own && f < e))));
+    constexpr int kBatch = 8;
+    for (int t0 = wave; t0 < a.tokens; t0 += kBatch * waves) {
+      uint32_t own[kBatch];
+      int place[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {   // past the last token: the last again, unused
+        own[i] = logit_key(a.logits[(int64_t)min(t0 + i * waves, a.tokens - 1) * a.experts + e]);
+        place[i] = 0;
       }
-      if (lane == 0) {
-        place[t] = (uint8_t)min(rank, 255);
-        if (publish && rank < a.topk) a.ids[t * a.topk + rank] = e;
+      for (int f0 = 0; f0 < a.experts; f0 += 64) {
+        const int f = min(f0 + lane, a.experts - 1);
+        uint32_t key[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          key[i] = logit_key(a.logits[(int64_t)min(t0 + i * waves, a.tokens - 1) * a.experts + f]);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          place[i] += __popcll(__ballot(f0 + lane < a.experts && (key[i] > own[i] || (key[i] == own[i] && f < e))));
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int t = t0 + i * waves;
+        if (lane == 0 && t < a.tokens) {
+          r.place[t] = (uint8_t)min(place[i], 255);
+          if (publish && place[i] < a.topk) a.ids[t * a.topk + place[i]] = e;
+        }
       }
     }
     __syncthreads();
     if (wave == 0) {
-      const int rank = lane < a.tokens ? place[lane] : 255;
-      const bool hit = rank < a.topk;
+      const int place = lane < a.tokens ? r.place[lane] : 255;
+      const bool hit = place < a.topk;
       const uint64_t m = __ballot(hit);
-      if (hit) list[__popcll(m & ((1ull << lane) - 1ull))] = (uint16_t)(lane * a.topk + rank);
-      if (lane == 0) *count = __popcll(m);
+      if (hit) r.list[__popcll(m & below)] = (uint16_t)(lane * a.topk + place);
+      if (lane == 0) r.count = __popcll(m);
     }
   }
   __syncthreads();
-  return __builtin_amdgcn_readfirstlane(*count);
+  return __builtin_amdgcn_readfirstlane(r.count);
 }
 
 // Workgroup column -> expert.  With at least as many choices as experts there is a column per
 // expert; with fewer there is one per choice, and the one that holds an expert's first choice
 // takes it (the caller compares).  -1: nothing to do.
 template <bool ROUTE>
-__device__ int expert_of_slot(const Moe& a, int slot, int* found) {
+__device__ int expert_of_slot(const Moe& a, int slot, RouteLds& r) {
   if (a.slots == a.experts) return slot;
   if constexpr (!ROUTE) {
     const int e = a.ids[slot];
     return e >= 0 && e < a.experts ? e : -1;
   } else {
     const int t = slot / a.topk, want = slot % a.topk;
-    const float* l = a.logits + (int64_t)t * a.experts;
+    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+      r.key[e] = logit_key(a.logits[(int64_t)t * a.experts + e]);
+    __syncthreads();
     for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-      const uint32_t own = logit_key(l[e]);
-      int rank = 0;
+      const uint32_t own = r.key[e];
+      int place = 0;
+#pragma unroll 8
       for (int f = 0; f < a.experts; ++f) {
-        const uint32_t k = logit_key(l[f]);
-        rank += k > own || (k == own && f < e);
+        const uint32_t k = r.key[f];
+        place += k > own || (k == own && f < e);
       }
-      if (rank == want) *found = e;   // ranks are distinct: exactly one thread
+      if (place == want) r.found = e;   // places are distinct: exactly one thread
     }
     __syncthreads();
-    return __builtin_amdgcn_readfirstlane(*found);
+    return __builtin_amdgcn_readfirstlane(r.found);
   }
 }
 
@@ -210,10 +247,10 @@ __device__ void up_tiles(const Moe& a, int e, int h0, const uint16_t* list, int 
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[i][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = 2;   // steps whose weights are in flight together; past the end the last one again, unused
+  constexpr int U = G == 1 ? 2 : 1;   // steps whose loads are in flight together; past the end the last again, unused
   for (int s = first; s < last; s += U) {
-    u32x4_m w[U][4];
-    uint32_t sw[U][4];
+    u32x4_m w[U][4], xl[U][G], xh[U][G];
+    uint32_t sw[U][4], sx[U][G];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int at = min(s + u, last - 1);
@@ -222,19 +259,22 @@ __device__ void up_tiles(const Moe& a, int e, int h0, const uint16_t* list, int 
         w[u][i] = *reinterpret_cast<const u32x4_m*>(wc[i] + at * 64);
         sw[u][i] = *reinterpret_cast<const uint32_t*>(ws[i] + at * 4);
       }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        xl[u][g] = *reinterpret_cast<const u32x4_m*>(xc[g] + at * 128);
+        xh[u][g] = *reinterpret_cast<const u32x4_m*>(xc[g] + at * 128 + 64);
+        sx[u][g] = *reinterpret_cast<const uint32_t*>(xs[g] + at * 4);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (s + u >= last) break;
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint8_t* p = xc[g] + (s + u) * 128;
-        const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
-        const uint32_t sx = *reinterpret_cast<const uint32_t*>(xs[g] + (s + u) * 4) >> (8 * q);
+      for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          acc[i][g] = mma_w4x8(frag4(w[u][i]), frag8(lo, hi), acc[i][g], sw[u][i] >> (8 * q), sx);
-      }
+          acc[i][g] = mma_w4x8(frag4(w[u][i]), frag8(xl[u][g], xh[u][g]), acc[i][g], sw[u][i] >> (8 * q),
+                               sx[u][g] >> (8 * q));
     }
   }
 #pragma unroll
@@ -269,53 +309,71 @@ __device__ void up_tiles(const Moe& a, int e, int h0, const uint16_t* list, int 
   }
 }
 
-// Grid: hidden / 32 tiles x slots.  GMAX: groups of 16 tokens an expert can have.
-template <int GMAX, bool ROUTE>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(Moe a) {
+// Grid: hidden / 32 tiles x slots.  G: groups of 16 tokens per pass over the expert's weights.
+template <int G, bool ROUTE>
+__global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_up(Moe a) {
   __shared__ UpSums sums;
-  __shared__ uint16_t list[kMaxTokens];
-  __shared__ int count, found;
-  const int e = expert_of_slot<ROUTE>(a, blockIdx.y, &found);
+  __shared__ RouteLds r;
+  // the arrival counts of the launch that follows; any workgroups do, before the first can leave
+  for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < a.d / 16;
+       i += gridDim.x * gridDim.y * blockDim.x)
+    a.arrived[i] = 0;
+  const int e = expert_of_slot<ROUTE>(a, blockIdx.y, r);
   if (e < 0) return;
-  const int n = pairs_of_expert<ROUTE>(a, e, list, &count, blockIdx.x == 0);
-  if (n == 0 || (a.slots != a.experts && list[0] != blockIdx.y)) return;
+  int n;
+  if (ROUTE && a.tokens == 1 && a.slots != a.experts) {   // one token: its choice is the whole list
+    if (threadIdx.x == 0) {
+      r.list[0] = (uint16_t)blockIdx.y;
+      if (blockIdx.x == 0) a.ids[blockIdx.y] = e;
+    }
+    __syncthreads();
+    n = 1;
+  } else {
+    n = pairs_of_expert<ROUTE>(a, e, r, blockIdx.x == 0);
+  }
+  if (n == 0 || (a.slots != a.experts && r.list[0] != blockIdx.y)) return;
   const int h0 = blockIdx.x * 32;
-  if (GMAX == 1 || n <= 16) up_tiles<1>(a, e, h0, list, n, sums);
-  else if (GMAX == 2 || n <= 32) up_tiles<2>(a, e, h0, list, n, sums);
-  else up_tiles<GMAX < 4 ? 1 : 4>(a, e, h0, list, n, sums);
+  for (int i = 0; i < n; i += 16 * G) up_tiles<G>(a, e, h0, r.list + i, min(n - i, 16 * G), sums);
 }
 
 constexpr int kDownWaves = 16;
 constexpr int kDownSteps = 4;   // most K steps of a unit of work
 
-// One expert's down product for 16 output rows over K steps [s0, s1), at most kDownSteps, added with the pairs'
-// weights to this wave's own sums (out[token][16]).
-template <int G>
-__device__ void down_tile(const Moe& a, int e, int n0, int s0, int s1, const uint16_t* list, int n, const float* wts,
-                          float (*out)[16]) {
+// Weights of one unit of work: up to kDownSteps K steps of one expert's 16 output rows.
+struct DownUnit {
+  u32x4_m w[kDownSteps];
+  uint32_t sw[kDownSteps];
+};
+__device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, int s1, DownUnit& d) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int64_t row = (int64_t)e * a.d + n0 + r, cols = a.hidden / 2, scols = a.hidden / 32;
-  const uint8_t* wc = a.w2c + row * cols + 16 * q;
-  const uint8_t* ws = a.w2s + row * scols;
+  const int64_t row = (int64_t)e * a.d + n0 + r;
+  const uint8_t* wc = a.w2c + row * (a.hidden / 2) + 16 * q;
+  const uint8_t* ws = a.w2s + row * (a.hidden / 32);
+#pragma unroll
+  for (int u = 0; u < kDownSteps; ++u) {   // past the unit's end the last step again, unused
+    const int at = min(s0 + u, s1 - 1);
+    d.w[u] = *reinterpret_cast<const u32x4_m*>(wc + at * 64);
+    d.sw[u] = *reinterpret_cast<const uint32_t*>(ws + at * 4);
+  }
+}
+
+// The unit's product with its expert's hidden rows, added with the pairs' weights to this wave's
+// own sums (out[token][16]).
+template <int G>
+__device__ __forceinline__ void down_unit(const Moe& a, const DownUnit& d, int s0, int s1, const uint16_t* list, int n,
+                                          const float* wts, float (*out)[16]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const uint8_t* hc[G];
   const uint8_t* hs[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int64_t p = list[min(16 * g + r, n - 1)];
     hc[g] = a.hc + p * a.hidden + 16 * q;
-    hs[g] = a.hs + p * scols;
+    hs[g] = a.hs + p * (a.hidden / 32);
   }
   v4f_m acc[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc[g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4_m w[kDownSteps];   // all of the unit's weights in flight; past its end the last step again, unused
-  uint32_t sw[kDownSteps];
-#pragma unroll
-  for (int u = 0; u < kDownSteps; ++u) {
-    const int at = min(s0 + u, s1 - 1);
-    w[u] = *reinterpret_cast<const u32x4_m*>(wc + at * 64);
-    sw[u] = *reinterpret_cast<const uint32_t*>(ws + at * 4);
-  }
 #pragma unroll
   for (int u = 0; u < kDownSteps; ++u) {
     if (s0 + u >= s1) break;
@@ -324,7 +382,7 @@ __device__ void down_tile(const Moe& a, int e, int n0, int s0, int s1, const uin
       const uint8_t* p = hc[g] + (s0 + u) * 128;
       const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
       const uint32_t sh = *reinterpret_cast<const uint32_t*>(hs[g] + (s0 + u) * 4) >> (8 * q);
-      acc[g] = mma_w4x8(frag4(w[u]), frag8(lo, hi), acc[g], sw[u] >> (8 * q), sh);
+      acc[g] = mma_w4x8(frag4(d.w[u]), frag8(lo, hi), acc[g], d.sw[u] >> (8 * q), sh);
     }
   }
 #pragma unroll
@@ -336,127 +394,212 @@ __device__ void down_tile(const Moe& a, int e, int n0, int s0, int s1, const uin
     }
 }
 
-// Grid: d / 16.  Work units are (used expert in rising order, range of its K steps), dealt to the
-// waves in turn; each wave adds into sums of its own, which are joined in wave order.
-template <int GMAX, bool ROUTE, bool BF16OUT>
+template <bool BF16OUT>
+__device__ __forceinline__ void store_y(const Moe& a, int t, int col, float v0, float v1) {
+  const int64_t at = (int64_t)t * a.d + col;
+  if constexpr (BF16OUT) *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) = bf16_pair(v0, v1);
+  else *reinterpret_cast<f32x2_m*>(static_cast<float*>(a.y) + at) = f32x2_m{v0, v1};
+}
+
+// Grid: d / 16 x splits.  Work units are (used expert in rising order, range of its K steps), dealt
+// in turn to the waves of all the splits; each wave adds into sums of its own.  A workgroup joins
+// its waves in order; with several splits the last workgroup of a row tile to finish joins them in
+// order (their number is fixed by the shape), so the sums do not depend on who that is.
+// TOK: token capacity; G: groups of 16 tokens per pass over an expert's weights.
+template <int TOK, int G, bool ROUTE, bool BF16OUT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
-  constexpr int kTokens = 16 * GMAX;   // a.tokens is at most this
-  __shared__ __align__(16) float out[kDownWaves][kTokens][16];
-  __shared__ int16_t id[kMaxPairs];
-  __shared__ float wts[kMaxPairs];
-  __shared__ uint64_t used[8];         // experts that a token chose: experts <= 512
-  __shared__ uint16_t lists[kDownWaves][kMaxTokens];
+  constexpr int kPairs = 16 * TOK;
+  __shared__ __align__(16) float out[kDownWaves][TOK][16];
+  __shared__ int16_t id[kPairs];
+  __shared__ float wts[kPairs];
+  __shared__ int count[512];            // by expert: pairs, then the first place in `sorted`
+  __shared__ uint16_t sorted[kPairs];   // pairs by expert
+  __shared__ uint16_t expert[kPairs], start[kPairs + 1];   // the used experts and their first place in `sorted`
+  __shared__ int used, last;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * 16;
-  if (tid < 8) used[tid] = 0;
-  for (int i = tid; i < kDownWaves * kTokens * 4; i += 64 * kDownWaves)
+  const int n0 = blockIdx.x * 16, pairs = a.tokens * a.topk;
+  // a pair's expert and weight, one thread per pair
+  int e = -1;
+  float w = 0.0f;
+  if (tid < pairs) {
+    e = a.ids[tid];
+    if constexpr (ROUTE) w = a.logits[(int64_t)(tid / a.topk) * a.experts + e];
+    else w = a.weights[tid];
+    if (e < 0 || e >= a.experts) e = -1;
+    id[tid] = (int16_t)e;
+    wts[tid] = w;
+  }
+  if (tid < 512) count[tid] = 0;
+  for (int i = tid; i < kDownWaves * TOK * 4; i += 64 * kDownWaves)
     reinterpret_cast<v4f_m*>(out)[i] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
-  if (tid < a.tokens) {   // one thread per token: its choices, weights and repeats
-    const int p0 = tid * a.topk;
-    float total = 0.0f, top = 0.0f;
-    for (int j = 0; j < a.topk; ++j) {
-      const int e = a.ids[p0 + j];
-      float w;
-      if constexpr (ROUTE) {
-        const float l = a.logits[(int64_t)tid * a.experts + e];
-        if (j == 0) top = l;
-        w = expf(l - top);
-        total += w;
-      } else {
-        w = a.weights[p0 + j];
-      }
-      wts[p0 + j] = w;
-      bool keep = e >= 0 && e < a.experts;
-      if constexpr (!ROUTE) {
-        for (int f = 0; keep && f < j; ++f)
-          if (id[p0 + f] == e) {   // an earlier place holds this expert: its weight takes this one's too
-            wts[p0 + f] += w;
-            keep = false;
-          }
-      }
-      id[p0 + j] = keep ? (int16_t)e : (int16_t)-1;
-      if (keep) atomicOr(reinterpret_cast<unsigned long long*>(&used[e >> 6]), 1ull << (e & 63));
+  int place = 0;
+  if (tid < pairs) {
+    const int p0 = tid - tid % a.topk;
+    if constexpr (ROUTE) {   // softmax over the token's choices; the first is the largest
+      const float top = wts[p0];
+      float total = 0.0f;
+      for (int j = 0; j < a.topk; ++j) total += expf(wts[p0 + j] - top);
+      w = expf(w - top) / total;
+      if (blockIdx.x == 0 && blockIdx.y == 0) a.weights[tid] = w;
+    } else if (e >= 0) {     // the first place of an expert takes the weights of its repeats, which take no part
+      for (int f = p0; f < tid; ++f)
+        if (id[f] == e) e = -1;
+      if (e >= 0)
+        for (int f = tid + 1; f < p0 + a.topk; ++f)
+          if (id[f] == e) w += wts[f];
     }
-    if constexpr (ROUTE) {
-      for (int j = 0; j < a.topk; ++j) {
-        const float w = wts[p0 + j] / total;
-        wts[p0 + j] = w;
-        if (blockIdx.x == 0) a.weights[p0 + j] = w;
+    if (e >= 0) place = atomicAdd(&count[e], 1);   // the order among an expert's pairs changes no sum
+  }
+  __syncthreads();
+  if (tid < pairs) wts[tid] = w;
+  if (wave == 0) {   // eight experts per lane: prefix sums of pairs (low half) and used experts (high half)
+    int c[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = count[8 * lane + i];
+      sum += c[i] + (c[i] ? 1 << 16 : 0);
+    }
+    int run = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+      const int v = __shfl_up(run, off, 64);
+      if (lane >= off) run += v;
+    }
+    if (lane == 63) used = run >> 16, start[run >> 16] = (uint16_t)(run & 0xFFFF);
+    run -= sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      count[8 * lane + i] = run & 0xFFFF;
+      if (c[i]) {
+        expert[run >> 16] = (uint16_t)(8 * lane + i);
+        start[run >> 16] = (uint16_t)(run & 0xFFFF);
+        run += c[i] + (1 << 16);
       }
     }
   }
   __syncthreads();
-  int active = 0;
-  for (int i = 0; i < 8; ++i) active += __popcll(used[i]);
-  // K steps per unit: enough units for every wave, at most four steps' loads in flight
-  const int nk = a.hidden / 128, pairs = a.tokens * a.topk;
-  const int per = min(max(active * nk / kDownWaves, 1), kDownSteps), parts = (nk + per - 1) / per;
-  uint16_t* list = lists[wave];
-  int unit = 0;   // first unit of the current expert
-  for (int word = 0; word < 8; ++word) {
-    // the builtin returns int: the low half must not be widened with its sign
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)used[word]);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(used[word] >> 32));
-    uint64_t m = ((uint64_t)hi << 32) | lo;
-    for (; m; m &= m - 1, unit += parts) {
-      const int e = 64 * word + __builtin_ctzll(m);
-      int k = (wave - unit % kDownWaves + kDownWaves) % kDownWaves;   // this wave's first part, if any
-      if (k >= parts) continue;
-      int n = 0;
-      for (int p0 = 0; p0 < pairs; p0 += 64) {
-        const bool hit = p0 + lane < pairs && id[p0 + lane] == e;
-        const uint64_t b = __ballot(hit);
-        if (hit) list[n + __popcll(b & ((1ull << lane) - 1ull))] = (uint16_t)(p0 + lane);
-        n += __popcll(b);
-      }
-      __builtin_amdgcn_wave_barrier();   // the list is this wave's own: LDS keeps its order
-      for (; k < parts; k += kDownWaves) {
-        const int s0 = k * per, s1 = min(s0 + per, nk);
-        if (GMAX == 1 || n <= 16) down_tile<1>(a, e, n0, s0, s1, list, n, wts, out[wave]);
-        else if (GMAX == 2 || n <= 32) down_tile<2>(a, e, n0, s0, s1, list, n, wts, out[wave]);
-        else down_tile<GMAX < 4 ? 1 : 4>(a, e, n0, s0, s1, list, n, wts, out[wave]);
-      }
-      __builtin_amdgcn_wave_barrier();
-    }
+  if (e >= 0) sorted[count[e] + place] = (uint16_t)tid;
+  const int active = __builtin_amdgcn_readfirstlane(used);
+  __syncthreads();
+  // K steps per unit: enough units for every wave, at most what one unit's registers hold
+  const int nk = a.hidden / 128, workers = kDownWaves * gridDim.y;
+  const int per = min(max(active * nk / workers, 1), kDownSteps), parts = (nk + per - 1) / per;
+  const int units = active * parts;
+  const auto load = [&](int u, DownUnit& d) {
+    const int s0 = u % parts * per;
+    load_unit(a, __builtin_amdgcn_readfirstlane(expert[u / parts]), n0, s0, min(s0 + per, nk), d);
+  };
+  DownUnit now, next;
+  int u = wave * gridDim.y + blockIdx.y;
+  if (u < units) load(u, now);
+  for (; u < units; u += workers) {
+    if (u + workers < units) load(u + workers, next);   // travels while this unit is multiplied
+    const int s0 = u % parts * per, s1 = min(s0 + per, nk);
+    const int first = __builtin_amdgcn_readfirstlane(start[u / parts]);
+    const int n = __builtin_amdgcn_readfirstlane(start[u / parts + 1]) - first;
+    for (int i = 0; i < n; i += 16 * G)
+      down_unit<G>(a, now, s0, s1, sorted + first + i, min(n - i, 16 * G), wts, out[wave]);
+    now = next;
   }
   __syncthreads();
+  const int splits = gridDim.y;
+  float* part = a.partial + ((int64_t)blockIdx.x * splits + blockIdx.y) * (kMaxTokens * 16);
+  const float* parts0 = a.partial + (int64_t)blockIdx.x * splits * (kMaxTokens * 16);
   for (int i = tid; i < a.tokens * 8; i += 64 * kDownWaves) {   // two neighbouring columns per thread
     const int t = i >> 3, c = (i & 7) * 2;
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int v = 0; v < kDownWaves; ++v) s0 += out[v][t][c], s1 += out[v][t][c + 1];
-    const int64_t at = (int64_t)t * a.d + n0 + c;
-    if constexpr (BF16OUT) {
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.y) + at) = bf16_pair(s0, s1);
+    if (splits == 1) {
+      store_y<BF16OUT>(a, t, n0 + c, s0, s1);
     } else {
-      *reinterpret_cast<f32x2_m*>(static_cast<float*>(a.y) + at) = f32x2_m{s0, s1};
+      // agent scope: the joining workgroup may sit on another die
+      __hip_atomic_store(part + 2 * i, s0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(part + 2 * i + 1, s1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+  }
+  if (splits == 1) return;
+  // The sums are written and read past the caches (agent-scope atomics), so all it takes is that
+  // every wave's stores have arrived before the count rises; a fence here would write back and
+  // invalidate the die's L2 (60 us on this launch).
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0)
+    last = __hip_atomic_fetch_add(&a.arrived[blockIdx.x], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int i = tid; i < a.tokens * 8; i += 64 * kDownWaves) {
+    float s0 = 0.0f, s1 = 0.0f;
+    for (int v = 0; v < splits; ++v) {
+      const float* p = parts0 + v * (kMaxTokens * 16) + 2 * i;
+      s0 += __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s1 += __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    store_y<BF16OUT>(a, i >> 3, n0 + (i & 7) * 2, s0, s1);
   }
 }
 
-template <int GMAX, bool ROUTE>
-void run(const Moe& a, bool bf16_out, hipStream_t st) {
-  k_moe_up<GMAX, ROUTE><<<dim3(a.hidden / 32, a.slots), 64 * kUpWaves, 0, st>>>(a);
-  if (bf16_out) k_moe_down<GMAX, ROUTE, true><<<a.d / 16, 64 * kDownWaves, 0, st>>>(a);
-  else k_moe_down<GMAX, ROUTE, false><<<a.d / 16, 64 * kDownWaves, 0, st>>>(a);
+// Groups of 16 tokens that a pass over an expert's weights takes: from the mean number of tokens
+// per expert, so that a second pass (from L2) is rare, with as few registers as that allows.
+int groups(const Moe& a) {
+  const int mean = a.tokens * a.topk / a.experts;
+  return a.tokens <= 16 || mean <= 8 ? 1 : a.tokens <= 32 || mean <= 20 ? 2 : 4;
+}
+
+template <int G, bool ROUTE>
+void run_up(const Moe& a, hipStream_t st) {
+  k_moe_up<G, ROUTE><<<dim3(a.hidden / 32, a.slots), 64 * kUpWaves, 0, st>>>(a);
+}
+
+template <int TOK, int G, bool ROUTE>
+void run_down(const Moe& a, bool bf16_out, hipStream_t st) {
+  const dim3 grid(a.d / 16, a.splits);
+  if (bf16_out) k_moe_down<TOK, G, ROUTE, true><<<grid, 64 * kDownWaves, 0, st>>>(a);
+  else k_moe_down<TOK, G, ROUTE, false><<<grid, 64 * kDownWaves, 0, st>>>(a);
 }
 
 template <bool ROUTE>
-void run_tokens(const Moe& a, bool bf16_out, hipStream_t st) {
-  if (a.tokens <= 16) run<1, ROUTE>(a, bf16_out, st);
-  else if (a.tokens <= 32) run<2, ROUTE>(a, bf16_out, st);
-  else run<4, ROUTE>(a, bf16_out, st);
+void run(const Moe& a, bool bf16_out, hipStream_t st) {
+  const int g = groups(a);
+  if (g == 1) run_up<1, ROUTE>(a, st);
+  else if (g == 2) run_up<2, ROUTE>(a, st);
+  else run_up<4, ROUTE>(a, st);
+  if (a.tokens <= 16) run_down<16, 1, ROUTE>(a, bf16_out, st);
+  else if (g == 1) run_down<64, 1, ROUTE>(a, bf16_out, st);
+  else if (g == 2) run_down<64, 2, ROUTE>(a, bf16_out, st);
+  else run_down<64, 4, ROUTE>(a, bf16_out, st);
+}
+
+// Workgroups that share a row tile of the down product: the CUs over the row tiles, up to eight.
+int down_splits(int64_t d) {
+  const int64_t s = kCus / (d / 16);
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
 int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
+// Scratch: logits, hidden codes, hidden scales, the down splits' sums and arrival counts.
+struct Layout {
+  int64_t logits, codes, scales, partial, arrived, bytes;
+};
+Layout layout(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
+  Layout l;
+  l.logits = 0;
+  l.codes = up16(tokens * experts * 4);
+  l.scales = l.codes + up16(tokens * topk * hidden);
+  l.partial = l.scales + up16(tokens * topk * (hidden / 32));
+  const int splits = down_splits(d);
+  l.arrived = l.partial + (splits > 1 ? d / 16 * splits * kMaxTokens * 16 * 4 : 0);
+  l.bytes = l.arrived + up16(d / 16 * 4);
+  return l;
+}
+
 }  // namespace
 
-// Scratch: logits, hidden codes, hidden scales.
-int64_t moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk) {
-  return up16(tokens * experts * 4) + up16(tokens * topk * hidden) + up16(tokens * topk * (hidden / 32));
+int64_t moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
+  return layout(tokens, d, hidden, experts, topk).bytes;
 }
 
 void launch_moe(const MoeArgs& m, hipStream_t st) {
@@ -464,13 +607,18 @@ void launch_moe(const MoeArgs& m, hipStream_t st) {
   a.xc = m.x_codes, a.xs = m.x_scales, a.w13c = m.w13_codes, a.w13s = m.w13_scales, a.w2c = m.w2_codes;
   a.w2s = m.w2_scales, a.tokens = m.tokens, a.d = m.d, a.hidden = m.hidden, a.experts = m.experts, a.topk = m.topk;
   a.slots = m.tokens * m.topk < m.experts ? m.tokens * m.topk : m.experts;
+  a.splits = down_splits(m.d);
   a.ids = m.ids, a.weights = m.weights, a.y = m.y;
-  float* logits = static_cast<float*>(m.scratch);
+  const Layout l = layout(m.tokens, m.d, m.hidden, m.experts, m.topk);
+  uint8_t* scratch = static_cast<uint8_t*>(m.scratch);
+  float* logits = reinterpret_cast<float*>(scratch + l.logits);
   a.logits = logits;
-  a.hc = static_cast<uint8_t*>(m.scratch) + up16((int64_t)m.tokens * m.experts * 4);
-  a.hs = a.hc + up16((int64_t)m.tokens * m.topk * m.hidden);
+  a.hc = scratch + l.codes;
+  a.hs = scratch + l.scales;
+  a.partial = reinterpret_cast<float*>(scratch + l.partial);
+  a.arrived = reinterpret_cast<int*>(scratch + l.arrived);
   if (!m.router_w) {
-    run_tokens<false>(a, m.bf16_out, st);
+    run<false>(a, m.bf16_out, st);
     return;
   }
   const dim3 grid((m.experts + 15) / 16, (m.tokens + 15) / 16);
@@ -481,7 +629,7 @@ void launch_moe(const MoeArgs& m, hipStream_t st) {
   else
     k_moe_logits<float><<<grid, 1024, 0, st>>>(static_cast<const float*>(m.router_x),
                                                static_cast<const float*>(m.router_w), m.tokens, m.d, m.experts, logits);
-  run_tokens<true>(a, m.bf16_out, st);
+  run<true>(a, m.bf16_out, st);
 }
 
 }  // namespace fp4q

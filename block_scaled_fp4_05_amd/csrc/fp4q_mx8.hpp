@@ -22,6 +22,7 @@ typedef int v8i_m __attribute__((ext_vector_type(8)));
 typedef float v4f_m __attribute__((ext_vector_type(4)));
 typedef float v16f_m __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_m __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_w __attribute__((ext_vector_type(4), aligned(4)));   // four words at a word's alignment
 typedef uint32_t u32x2_m __attribute__((ext_vector_type(2)));
 typedef float f32x2_m __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_m __attribute__((ext_vector_type(2)));

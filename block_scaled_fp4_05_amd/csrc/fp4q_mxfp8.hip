@@ -357,16 +357,17 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_dgain(const float* __restrict_
 }
 
 // Threads and chunks per thread for a row of `chunks` chunks: the fewest chunks per thread
-// (powers of two up to 32 elements, which keeps a row in registers) that fit `most` threads,
-// else 512, else 1024 (FP4Q_NORM_MAX_COLS is 1024 x 32).
+// (powers of two up to 32 elements, which keeps a row in registers) that fit 256 threads, else
+// 512, else 1024 (FP4Q_NORM_MAX_COLS is 1024 x 32).  From the width alone, so that a row's sums,
+// and with them its results, are the same whatever number of rows it comes with.
 struct RowShape {
   int v, threads;
 };
 template <typename T>
-RowShape row_shape(int64_t cols, int most) {
+RowShape row_shape(int64_t cols) {
   const int64_t chunks = cols / Chunk<T>::N;
   constexpr int kMost = 32 / Chunk<T>::N;
-  for (int limit : {most, 512, 1024})
+  for (int limit : {256, 512, 1024})
     for (int v = 1; v <= kMost; v *= 2) {
       const int64_t t = (chunks + v - 1) / v;
       if (t <= limit) return RowShape{v, (int)((t + 63) / 64 * 64)};
@@ -395,7 +396,7 @@ constexpr int kBackwardGroups = 1024;   // at most so many partial rows of dgain
 template <typename T>
 void rmsnorm(const T* x, const T* res, int64_t rows, int64_t cols, const float* gain, float eps, uint8_t* codes,
              uint8_t* scales, T* sum, float* rstd, T* y, hipStream_t st) {
-  const RowShape s = row_shape<T>(cols, rows < 512 ? 1024 : 256);
+  const RowShape s = row_shape<T>(cols);
   const int grid = (int)(rows < 2048 ? rows : 2048);
   by_chunks<NormKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(x, res, (int)rows, (int)cols, gain, eps, codes, scales, sum, rstd, y);
 }
@@ -403,7 +404,7 @@ void rmsnorm(const T* x, const T* res, int64_t rows, int64_t cols, const float* 
 template <typename T>
 void rmsnorm_backward(const T* dy, const T* s_in, const T* dsum, int64_t rows, int64_t cols, const float* gain,
                       const float* rstd, T* dx, float* dgain, float* partial, hipStream_t st) {
-  const RowShape s = row_shape<T>(cols, rows < 512 ? 1024 : 256);
+  const RowShape s = row_shape<T>(cols);
   const int grid = (int)(rows < kBackwardGroups ? rows : kBackwardGroups);
   by_chunks<BackwardKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(dy, s_in, dsum, (int)rows, (int)cols, gain, rstd, dx, partial);
   k_rmsnorm_dgain<<<(unsigned)(cols / 32), 1024, 0, st>>>(partial, grid, (int)cols, dgain);

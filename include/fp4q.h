@@ -392,7 +392,8 @@ fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, i
  * Residual addition, root-mean-square norm and MXFP8 in one read of x:
  *   s = x + residual (x without one),  r = 1 / sqrt(mean(s^2) + eps),  n = (s r) gain,
  *   codes, scales = MXFP8(n) as fp4q_quantize_mxfp8 writes it.
- * All of it in fp32 from the unrounded s; what is stored is rounded once.
+ * All of it in fp32 from the unrounded s; what is stored is rounded once.  A row's results do not
+ * depend on the other rows or their number.
  *   x, residual  [rows][cols] of type dt; residual may be NULL.
  *   gain         device float [cols].        eps >= 0, finite.
  *   sum          s in type dt, or NULL.  It may be x itself or residual itself (in place);
@@ -441,7 +442,8 @@ int64_t fp4q_rmsnorm_backward_scratch(int64_t rows, int64_t cols);
  * rounding A to E4M3).
  *   out_dt FP4Q_F32: float [m][n];  FP4Q_BF16: bf16 [m][n] = RNE(fp32 result).
  * A NaN code or scale (255) makes the elements of C that it takes part in NaN.
- * Shapes: m >= 1, n >= 1, k >= 128 with k % 128 == 0 and k <= 2^25, m, n < 2^31.
+ * Shapes: m >= 1, n >= 1, k >= 128 with k % 128 == 0 and k <= 2^25, m, n < 2^31 and at most 2^24
+ * tiles of 256 x 256 in C.
  */
 fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                                   const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, fp4q_dtype out_dt,
@@ -468,7 +470,7 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scale
  *               without any gets y = 0.  An expert that a token names twice gets both weights.
  *   ids      device int32 [tokens][topk];  weights  device float [tokens][topk]
  *   y        [tokens][d]: float, or bf16 (RNE of the fp32 sum)
- *   scratch  device memory of at least fp4q_moe_scratch(tokens, hidden, experts, topk) bytes,
+ *   scratch  device memory of at least fp4q_moe_scratch(tokens, d, hidden, experts, topk) bytes,
  *            16-byte aligned; its contents before and after the call mean nothing.
  * A NaN logit ranks above every number, so it is chosen and makes its token's weights NaN; so does
  * a chosen +infinity.
@@ -487,7 +489,7 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
                            unsigned route_mode, int32_t* ids, float* weights, fp4q_dtype out_dt, void* y,
                            void* scratch, int64_t scratch_bytes, hipStream_t stream);
 /* Bytes of scratch for that call (0 for a shape it refuses).  Host only. */
-int64_t fp4q_moe_scratch(int64_t tokens, int64_t hidden, int64_t experts, int64_t topk);
+int64_t fp4q_moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk);
 
 /* max |x| over the whole matrix, written to device float *amax. */
 fp4q_status fp4q_amax(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, float* amax,

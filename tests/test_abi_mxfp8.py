@@ -73,13 +73,15 @@ def test_helpers_refuse_what_the_library_cannot_see():
         B.quantize_mxfp8(torch.zeros(4, 64))
     with pytest.raises(ValueError):
         B.rmsnorm_mxfp8(torch.zeros(4, 64), torch.ones(64))
-    dev = torch.device("cpu")
+    dev = -1                                               # the CPU's index
     x = torch.zeros(8, 64)
     for bad, err in ((x.double(), TypeError), (torch.zeros(8, 32), ValueError), (torch.zeros(64, 8).t(), ValueError),
-                     (None, TypeError), (x[:, ::1].to("meta"), ValueError)):
+                     (None, TypeError)):
         with pytest.raises(err):
             B._need("t", bad, torch.float32, (8, 64), dev)
-    B._need("t", x, torch.float32, (8, 64), dev)
+    with pytest.raises(ValueError):
+        B._need("t", x, torch.float32, (8, 64), 0)         # another device
+    assert B._need("t", x, torch.float32, (8, 64), dev) == x.data_ptr()
 
 
 GEMM = dict(ac=A, asc=A, bc=A, bsc=A, m=4, n=8, k=256, dt=B.F32, c=A, stream=0)
@@ -105,7 +107,7 @@ MOE = dict(xc=A, xs=A, rx=A, rw=A, rdt=B.BF16, w13c=A, w13s=A, w2c=A, w2s=A, tok
     (dict(tokens=0), 2), (dict(tokens=65), 2), (dict(d=192), 2), (dict(d=0), 2), (dict(d=65664), 2),
     (dict(hidden=64), 2), (dict(hidden=65664), 2), (dict(experts=0), 2), (dict(experts=513), 2), (dict(topk=0), 2),
     (dict(topk=9), 2), (dict(experts=64, topk=17), 2),
-    (dict(scratch_bytes=B.fp4q_moe_scratch(4, 128, 8, 2) - 1), 4), (dict(xc=MIS), 3), (dict(rx=MIS), 3),
+    (dict(scratch_bytes=B.fp4q_moe_scratch(4, 256, 128, 8, 2) - 1), 4), (dict(xc=MIS), 3), (dict(rx=MIS), 3),
     (dict(w13c=MIS), 3), (dict(w2s=MIS), 3), (dict(ids=A + 2), 3), (dict(weights=A + 1), 3), (dict(y=MIS), 3),
     (dict(scratch=MIS), 3),
     (dict(mode=B.ROUTE_GIVEN, rx=None, rw=None, y=None), 1), (dict(mode=B.ROUTE_GIVEN, rx=None, rw=None, xs=MIS), 3)])
@@ -114,5 +116,5 @@ def test_moe(kw, status):
 
 
 def test_moe_scratch():
-    assert B.fp4q_moe_scratch(65, 128, 8, 2) == 0 and B.fp4q_moe_scratch(4, 100, 8, 2) == 0
-    assert B.fp4q_moe_scratch(64, 65536, 512, 16) >= 64 * 16 * 65536
+    assert B.fp4q_moe_scratch(65, 128, 128, 8, 2) == 0 and B.fp4q_moe_scratch(4, 128, 100, 8, 2) == 0
+    assert B.fp4q_moe_scratch(64, 128, 65536, 512, 16) >= 64 * 16 * 65536

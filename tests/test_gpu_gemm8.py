@@ -52,9 +52,30 @@ def test_whole_values_are_exact(m, n, k):
 
 @pytest.mark.parametrize("m,n,k", [(1, 4096, 8192), (64, 2050, 2048), (70, 13000, 512), (1000, 3000, 640),
                                    (1500, 2301, 256), (3600, 3601, 384), (4096, 8192, 256), (65, 70000, 128),
-                                   (20000, 65, 128)])
+                                   (20000, 65, 128), (3600, 3601, 512), (3600, 3601, 640), (3500, 3700, 1536),
+                                   (1000, 3000, 1024), (900, 3001, 2688), (193, 4099, 640), (193, 4099, 1536),
+                                   (1, 33000, 256), (16, 8200, 640), (5, 40001, 1152), (32, 8193, 384),
+                                   (20, 8193, 1280), (3, 70000, 512)])
 def test_whole_values_large(m, n, k):
     _check_whole(m, n, k)
+
+
+@pytest.mark.parametrize("m,n,k", [(2, (1 << 25) + 33, 256), (3, (1 << 26) + 17, 128), (70000, 65540, 128)])
+def test_offsets_past_32_bits(m, n, k):
+    """Codes of B past 4 GiB (few rows, and the tiles that take over), or 2^32 outputs: the last
+    rows against the same rows multiplied alone."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    a, b = _dev(*_whole(min(m, 1000), k, 8, 0)), _dev(*_whole(1000, k, 4, 1))
+    a = {key: v.repeat(-(-m // v.shape[0]), 1)[:m].contiguous() for key, v in a.items()}
+    codes = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device=DEV, generator=g)
+    scales = torch.randint(126, 129, (n, k // 32), dtype=torch.uint8, device=DEV, generator=g)
+    print("gemm8", m, n, k, flush=True)
+    c = B.gemm_mxfp8_mxfp4(a, {"codes": codes, "scales": scales}, torch.bfloat16)
+    rows = slice(max(0, m - 70), m)
+    last = {key: v[rows].clone() for key, v in a.items()}
+    for at in (0, n // 2, n - 300):
+        part = {"codes": codes[at:at + 300].clone(), "scales": scales[at:at + 300].clone()}
+        assert torch.equal(c[rows, at:at + 300], B.gemm_mxfp8_mxfp4(last, part, torch.bfloat16))
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 64, 4096), (5, 33, 1152), (48, 40, 640), (130, 70, 512), (260, 96, 256)])

@@ -228,3 +228,19 @@ def test_norm_and_quantizer_in_a_graph():
         for a, b in ((o["codes"], e["codes"]), (o["scales"], e["scales"]), (o["sum"], e["sum"]),
                      (q["codes"], B.quantize_mxfp8(x)["codes"]), (dx, ex), (dg, eg)):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements: the last rows against the same rows alone."""
+    rows, cols = (1 << 20) + 5, 4128
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV)
+    x[:] = torch.randn(cols, device=DEV).bfloat16()
+    x[-7:] = torch.randn(7, cols, device=DEV).bfloat16()
+    tail = x[-7:].clone()
+    gain = torch.ones(cols, device=DEV)
+    for q, t in ((B.quantize_mxfp8(x), B.quantize_mxfp8(tail)), (B.rmsnorm_mxfp8(x, gain), B.rmsnorm_mxfp8(tail, gain))):
+        assert torch.equal(q["codes"][-7:], t["codes"]) and torch.equal(q["scales"][-7:], t["scales"])
+    assert torch.equal(B.dequantize_mxfp8(q, torch.bfloat16)[-7:], B.dequantize_mxfp8(t, torch.bfloat16))
+    rstd = torch.ones(rows, device=DEV)
+    assert torch.equal(B.rmsnorm_backward(x, x, gain, rstd)[0][-7:],
+                       B.rmsnorm_backward(tail, tail, gain, rstd[:7].contiguous())[0])
