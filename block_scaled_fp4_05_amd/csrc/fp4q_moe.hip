@@ -212,69 +212,94 @@ __device__ int expert_of_slot(const Moe& a, int slot, RouteLds& r) {
   }
 }
 
-constexpr int kUpWaves = 8;
-
-// Sums of the eight waves on their way to one: [wave][row tile][q][17 columns] of four rows each
+// Sums of a workgroup's waves on their way to one: [wave][row tile][q][17 columns] of four rows each
 // (the 17th column spreads the readers over the banks).
-typedef v4f_m UpSums[kUpWaves][4][4][17];
+typedef v4f_m UpSums[4][4][17];
 
-// Gate and up products of 32 hidden columns (four row tiles of 16: two of gate, two of up) for
-// G groups of 16 tokens, and the hidden activations of them.
-template <int G>
-__device__ void up_tiles(const Moe& a, int e, int h0, const uint16_t* list, int n, UpSums sums) {
+// K steps whose codes a wave has in flight: with more groups the registers go to their sums.
+constexpr int up_steps(int g) { return g == 1 ? 2 : 1; }
+
+// The weights of a workgroup's 32 hidden columns: four row tiles of 16, two of gate, two of up.
+template <int U>
+struct UpWeights {
+  u32x4_m w[U][4];
+};
+struct UpRows {   // the lane's row in the first tile; the others are uniform distances away
+  const uint8_t *wc, *ws;
+  int64_t up;   // rows from gate to up
+  __device__ __forceinline__ int64_t rows(int i) const { return (i & 1 ? 16 : 0) + (i >> 1 ? up : 0); }
+};
+__device__ __forceinline__ UpRows up_rows(const Moe& a, int e, int h0) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int64_t row = (int64_t)e * 2 * a.hidden + h0 + r;
+  return UpRows{a.w13c + row * (a.d / 2) + 16 * q, a.w13s + row * (a.d / 32), a.hidden};
+}
+// First K step of a wave, of W that share d.
+template <int W>
+__device__ __forceinline__ int up_first(const Moe& a, int wave) {
+  return a.d / 128 * wave / W;
+}
+// Steps s .. s + U - 1 (past `last` the last again, unused).
+template <int U>
+__device__ __forceinline__ void load_up(const Moe& a, const UpRows& u, int s, int last, UpWeights<U>& d) {
+#pragma unroll
+  for (int k = 0; k < U; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      d.w[k][i] = *reinterpret_cast<const u32x4_m*>(u.wc + (u.rows(i) * (a.d / 2) + min(s + k, last - 1) * 64));
+}
+
+// Gate and up products for G groups of 16 tokens, and the hidden activations of them.  `ahead`: this
+// wave's first weights, loaded.
+template <int G, int W>
+__device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_t* list, int n,
+                         UpWeights<up_steps(G)>& ahead, UpSums* sums) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nk = a.d / 128, first = nk * wave / kUpWaves, last = nk * (wave + 1) / kUpWaves;
-  const int64_t cols = a.d / 2, scols = a.d / 32;
-  const uint8_t* wc[4];
-  const uint8_t* ws[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = ((int64_t)e * 2 + (i >> 1)) * a.hidden + h0 + 16 * (i & 1) + r;
-    wc[i] = a.w13c + row * cols + 16 * q;
-    ws[i] = a.w13s + row * scols;
-  }
+  constexpr int U = up_steps(G);
+  const int nk = a.d / 128, first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1);
   const uint8_t* xc[G];
   const uint8_t* xs[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int t = list[min(16 * g + r, n - 1)] / a.topk;   // columns past n repeat the last; not stored
     xc[g] = a.xc + (int64_t)t * a.d + 16 * q;
-    xs[g] = a.xs + (int64_t)t * scols;
+    xs[g] = a.xs + (int64_t)t * (a.d / 32);
   }
   v4f_m acc[4][G];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[i][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int U = G == 1 ? 2 : 1;   // steps whose loads are in flight together; past the end the last again, unused
-  for (int s = first; s < last; s += U) {
-    u32x4_m w[U][4], xl[U][G], xh[U][G];
-    uint32_t sw[U][4], sx[U][G];
+  for (int s = first; s < last; s += 4) {
+    u32x4_m sw[4], sx[G];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int at = min(s + u, last - 1);
+    for (int i = 0; i < 4; ++i) sw[i] = scale_words(rows.ws + rows.rows(i) * (a.d / 32), s, nk);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[u][i] = *reinterpret_cast<const u32x4_m*>(wc[i] + at * 64);
-        sw[u][i] = *reinterpret_cast<const uint32_t*>(ws[i] + at * 4);
+    for (int g = 0; g < G; ++g) sx[g] = scale_words(xs[g], s, nk);
+#pragma unroll
+    for (int h = 0; h < 4; h += U) {
+      if (s + h >= last) break;
+      u32x4_m xl[U][G], xh[U][G];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const uint8_t* p = xc[g] + min(s + h + k, last - 1) * 128;
+          xl[k][g] = *reinterpret_cast<const u32x4_m*>(p);
+          xh[k][g] = *reinterpret_cast<const u32x4_m*>(p + 64);
+        }
+      if (s + h > first) load_up<U>(a, rows, s + h, last, ahead);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (s + h + k >= last) break;
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[i][g] = mma_w4x8(frag4(ahead.w[k][i]), frag8(xl[k][g], xh[k][g]), acc[i][g], sw[i][h + k] >> (8 * q),
+                                 sx[g][h + k] >> (8 * q));
       }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        xl[u][g] = *reinterpret_cast<const u32x4_m*>(xc[g] + at * 128);
-        xh[u][g] = *reinterpret_cast<const u32x4_m*>(xc[g] + at * 128 + 64);
-        sx[u][g] = *reinterpret_cast<const uint32_t*>(xs[g] + at * 4);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (s + u >= last) break;
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[i][g] = mma_w4x8(frag4(w[u][i]), frag8(xl[u][g], xh[u][g]), acc[i][g], sw[u][i] >> (8 * q),
-                               sx[u][g] >> (8 * q));
     }
   }
 #pragma unroll
@@ -284,42 +309,53 @@ __device__ void up_tiles(const Moe& a, int e, int h0, const uint16_t* list, int 
     for (int i = 0; i < 4; ++i) sums[wave][i][q][r] = acc[i][g];
     __syncthreads();
     // thread -> token column c, hidden column i; 32 neighbouring lanes hold one MXFP8 block
-    const int c = threadIdx.x >> 5, i = threadIdx.x & 31;
-    float gate = 0.0f, up = 0.0f;
+    const int i = threadIdx.x & 31;
 #pragma unroll
-    for (int v = 0; v < kUpWaves; ++v) {
-      gate += sums[v][i >> 4][(i >> 2) & 3][c][i & 3];
-      up += sums[v][2 + (i >> 4)][(i >> 2) & 3][c][i & 3];
-    }
-    const float h = gate / (1.0f + expf(-gate)) * up;
-    float m = __builtin_fabsf(h);
-    m = m < __builtin_inff() ? m : 0.0f;   // the scale is that of the finite values
-    m = lane_xor_max<1>(m);
-    m = lane_xor_max<2>(m);
+    for (int c = threadIdx.x >> 5; c < 16; c += 2 * W) {
+      float gate = 0.0f, up = 0.0f;
 #pragma unroll
-    for (int off = 4; off <= 16; off *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, off, 64));
-    const uint32_t code = (uint32_t)max((int)((__float_as_uint(m) + 0x1FFFFFu) >> 23) - 8, 0);
-    const float inv = __uint_as_float((254u - code) << 23);
-    const uint32_t byte = __builtin_amdgcn_cvt_pk_fp8_f32(h * inv, 0.0f, 0, false) & 0xFFu;
-    if (16 * g + c < n) {
-      const int64_t p = list[16 * g + c];
-      a.hc[p * a.hidden + h0 + i] = (uint8_t)byte;
-      if (i == 0) a.hs[p * (a.hidden / 32) + h0 / 32] = (uint8_t)code;
+      for (int v = 0; v < W; ++v) {
+        gate += sums[v][i >> 4][(i >> 2) & 3][c][i & 3];
+        up += sums[v][2 + (i >> 4)][(i >> 2) & 3][c][i & 3];
+      }
+      const float h = gate / (1.0f + expf(-gate)) * up;
+      float m = __builtin_fabsf(h);
+      m = m < __builtin_inff() ? m : 0.0f;   // the scale is that of the finite values
+      m = lane_xor_max<1>(m);
+      m = lane_xor_max<2>(m);
+#pragma unroll
+      for (int off = 4; off <= 16; off *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, off, 64));
+      const uint32_t code = (uint32_t)max((int)((__float_as_uint(m) + 0x1FFFFFu) >> 23) - 8, 0);
+      const float inv = __uint_as_float((254u - code) << 23);
+      const uint32_t byte = __builtin_amdgcn_cvt_pk_fp8_f32(h * inv, 0.0f, 0, false) & 0xFFu;
+      if (16 * g + c < n) {
+        const int64_t p = list[16 * g + c];
+        a.hc[p * a.hidden + h0 + i] = (uint8_t)byte;
+        if (i == 0) a.hs[p * (a.hidden / 32) + h0 / 32] = (uint8_t)code;
+      }
     }
   }
 }
 
 // Grid: hidden / 32 tiles x slots.  G: groups of 16 tokens per pass over the expert's weights.
-template <int G, bool ROUTE>
-__global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_up(Moe a) {
-  __shared__ UpSums sums;
+template <int G, int W, bool ROUTE>
+__global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
+  __shared__ UpSums sums[W];
   __shared__ RouteLds r;
   // the arrival counts of the launch that follows; any workgroups do, before the first can leave
   for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < a.d / 16;
        i += gridDim.x * gridDim.y * blockDim.x)
     a.arrived[i] = 0;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1), h0 = blockIdx.x * 32;
   const int e = expert_of_slot<ROUTE>(a, blockIdx.y, r);
   if (e < 0) return;
+  // The first weights travel while the expert's tokens are looked up, where few workgroups turn
+  // out to have none (2 choices per expert: one in seven).
+  const bool early = a.tokens * a.topk >= 2 * a.experts;
+  const UpRows rows = up_rows(a, e, h0);
+  UpWeights<up_steps(G)> ahead;
+  if (early && first < last) load_up<up_steps(G)>(a, rows, first, last, ahead);
   int n;
   if (ROUTE && a.tokens == 1 && a.slots != a.experts) {   // one token: its choice is the whole list
     if (threadIdx.x == 0) {
@@ -332,17 +368,20 @@ __global__ __launch_bounds__(64 * kUpWaves, 4) void k_moe_up(Moe a) {
     n = pairs_of_expert<ROUTE>(a, e, r, blockIdx.x == 0);
   }
   if (n == 0 || (a.slots != a.experts && r.list[0] != blockIdx.y)) return;
-  const int h0 = blockIdx.x * 32;
-  for (int i = 0; i < n; i += 16 * G) up_tiles<G>(a, e, h0, r.list + i, min(n - i, 16 * G), sums);
+  for (int i = 0; i < n; i += 16 * G) {
+    if ((i > 0 || !early) && first < last) load_up<up_steps(G)>(a, rows, first, last, ahead);
+    up_tiles<G, W>(a, rows, h0, r.list + i, min(n - i, 16 * G), ahead, sums);
+  }
 }
 
 constexpr int kDownWaves = 16;
 constexpr int kDownSteps = 4;   // most K steps of a unit of work
+constexpr int kNone = 0xFFFF;   // no expert
 
 // Weights of one unit of work: up to kDownSteps K steps of one expert's 16 output rows.
 struct DownUnit {
   u32x4_m w[kDownSteps];
-  uint32_t sw[kDownSteps];
+  u32x4_m sw;
 };
 __device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, int s1, DownUnit& d) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
@@ -353,8 +392,8 @@ __device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, i
   for (int u = 0; u < kDownSteps; ++u) {   // past the unit's end the last step again, unused
     const int at = min(s0 + u, s1 - 1);
     d.w[u] = *reinterpret_cast<const u32x4_m*>(wc + at * 64);
-    d.sw[u] = *reinterpret_cast<const uint32_t*>(ws + at * 4);
   }
+  d.sw = scale_words(ws, s0, a.hidden / 128);
 }
 
 // The unit's product with its expert's hidden rows, added with the pairs' weights to this wave's
@@ -374,6 +413,9 @@ __device__ __forceinline__ void down_unit(const Moe& a, const DownUnit& d, int s
   v4f_m acc[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc[g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4_m sh[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) sh[g] = scale_words(hs[g], s0, a.hidden / 128);
 #pragma unroll
   for (int u = 0; u < kDownSteps; ++u) {
     if (s0 + u >= s1) break;
@@ -381,8 +423,7 @@ __device__ __forceinline__ void down_unit(const Moe& a, const DownUnit& d, int s
     for (int g = 0; g < G; ++g) {
       const uint8_t* p = hc[g] + (s0 + u) * 128;
       const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
-      const uint32_t sh = *reinterpret_cast<const uint32_t*>(hs[g] + (s0 + u) * 4) >> (8 * q);
-      acc[g] = mma_w4x8(frag4(d.w[u]), frag8(lo, hi), acc[g], d.sw[u] >> (8 * q), sh);
+      acc[g] = mma_w4x8(frag4(d.w[u]), frag8(lo, hi), acc[g], d.sw[u] >> (8 * q), sh[g][u] >> (8 * q));
     }
   }
 #pragma unroll
@@ -419,6 +460,19 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n0 = blockIdx.x * 16, pairs = a.tokens * a.topk;
+  // K steps per unit: enough units for every wave, at most what one unit's registers hold
+  const int nk = a.hidden / 128, workers = kDownWaves * gridDim.y;
+  DownUnit now, next;
+  int u = wave * gridDim.y + blockIdx.y;
+  const auto unit_steps = [&](int active) { return min(max(active * nk / workers, 1), kDownSteps); };
+  // One token: its choices are the units' experts as they stand (a repeated one is two units), so
+  // nothing is sorted and the first weights travel while the rest is set up.
+  const bool single = TOK == 16 && a.tokens == 1;
+  if (single) {
+    const int per = unit_steps(a.topk), parts = (nk + per - 1) / per, s0 = u % parts * per;
+    const int e = u < a.topk * parts ? a.ids[u / parts] : -1;
+    if (e >= 0 && e < a.experts) load_unit(a, e, n0, s0, min(s0 + per, nk), now);
+  }
   // a pair's expert and weight, one thread per pair
   int e = -1;
   float w = 0.0f;
@@ -443,18 +497,24 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
       for (int j = 0; j < a.topk; ++j) total += expf(wts[p0 + j] - top);
       w = expf(w - top) / total;
       if (blockIdx.x == 0 && blockIdx.y == 0) a.weights[tid] = w;
-    } else if (e >= 0) {     // the first place of an expert takes the weights of its repeats, which take no part
+    } else if (e >= 0 && !single) {   // the first place of an expert takes the weights of its repeats, which take no part
       for (int f = p0; f < tid; ++f)
         if (id[f] == e) e = -1;
       if (e >= 0)
         for (int f = tid + 1; f < p0 + a.topk; ++f)
           if (id[f] == e) w += wts[f];
     }
-    if (e >= 0) place = atomicAdd(&count[e], 1);   // the order among an expert's pairs changes no sum
+    if (single) {
+      sorted[tid] = start[tid] = (uint16_t)tid;
+      expert[tid] = (uint16_t)e;   // kNone: the unit is skipped
+      if (tid == 0) used = start[pairs] = (uint16_t)pairs;
+    } else if (e >= 0) {
+      place = atomicAdd(&count[e], 1);   // the order among an expert's pairs changes no sum
+    }
   }
   __syncthreads();
   if (tid < pairs) wts[tid] = w;
-  if (wave == 0) {   // eight experts per lane: prefix sums of pairs (low half) and used experts (high half)
+  if (!single && wave == 0) {   // eight experts per lane: prefix sums of pairs (low half) and used experts (high half)
     int c[8], sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -480,26 +540,25 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
     }
   }
   __syncthreads();
-  if (e >= 0) sorted[count[e] + place] = (uint16_t)tid;
+  if (!single) {
+    if (e >= 0) sorted[count[e] + place] = (uint16_t)tid;
+    __syncthreads();
+  }
   const int active = __builtin_amdgcn_readfirstlane(used);
-  __syncthreads();
-  // K steps per unit: enough units for every wave, at most what one unit's registers hold
-  const int nk = a.hidden / 128, workers = kDownWaves * gridDim.y;
-  const int per = min(max(active * nk / workers, 1), kDownSteps), parts = (nk + per - 1) / per;
+  const int per = unit_steps(active), parts = (nk + per - 1) / per;
   const int units = active * parts;
   const auto load = [&](int u, DownUnit& d) {
-    const int s0 = u % parts * per;
-    load_unit(a, __builtin_amdgcn_readfirstlane(expert[u / parts]), n0, s0, min(s0 + per, nk), d);
+    const int s0 = u % parts * per, e = __builtin_amdgcn_readfirstlane(expert[u / parts]);
+    if (e != kNone) load_unit(a, e, n0, s0, min(s0 + per, nk), d);
   };
-  DownUnit now, next;
-  int u = wave * gridDim.y + blockIdx.y;
-  if (u < units) load(u, now);
+  if (!single && u < units) load(u, now);
   for (; u < units; u += workers) {
     if (u + workers < units) load(u + workers, next);   // travels while this unit is multiplied
     const int s0 = u % parts * per, s1 = min(s0 + per, nk);
     const int first = __builtin_amdgcn_readfirstlane(start[u / parts]);
     const int n = __builtin_amdgcn_readfirstlane(start[u / parts + 1]) - first;
-    for (int i = 0; i < n; i += 16 * G)
+    const bool none = __builtin_amdgcn_readfirstlane(expert[u / parts]) == kNone;
+    for (int i = 0; i < n && !none; i += 16 * G)
       down_unit<G>(a, now, s0, s1, sorted + first + i, min(n - i, 16 * G), wts, out[wave]);
     now = next;
   }
@@ -550,7 +609,11 @@ int groups(const Moe& a) {
 
 template <int G, bool ROUTE>
 void run_up(const Moe& a, hipStream_t st) {
-  k_moe_up<G, ROUTE><<<dim3(a.hidden / 32, a.slots), 64 * kUpWaves, 0, st>>>(a);
+  // waves per workgroup: four K steps each, where there are as many (with eight for d = 2048, half
+  // of a workgroup's time went into its set-up and joins)
+  const dim3 grid(a.hidden / 32, a.slots);
+  if (a.d >= 4096) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
+  else k_moe_up<G, 4, ROUTE><<<grid, 256, 0, st>>>(a);
 }
 
 template <int TOK, int G, bool ROUTE>
@@ -572,9 +635,12 @@ void run(const Moe& a, bool bf16_out, hipStream_t st) {
   else run_down<64, 4, ROUTE>(a, bf16_out, st);
 }
 
-// Workgroups that share a row tile of the down product: the CUs over the row tiles, up to eight.
-int down_splits(int64_t d) {
-  const int64_t s = kCus / (d / 16);
+// Workgroups that share a row tile of the down product: as many as there are CUs for each tile, but
+// no more than leaves a wave a full unit of work (the join takes 2 us), up to eight.
+int down_splits(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
+  const int64_t used = tokens * topk < experts ? tokens * topk : experts;
+  const int64_t cus = kCus / (d / 16), work = used * (hidden / 128) / (kDownSteps * kDownWaves);
+  const int64_t s = cus < work ? cus : work;
   return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 
@@ -590,7 +656,7 @@ Layout layout(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_
   l.codes = up16(tokens * experts * 4);
   l.scales = l.codes + up16(tokens * topk * hidden);
   l.partial = l.scales + up16(tokens * topk * (hidden / 32));
-  const int splits = down_splits(d);
+  const int splits = down_splits(tokens, d, hidden, experts, topk);
   l.arrived = l.partial + (splits > 1 ? d / 16 * splits * kMaxTokens * 16 * 4 : 0);
   l.bytes = l.arrived + up16(d / 16 * 4);
   return l;
@@ -607,7 +673,7 @@ void launch_moe(const MoeArgs& m, hipStream_t st) {
   a.xc = m.x_codes, a.xs = m.x_scales, a.w13c = m.w13_codes, a.w13s = m.w13_scales, a.w2c = m.w2_codes;
   a.w2s = m.w2_scales, a.tokens = m.tokens, a.d = m.d, a.hidden = m.hidden, a.experts = m.experts, a.topk = m.topk;
   a.slots = m.tokens * m.topk < m.experts ? m.tokens * m.topk : m.experts;
-  a.splits = down_splits(m.d);
+  a.splits = down_splits(m.tokens, m.d, m.hidden, m.experts, m.topk);
   a.ids = m.ids, a.weights = m.weights, a.y = m.y;
   const Layout l = layout(m.tokens, m.d, m.hidden, m.experts, m.topk);
   uint8_t* scratch = static_cast<uint8_t*>(m.scratch);

@@ -51,6 +51,26 @@ __device__ __forceinline__ v16f_m mma_x8w4_hi(v8i_m x, v8i_m w, v16f_m acc, uint
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, w, acc, 0, 4, 2, (int)sx, 2, (int)sw);
 }
 
+// Scale words s .. s + 3 of a row of n words (four blocks each, little end first), in one load
+// where the row has four: a load of one word per row costs the address unit as much as 16 bytes
+// per lane.  Words past the row's end repeat its last.
+__device__ __forceinline__ u32x4_m scale_words(const uint8_t* row, int s, int n) {
+  u32x4_m v;
+  if (n >= 4) {
+    const int at = min(s, n - 4), down = min(s - at, 3);
+    v = *reinterpret_cast<const u32x4_w*>(row + 4 * at);
+    const uint32_t one = 0u - (uint32_t)(down & 1), two = 0u - (uint32_t)(down >> 1);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] = (v[j] & ~one) | (v[j + 1] & one);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[j] = (v[j] & ~two) | (v[j + 2] & two);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(row + 4 * min(s + j, n - 1));
+  }
+  return v;
+}
+
 // Two fp32 values to packed bf16, nearest even (v_cvt_pk_bf16_f32; NaN stays NaN).
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_m{a, b}), bf16x2_m));
