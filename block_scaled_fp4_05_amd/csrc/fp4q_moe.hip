@@ -1,7 +1,8 @@
-// A mixture-of-experts layer for a few tokens over MXFP4 expert weights, in two launches, three
-// with the router:
+// A mixture-of-experts layer for a few tokens over MXFP4 expert weights, in two launches, and up to
+// two more for the router:
 //
 //   k_moe_logits   l = router_x router_w^T                                 (router only)
+//   k_moe_topk     each token's experts and weights          (router, more than one token)
 //   k_moe_up       per expert and 32 hidden columns: its tokens' gate and up products,
 //                  silu(gate) * up, rounded to MXFP8
 //   k_moe_down     per 16 output columns: every expert's down product, weighted and added up
@@ -82,16 +83,55 @@ __global__ __launch_bounds__(1024) void k_moe_logits(const T* __restrict__ x, co
   }
 }
 
+// Each token's top-k, one wave per token: k rounds of a maximum over (logit, lower index first) that
+// each lane keeps for its experts (lane, lane + 64, ...), then the softmax over the k.
+__global__ __launch_bounds__(64) void k_moe_topk(const float* __restrict__ logits, int experts, int topk,
+                                                 int32_t* __restrict__ ids, float* __restrict__ weights) {
+  constexpr int kPerLane = 512 / 64;
+  const int lane = threadIdx.x, t = blockIdx.x;
+  const float* l = logits + (int64_t)t * experts;
+  // key of an expert: its logit's order above, the complement of its index below; 0: taken or none
+  uint64_t key[kPerLane];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int e = lane + 64 * i;
+    key[i] = e < experts ? ((uint64_t)logit_key(l[e]) << 32) | (uint32_t)~e : 0ull;
+  }
+  int chosen = 0;   // lane j: the j-th choice
+  for (int j = 0; j < topk; ++j) {
+    uint64_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < kPerLane; ++i) best = key[i] > best ? key[i] : best;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)best, off, 64);
+      best = o > best ? o : best;
+    }
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) key[i] = key[i] == best ? 0ull : key[i];
+    if (lane == j) chosen = (int)~(uint32_t)best;
+  }
+  // every lane adds the exponentials in the order of the choices
+  const float own = lane < topk ? l[chosen] : 0.0f, top = __shfl(own, 0, 64);
+  const float w = expf(own - top);
+  float total = 0.0f;
+  for (int j = 0; j < topk; ++j) total += __shfl(w, j, 64);
+  if (lane < topk) {
+    ids[t * topk + lane] = chosen;
+    weights[t * topk + lane] = w / total;
+  }
+}
+
 // Arguments of the expert kernels.
 struct Moe {
   const uint8_t *xc, *xs;       // MXFP8 tokens [tokens][d]
   const uint8_t *w13c, *w13s;   // MXFP4 [experts][2 hidden][d]: gate rows, then up rows
   const uint8_t *w2c, *w2s;     // MXFP4 [experts][d][hidden]
   int tokens, d, hidden, experts, topk;
-  int slots;                    // workgroup columns of k_moe_up: see expert_of_slot
-  int32_t* ids;                 // [tokens][topk]; read, or written by k_moe_up when routing
-  float* weights;               // [tokens][topk]; read, or written by k_moe_down when routing
-  const float* logits;          // [tokens][experts], routing only
+  int slots;                    // workgroup columns of k_moe_up: see there
+  int32_t* ids;                 // [tokens][topk]; routing one token, k_moe_up writes them
+  float* weights;               // [tokens][topk]; routing one token, k_moe_down writes them
+  const float* logits;          // [experts], routing one token only
   uint8_t *hc, *hs;             // scratch: MXFP8 hidden rows [tokens * topk][hidden]
   int splits;                   // workgroups per row tile of k_moe_down
   float* partial;               // scratch: their sums [d / 16][splits][64][16]
@@ -100,116 +140,58 @@ struct Moe {
 };
 
 // Which pairs (token * topk + place) chose expert `e`, in order, in `list`; returns how many.  Whole
-// workgroup; ends with a barrier.
-//
-// With given ids: a token that names an expert twice counts once (its first place; k_moe_down
-// adds the weights up).  When routing: the place of e among a token's logits is the number of
-// larger ones, ties to the lower index, so no sort is needed; each wave takes eight tokens at a
-// time, whose logits are loaded together.
+// workgroup; ends with a barrier.  A token that names an expert twice counts once, by its first
+// place; k_moe_down adds the weights up.
 struct RouteLds {
   union {
     int16_t id[kMaxPairs];
     uint32_t key[512];
-    uint8_t place[kMaxTokens];
   };
   uint16_t list[kMaxTokens];
   int count, found;
 };
 
-template <bool ROUTE>
-__device__ int pairs_of_expert(const Moe& a, int e, RouteLds& r, bool publish) {
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint64_t below = (1ull << lane) - 1ull;
-  if constexpr (!ROUTE) {
-    const int pairs = a.tokens * a.topk;
-    for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-      const int v = a.ids[p];
-      r.id[p] = v >= 0 && v < a.experts ? (int16_t)v : (int16_t)-1;
-    }
-    __syncthreads();
-    if (wave == 0) {
-      int n = 0;
-      for (int p0 = 0; p0 < pairs; p0 += 64) {
-        const int p = p0 + lane;
-        bool hit = p < pairs && r.id[p] == e;
-        if (hit)
-          for (int f = p - p % a.topk; f < p; ++f) hit = hit && r.id[f] != e;
-        const uint64_t m = __ballot(hit);
-        if (hit) r.list[n + __popcll(m & below)] = (uint16_t)p;
-        n += __popcll(m);
-      }
-      if (lane == 0) r.count = n;
-    }
-  } else {
-    constexpr int kBatch = 8;
-    for (int t0 = wave; t0 < a.tokens; t0 += kBatch * waves) {
-      uint32_t own[kBatch];
-      int place[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {   // past the last token: the last again, unused
-        own[i] = logit_key(a.logits[(int64_t)min(t0 + i * waves, a.tokens - 1) * a.experts + e]);
-        place[i] = 0;
-      }
-      for (int f0 = 0; f0 < a.experts; f0 += 64) {
-        const int f = min(f0 + lane, a.experts - 1);
-        uint32_t key[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          key[i] = logit_key(a.logits[(int64_t)min(t0 + i * waves, a.tokens - 1) * a.experts + f]);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          place[i] += __popcll(__ballot(f0 + lane < a.experts && (key[i] > own[i] || (key[i] == own[i] && f < e))));
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = t0 + i * waves;
-        if (lane == 0 && t < a.tokens) {
-          r.place[t] = (uint8_t)min(place[i], 255);
-          if (publish && place[i] < a.topk) a.ids[t * a.topk + place[i]] = e;
-        }
-      }
-    }
-    __syncthreads();
-    if (wave == 0) {
-      const int place = lane < a.tokens ? r.place[lane] : 255;
-      const bool hit = place < a.topk;
+__device__ int pairs_of_expert(const Moe& a, int e, RouteLds& r) {
+  const int lane = threadIdx.x & 63, pairs = a.tokens * a.topk;
+  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
+    const int v = a.ids[p];
+    r.id[p] = v >= 0 && v < a.experts ? (int16_t)v : (int16_t)-1;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    int n = 0;
+    for (int p0 = 0; p0 < pairs; p0 += 64) {
+      const int p = p0 + lane;
+      bool hit = p < pairs && r.id[p] == e;
+      if (hit)
+        for (int f = p - p % a.topk; f < p; ++f) hit = hit && r.id[f] != e;
       const uint64_t m = __ballot(hit);
-      if (hit) r.list[__popcll(m & below)] = (uint16_t)(lane * a.topk + place);
-      if (lane == 0) r.count = __popcll(m);
+      if (hit) r.list[n + __popcll(m & ((1ull << lane) - 1ull))] = (uint16_t)p;
+      n += __popcll(m);
     }
+    if (lane == 0) r.count = n;
   }
   __syncthreads();
   return __builtin_amdgcn_readfirstlane(r.count);
 }
 
-// Workgroup column -> expert.  With at least as many choices as experts there is a column per
-// expert; with fewer there is one per choice, and the one that holds an expert's first choice
-// takes it (the caller compares).  -1: nothing to do.
-template <bool ROUTE>
-__device__ int expert_of_slot(const Moe& a, int slot, RouteLds& r) {
-  if (a.slots == a.experts) return slot;
-  if constexpr (!ROUTE) {
-    const int e = a.ids[slot];
-    return e >= 0 && e < a.experts ? e : -1;
-  } else {
-    const int t = slot / a.topk, want = slot % a.topk;
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
-      r.key[e] = logit_key(a.logits[(int64_t)t * a.experts + e]);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
-      const uint32_t own = r.key[e];
-      int place = 0;
+// The single token's choice number `want`: the place of an expert among the logits is the number of
+// larger ones, ties to the lower index.
+__device__ int choice_of_one(const Moe& a, int want, RouteLds& r) {
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) r.key[e] = logit_key(a.logits[e]);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+    const uint32_t own = r.key[e];
+    int place = 0;
 #pragma unroll 8
-      for (int f = 0; f < a.experts; ++f) {
-        const uint32_t k = r.key[f];
-        place += k > own || (k == own && f < e);
-      }
-      if (place == want) r.found = e;   // places are distinct: exactly one thread
+    for (int f = 0; f < a.experts; ++f) {
+      const uint32_t k = r.key[f];
+      place += k > own || (k == own && f < e);
     }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(r.found);
+    if (place == want) r.found = e;   // places are distinct: exactly one thread
   }
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(r.found);
 }
 
 // Sums of a workgroup's waves on their way to one: [wave][row tile][q][17 columns] of four rows each
@@ -224,15 +206,19 @@ template <int U>
 struct UpWeights {
   u32x4_m w[U][4];
 };
-struct UpRows {   // the lane's row in the first tile; the others are uniform distances away
-  const uint8_t *wc, *ws;
-  int64_t up;   // rows from gate to up
+struct UpRows {
+  const uint8_t *codes, *scales;   // of the first tile's first row; the others are uniform distances away
+  int64_t up;                      // rows from gate to up
+  uint32_t row;                    // the lane's place in a tile's codes, in bytes
+  uint32_t srow;                   // the scales of row lane % 16 of tile lane / 16
   __device__ __forceinline__ int64_t rows(int i) const { return (i & 1 ? 16 : 0) + (i >> 1 ? up : 0); }
 };
 __device__ __forceinline__ UpRows up_rows(const Moe& a, int e, int h0) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int64_t row = (int64_t)e * 2 * a.hidden + h0 + r;
-  return UpRows{a.w13c + row * (a.d / 2) + 16 * q, a.w13s + row * (a.d / 32), a.hidden};
+  const int64_t row = (int64_t)e * 2 * a.hidden + h0;
+  UpRows u{a.w13c + row * (a.d / 2), a.w13s + row * (a.d / 32), a.hidden, (uint32_t)(r * (a.d / 2) + 16 * q), 0};
+  u.srow = (uint32_t)((u.rows(q) + r) * (a.d / 32));
+  return u;
 }
 // First K step of a wave, of W that share d.
 template <int W>
@@ -246,7 +232,7 @@ __device__ __forceinline__ void load_up(const Moe& a, const UpRows& u, int s, in
   for (int k = 0; k < U; ++k)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      d.w[k][i] = *reinterpret_cast<const u32x4_m*>(u.wc + (u.rows(i) * (a.d / 2) + min(s + k, last - 1) * 64));
+      d.w[k][i] = load16(u.codes + (u.rows(i) * (a.d / 2) + min(s + k, last - 1) * 64), u.row);
 }
 
 // Gate and up products for G groups of 16 tokens, and the hidden activations of them.  `ahead`: this
@@ -258,13 +244,12 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int U = up_steps(G);
   const int nk = a.d / 128, first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1);
-  const uint8_t* xc[G];
-  const uint8_t* xs[G];
+  uint32_t xc[G], xs[G];   // the lane's token (64 of 64 K bytes at most)
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int t = list[min(16 * g + r, n - 1)] / a.topk;   // columns past n repeat the last; not stored
-    xc[g] = a.xc + (int64_t)t * a.d + 16 * q;
-    xs[g] = a.xs + (int64_t)t * (a.d / 32);
+    const uint32_t t = (uint32_t)list[min(16 * g + r, n - 1)] / (uint32_t)a.topk;   // columns past n repeat the last; not stored
+    xc[g] = t * (uint32_t)a.d + 16 * q;
+    xs[g] = t * (uint32_t)(a.d / 32);
   }
   v4f_m acc[4][G];
 #pragma unroll
@@ -272,11 +257,10 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[i][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = first; s < last; s += 4) {
-    u32x4_m sw[4], sx[G];
+    const u32x4_m sw = scale_words(rows.scales, rows.srow, s, nk);   // the four tiles' at once
+    u32x4_m sx[G];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sw[i] = scale_words(rows.ws + rows.rows(i) * (a.d / 32), s, nk);
-#pragma unroll
-    for (int g = 0; g < G; ++g) sx[g] = scale_words(xs[g], s, nk);
+    for (int g = 0; g < G; ++g) sx[g] = scale_words(a.xs, xs[g], s, nk);
 #pragma unroll
     for (int h = 0; h < 4; h += U) {
       if (s + h >= last) break;
@@ -285,19 +269,21 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
       for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-          const uint8_t* p = xc[g] + min(s + h + k, last - 1) * 128;
-          xl[k][g] = *reinterpret_cast<const u32x4_m*>(p);
-          xh[k][g] = *reinterpret_cast<const u32x4_m*>(p + 64);
+          const uint8_t* p = a.xc + min(s + h + k, last - 1) * 128;
+          xl[k][g] = load16(p, xc[g]);
+          xh[k][g] = load16(p + 64, xc[g]);
         }
       if (s + h > first) load_up<U>(a, rows, s + h, last, ahead);
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         if (s + h + k >= last) break;
+        uint32_t tile[4];
+        spread4(sw[h + k], tile);
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[i][g] = mma_w4x8(frag4(ahead.w[k][i]), frag8(xl[k][g], xh[k][g]), acc[i][g], sw[i][h + k] >> (8 * q),
+            acc[i][g] = mma_w4x8(frag4(ahead.w[k][i]), frag8(xl[k][g], xh[k][g]), acc[i][g], tile[i] >> (8 * q),
                                  sx[g][h + k] >> (8 * q));
       }
     }
@@ -338,6 +324,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 }
 
 // Grid: hidden / 32 tiles x slots.  G: groups of 16 tokens per pass over the expert's weights.
+// ROUTE: one token, whose choices come from the logits and are written to a.ids.
 template <int G, int W, bool ROUTE>
 __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
   __shared__ UpSums sums[W];
@@ -348,16 +335,22 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
     a.arrived[i] = 0;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1), h0 = blockIdx.x * 32;
-  const int e = expert_of_slot<ROUTE>(a, blockIdx.y, r);
-  if (e < 0) return;
+  // Workgroup column -> expert.  With at least as many choices as experts there is a column per
+  // expert; with fewer there is one per choice, and the one that holds an expert's first choice
+  // takes it.
+  const bool by_choice = a.slots != a.experts;
+  int e = blockIdx.y;
+  if constexpr (ROUTE) e = choice_of_one(a, blockIdx.y, r);
+  else if (by_choice) e = a.ids[blockIdx.y];
+  if (e < 0 || e >= a.experts) return;
   // The first weights travel while the expert's tokens are looked up, where few workgroups turn
   // out to have none (2 choices per expert: one in seven).
-  const bool early = a.tokens * a.topk >= 2 * a.experts;
+  const bool early = ROUTE || a.tokens * a.topk >= 2 * a.experts;
   const UpRows rows = up_rows(a, e, h0);
   UpWeights<up_steps(G)> ahead;
   if (early && first < last) load_up<up_steps(G)>(a, rows, first, last, ahead);
   int n;
-  if (ROUTE && a.tokens == 1 && a.slots != a.experts) {   // one token: its choice is the whole list
+  if constexpr (ROUTE) {
     if (threadIdx.x == 0) {
       r.list[0] = (uint16_t)blockIdx.y;
       if (blockIdx.x == 0) a.ids[blockIdx.y] = e;
@@ -365,9 +358,9 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
     __syncthreads();
     n = 1;
   } else {
-    n = pairs_of_expert<ROUTE>(a, e, r, blockIdx.x == 0);
+    n = pairs_of_expert(a, e, r);
+    if (n == 0 || (by_choice && r.list[0] != blockIdx.y)) return;
   }
-  if (n == 0 || (a.slots != a.experts && r.list[0] != blockIdx.y)) return;
   for (int i = 0; i < n; i += 16 * G) {
     if ((i > 0 || !early) && first < last) load_up<up_steps(G)>(a, rows, first, last, ahead);
     up_tiles<G, W>(a, rows, h0, r.list + i, min(n - i, 16 * G), ahead, sums);
@@ -385,15 +378,13 @@ struct DownUnit {
 };
 __device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, int s1, DownUnit& d) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int64_t row = (int64_t)e * a.d + n0 + r;
-  const uint8_t* wc = a.w2c + row * (a.hidden / 2) + 16 * q;
-  const uint8_t* ws = a.w2s + row * (a.hidden / 32);
+  const int64_t row = (int64_t)e * a.d + n0;
+  const uint8_t* wc = a.w2c + row * (a.hidden / 2);
+  const uint32_t at = (uint32_t)(r * (a.hidden / 2) + 16 * q);
 #pragma unroll
-  for (int u = 0; u < kDownSteps; ++u) {   // past the unit's end the last step again, unused
-    const int at = min(s0 + u, s1 - 1);
-    d.w[u] = *reinterpret_cast<const u32x4_m*>(wc + at * 64);
-  }
-  d.sw = scale_words(ws, s0, a.hidden / 128);
+  for (int u = 0; u < kDownSteps; ++u)   // past the unit's end the last step again, unused
+    d.w[u] = load16(wc + min(s0 + u, s1 - 1) * 64, at);
+  d.sw = scale_words(a.w2s + row * (a.hidden / 32), (uint32_t)(r * (a.hidden / 32)), s0, a.hidden / 128);
 }
 
 // The unit's product with its expert's hidden rows, added with the pairs' weights to this wave's
@@ -402,28 +393,26 @@ template <int G>
 __device__ __forceinline__ void down_unit(const Moe& a, const DownUnit& d, int s0, int s1, const uint16_t* list, int n,
                                           const float* wts, float (*out)[16]) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const uint8_t* hc[G];
-  const uint8_t* hs[G];
+  uint32_t hc[G], hs[G];   // the lane's hidden row (1024 of 64 K bytes at most)
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const int64_t p = list[min(16 * g + r, n - 1)];
-    hc[g] = a.hc + p * a.hidden + 16 * q;
-    hs[g] = a.hs + p * (a.hidden / 32);
+    const uint32_t p = list[min(16 * g + r, n - 1)];
+    hc[g] = p * (uint32_t)a.hidden + 16 * q;
+    hs[g] = p * (uint32_t)(a.hidden / 32);
   }
   v4f_m acc[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc[g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
   u32x4_m sh[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) sh[g] = scale_words(hs[g], s0, a.hidden / 128);
+  for (int g = 0; g < G; ++g) sh[g] = scale_words(a.hs, hs[g], s0, a.hidden / 128);
 #pragma unroll
   for (int u = 0; u < kDownSteps; ++u) {
     if (s0 + u >= s1) break;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const uint8_t* p = hc[g] + (s0 + u) * 128;
-      const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
-      acc[g] = mma_w4x8(frag4(d.w[u]), frag8(lo, hi), acc[g], d.sw[u] >> (8 * q), sh[g][u] >> (8 * q));
+      const uint8_t* p = a.hc + (s0 + u) * 128;
+      acc[g] = mma_w4x8(frag4(d.w[u]), frag8(load16(p, hc[g]), load16(p + 64, hc[g])), acc[g], d.sw[u] >> (8 * q), sh[g][u] >> (8 * q));
     }
   }
 #pragma unroll
@@ -446,7 +435,8 @@ __device__ __forceinline__ void store_y(const Moe& a, int t, int col, float v0, 
 // in turn to the waves of all the splits; each wave adds into sums of its own.  A workgroup joins
 // its waves in order; with several splits the last workgroup of a row tile to finish joins them in
 // order (their number is fixed by the shape), so the sums do not depend on who that is.
-// TOK: token capacity; G: groups of 16 tokens per pass over an expert's weights.
+// TOK: token capacity; G: groups of 16 tokens per pass over an expert's weights; ROUTE: one token, whose
+// weights come from its choices' logits and are written to a.weights.
 template <int TOK, int G, bool ROUTE, bool BF16OUT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   constexpr int kPairs = 16 * TOK;
@@ -467,7 +457,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   const auto unit_steps = [&](int active) { return min(max(active * nk / workers, 1), kDownSteps); };
   // One token: its choices are the units' experts as they stand (a repeated one is two units), so
   // nothing is sorted and the first weights travel while the rest is set up.
-  const bool single = TOK == 16 && a.tokens == 1;
+  const bool single = ROUTE || (TOK == 16 && a.tokens == 1);
   if (single) {
     const int per = unit_steps(a.topk), parts = (nk + per - 1) / per, s0 = u % parts * per;
     const int e = u < a.topk * parts ? a.ids[u / parts] : -1;
@@ -478,7 +468,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   float w = 0.0f;
   if (tid < pairs) {
     e = a.ids[tid];
-    if constexpr (ROUTE) w = a.logits[(int64_t)(tid / a.topk) * a.experts + e];
+    if constexpr (ROUTE) w = a.logits[e];
     else w = a.weights[tid];
     if (e < 0 || e >= a.experts) e = -1;
     id[tid] = (int16_t)e;
@@ -609,10 +599,10 @@ int groups(const Moe& a) {
 
 template <int G, bool ROUTE>
 void run_up(const Moe& a, hipStream_t st) {
-  // waves per workgroup: four K steps each, where there are as many (with eight for d = 2048, half
-  // of a workgroup's time went into its set-up and joins)
+  // Waves per workgroup: eight where there are too few workgroups to fill the GPU with four (one
+  // token, 4 of 64 experts of 2048 x 1024: 8.9 against 10.1 us; 64 tokens, 8 of 64: 48.2 against 43.5).
   const dim3 grid(a.hidden / 32, a.slots);
-  if (a.d >= 4096) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
+  if ((int64_t)grid.x * grid.y <= 2 * kCus) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
   else k_moe_up<G, 4, ROUTE><<<grid, 256, 0, st>>>(a);
 }
 
@@ -623,16 +613,15 @@ void run_down(const Moe& a, bool bf16_out, hipStream_t st) {
   else k_moe_down<TOK, G, ROUTE, false><<<grid, 64 * kDownWaves, 0, st>>>(a);
 }
 
-template <bool ROUTE>
 void run(const Moe& a, bool bf16_out, hipStream_t st) {
   const int g = groups(a);
-  if (g == 1) run_up<1, ROUTE>(a, st);
-  else if (g == 2) run_up<2, ROUTE>(a, st);
-  else run_up<4, ROUTE>(a, st);
-  if (a.tokens <= 16) run_down<16, 1, ROUTE>(a, bf16_out, st);
-  else if (g == 1) run_down<64, 1, ROUTE>(a, bf16_out, st);
-  else if (g == 2) run_down<64, 2, ROUTE>(a, bf16_out, st);
-  else run_down<64, 4, ROUTE>(a, bf16_out, st);
+  if (g == 1) run_up<1, false>(a, st);
+  else if (g == 2) run_up<2, false>(a, st);
+  else run_up<4, false>(a, st);
+  if (a.tokens <= 16) run_down<16, 1, false>(a, bf16_out, st);
+  else if (g == 1) run_down<64, 1, false>(a, bf16_out, st);
+  else if (g == 2) run_down<64, 2, false>(a, bf16_out, st);
+  else run_down<64, 4, false>(a, bf16_out, st);
 }
 
 // Workgroups that share a row tile of the down product: as many as there are CUs for each tile, but
@@ -684,7 +673,7 @@ void launch_moe(const MoeArgs& m, hipStream_t st) {
   a.partial = reinterpret_cast<float*>(scratch + l.partial);
   a.arrived = reinterpret_cast<int*>(scratch + l.arrived);
   if (!m.router_w) {
-    run<false>(a, m.bf16_out, st);
+    run(a, m.bf16_out, st);
     return;
   }
   const dim3 grid((m.experts + 15) / 16, (m.tokens + 15) / 16);
@@ -695,7 +684,13 @@ void launch_moe(const MoeArgs& m, hipStream_t st) {
   else
     k_moe_logits<float><<<grid, 1024, 0, st>>>(static_cast<const float*>(m.router_x),
                                                static_cast<const float*>(m.router_w), m.tokens, m.d, m.experts, logits);
-  run<true>(a, m.bf16_out, st);
+  if (m.tokens == 1 && m.topk < m.experts) {   // the expert kernels read the logits themselves: a launch less
+    run_up<1, true>(a, st);
+    run_down<16, 1, true>(a, m.bf16_out, st);
+    return;
+  }
+  k_moe_topk<<<m.tokens, 64, 0, st>>>(logits, m.experts, m.topk, m.ids, m.weights);
+  run(a, m.bf16_out, st);
 }
 
 }  // namespace fp4q

@@ -54,11 +54,12 @@ __device__ __forceinline__ v16f_m mma_x8w4_hi(v8i_m x, v8i_m w, v16f_m acc, uint
 // Scale words s .. s + 3 of a row of n words (four blocks each, little end first), in one load
 // where the row has four: a load of one word per row costs the address unit as much as 16 bytes
 // per lane.  Words past the row's end repeat its last.
-__device__ __forceinline__ u32x4_m scale_words(const uint8_t* row, int s, int n) {
+// The row is at `base` (the same for the wave) + `row` bytes.
+__device__ __forceinline__ u32x4_m scale_words(const uint8_t* base, uint32_t row, int s, int n) {
   u32x4_m v;
   if (n >= 4) {
     const int at = min(s, n - 4), down = min(s - at, 3);
-    v = *reinterpret_cast<const u32x4_w*>(row + 4 * at);
+    v = *reinterpret_cast<const u32x4_w*>(base + 4 * at + row);
     const uint32_t one = 0u - (uint32_t)(down & 1), two = 0u - (uint32_t)(down >> 1);
 #pragma unroll
     for (int j = 0; j < 3; ++j) v[j] = (v[j] & ~one) | (v[j + 1] & one);
@@ -66,9 +67,24 @@ __device__ __forceinline__ u32x4_m scale_words(const uint8_t* row, int s, int n)
     for (int j = 0; j < 2; ++j) v[j] = (v[j] & ~two) | (v[j + 2] & two);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(row + 4 * min(s + j, n - 1));
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(base + 4 * min(s + j, n - 1) + row);
   }
   return v;
+}
+
+// From a register whose lanes 16 i .. 16 i + 15 belong to row tile i, four registers with tile i's
+// lanes in all four groups of 16: v_permlane16_swap exchanges the odd groups of its first operand
+// with the even groups of its second, v_permlane32_swap the upper half with the lower half.
+__device__ __forceinline__ void spread4(uint32_t w, uint32_t (&o)[4]) {
+  const auto a = __builtin_amdgcn_permlane16_swap(w, w, false, false);         // 0 0 2 2 and 1 1 3 3
+  const auto e = __builtin_amdgcn_permlane32_swap(a[0], a[0], false, false);   // 0 0 0 0 and 2 2 2 2
+  const auto f = __builtin_amdgcn_permlane32_swap(a[1], a[1], false, false);
+  o[0] = e[0], o[2] = e[1], o[1] = f[0], o[3] = f[1];
+}
+
+// 16 bytes at `base` (the same for the wave) + `off`: the address costs a lane one register.
+__device__ __forceinline__ u32x4_m load16(const uint8_t* base, uint32_t off) {
+  return *reinterpret_cast<const u32x4_m*>(base + off);
 }
 
 // Two fp32 values to packed bf16, nearest even (v_cvt_pk_bf16_f32; NaN stays NaN).
