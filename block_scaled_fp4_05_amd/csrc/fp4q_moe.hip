@@ -28,10 +28,19 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 }
 
 // -----------------------------------------------------------------------------------------
-// Router logits: 16 experts x 16 tokens per workgroup, sixteen waves that split d and join in
-// LDS in wave order.  fp32 inputs go through the fp32 matrix instruction, so nothing is rounded
-// but the sums.
+// Router logits: 16 experts x 16 tokens per workgroup, over a quarter of d that its four waves split
+// and join in LDS in wave order; whoever reads a logit adds its quarters up (logit_of).  (One
+// workgroup over all of d: 10.2 us for 64 tokens, 32 experts and d = 4096, all of it the address
+// unit of the few CUs that had a workgroup.)  fp32 inputs go through the fp32 matrix instruction,
+// so nothing is rounded but the sums.
 // -----------------------------------------------------------------------------------------
+constexpr int kQuarters = 4;
+
+// Logit at `at` = token * experts + expert of the quarters' arrays of n.
+__device__ __forceinline__ float logit_of(const float* part, int at, int n) {
+  return ((part[at] + part[at + n]) + part[at + 2 * n]) + part[at + 3 * n];
+}
+
 typedef __bf16 bf16x8_m __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ v4f_m router_mma(u32x4_m w, u32x4_m x, v4f_m acc, const uint16_t*) {
@@ -46,16 +55,17 @@ __device__ __forceinline__ v4f_m router_mma(u32x4_m w, u32x4_m x, v4f_m acc, con
 }
 
 template <typename T>
-__global__ __launch_bounds__(1024) void k_moe_logits(const T* __restrict__ x, const T* __restrict__ w, int tokens,
+__global__ __launch_bounds__(256) void k_moe_logits(const T* __restrict__ x, const T* __restrict__ w, int tokens,
                                                      int d, int experts, float* __restrict__ logits) {
-  __shared__ v4f_m sums[16][64];
+  __shared__ v4f_m sums[4][64];
   constexpr int N = 16 / (int)sizeof(T);   // elements per lane and load; a step is 4 N
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
   const T* wp = w + (int64_t)min(e0 + r, experts - 1) * d + N * q;
   const T* xp = x + (int64_t)min(t0 + r, tokens - 1) * d + N * q;
-  const int steps = d / (4 * N), first = steps * wave / 16, last = steps * (wave + 1) / 16;
+  const int steps = d / (4 * N), share = 4 * blockIdx.z + wave;
+  const int first = steps * share / 16, last = steps * (share + 1) / 16;
   v4f_m acc = {0.0f, 0.0f, 0.0f, 0.0f};
   constexpr int U = 4;   // steps whose loads are in flight together; past the end the last one again, unused
   for (int s = first; s < last; s += U) {
@@ -75,11 +85,12 @@ __global__ __launch_bounds__(1024) void k_moe_logits(const T* __restrict__ x, co
   if (threadIdx.x < 64) {
     v4f_m v = sums[0][lane];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) v += sums[i][lane];
+    for (int i = 1; i < 4; ++i) v += sums[i][lane];
+    float* to = logits + (int64_t)blockIdx.z * tokens * experts;
     const int t = t0 + r;   // column: token; rows 4 q ..: experts
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (t < tokens && e0 + 4 * q + i < experts) logits[(int64_t)t * experts + e0 + 4 * q + i] = v[i];
+      if (t < tokens && e0 + 4 * q + i < experts) to[t * experts + e0 + 4 * q + i] = v[i];
   }
 }
 
@@ -88,14 +99,13 @@ __global__ __launch_bounds__(1024) void k_moe_logits(const T* __restrict__ x, co
 __global__ __launch_bounds__(64) void k_moe_topk(const float* __restrict__ logits, int experts, int topk,
                                                  int32_t* __restrict__ ids, float* __restrict__ weights) {
   constexpr int kPerLane = 512 / 64;
-  const int lane = threadIdx.x, t = blockIdx.x;
-  const float* l = logits + (int64_t)t * experts;
+  const int lane = threadIdx.x, t = blockIdx.x, n = gridDim.x * experts;
   // key of an expert: its logit's order above, the complement of its index below; 0: taken or none
   uint64_t key[kPerLane];
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 64 * i;
-    key[i] = e < experts ? ((uint64_t)logit_key(l[e]) << 32) | (uint32_t)~e : 0ull;
+    key[i] = e < experts ? ((uint64_t)logit_key(logit_of(logits, t * experts + e, n)) << 32) | (uint32_t)~e : 0ull;
   }
   int chosen = 0;   // lane j: the j-th choice
   for (int j = 0; j < topk; ++j) {
@@ -112,7 +122,7 @@ __global__ __launch_bounds__(64) void k_moe_topk(const float* __restrict__ logit
     if (lane == j) chosen = (int)~(uint32_t)best;
   }
   // every lane adds the exponentials in the order of the choices
-  const float own = lane < topk ? l[chosen] : 0.0f, top = __shfl(own, 0, 64);
+  const float own = lane < topk ? logit_of(logits, t * experts + chosen, n) : 0.0f, top = __shfl(own, 0, 64);
   const float w = expf(own - top);
   float total = 0.0f;
   for (int j = 0; j < topk; ++j) total += __shfl(w, j, 64);
@@ -131,10 +141,10 @@ struct Moe {
   int slots;                    // workgroup columns of k_moe_up: see there
   int32_t* ids;                 // [tokens][topk]; routing one token, k_moe_up writes them
   float* weights;               // [tokens][topk]; routing one token, k_moe_down writes them
-  const float* logits;          // [experts], routing one token only
+  const float* logits;          // [4][experts], routing one token only
   uint8_t *hc, *hs;             // scratch: MXFP8 hidden rows [tokens * topk][hidden]
   int splits;                   // workgroups per row tile of k_moe_down
-  float* partial;               // scratch: their sums [d / 16][splits][64][16]
+  float* partial;               // scratch: their sums [row tile][splits][64][rows of the tile]
   int* arrived;                 // scratch: how many of a row tile's have finished; k_moe_up clears it
   void* y;
 };
@@ -178,7 +188,7 @@ __device__ int pairs_of_expert(const Moe& a, int e, RouteLds& r) {
 // The single token's choice number `want`: the place of an expert among the logits is the number of
 // larger ones, ties to the lower index.
 __device__ int choice_of_one(const Moe& a, int want, RouteLds& r) {
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) r.key[e] = logit_key(a.logits[e]);
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) r.key[e] = logit_key(logit_of(a.logits, e, a.experts));
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
     const uint32_t own = r.key[e];
@@ -244,13 +254,13 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int U = up_steps(G);
   const int nk = a.d / 128, first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1);
-  uint32_t xc[G], xs[G];   // the lane's token (64 of 64 K bytes at most)
+  // the lane's tokens (64 of 64 K bytes at most; columns past n repeat the last and are not stored),
+  // and the one of group q % G whose scales it loads for all
+  const auto token = [&](int g) { return (uint32_t)list[min(16 * g + r, n - 1)] / (uint32_t)a.topk; };
+  uint32_t xc[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const uint32_t t = (uint32_t)list[min(16 * g + r, n - 1)] / (uint32_t)a.topk;   // columns past n repeat the last; not stored
-    xc[g] = t * (uint32_t)a.d + 16 * q;
-    xs[g] = t * (uint32_t)(a.d / 32);
-  }
+  for (int g = 0; g < G; ++g) xc[g] = token(g) * (uint32_t)a.d + 16 * q;
+  const uint32_t xs = token(q % G) * (uint32_t)(a.d / 32);
   v4f_m acc[4][G];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -258,9 +268,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
     for (int g = 0; g < G; ++g) acc[i][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = first; s < last; s += 4) {
     const u32x4_m sw = scale_words(rows.scales, rows.srow, s, nk);   // the four tiles' at once
-    u32x4_m sx[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) sx[g] = scale_words(a.xs, xs[g], s, nk);
+    const u32x4_m sx = scale_words(a.xs, xs, s, nk);
 #pragma unroll
     for (int h = 0; h < 4; h += U) {
       if (s + h >= last) break;
@@ -277,14 +285,15 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 #pragma unroll
       for (int k = 0; k < U; ++k) {
         if (s + h + k >= last) break;
-        uint32_t tile[4];
-        spread4(sw[h + k], tile);
+        uint32_t tile[4], group[G];
+        spread(sw[h + k], tile);
+        spread(sx[h + k], group);
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             acc[i][g] = mma_w4x8(frag4(ahead.w[k][i]), frag8(xl[k][g], xh[k][g]), acc[i][g], tile[i] >> (8 * q),
-                                 sx[g][h + k] >> (8 * q));
+                                 group[g] >> (8 * q));
       }
     }
   }
@@ -368,59 +377,71 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
 }
 
 constexpr int kDownWaves = 16;
-constexpr int kDownSteps = 4;   // most K steps of a unit of work
+// Most K steps of a unit of work, all of whose weights are in flight together: fewer where the sums
+// of four groups need the registers.
+constexpr int down_steps(int g) { return g == 4 ? 2 : 4; }
 constexpr int kNone = 0xFFFF;   // no expert
 
-// Weights of one unit of work: up to kDownSteps K steps of one expert's 16 output rows.
+// Weights of one unit of work: up to ST K steps of one expert's RT tiles of 16 output rows.
+template <int RT, int ST>
 struct DownUnit {
-  u32x4_m w[kDownSteps];
-  u32x4_m sw;
+  u32x4_m w[ST][RT];
+  u32x4_m sw;   // of row lane % 16 of tile lane / 16 % RT
 };
-__device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, int s1, DownUnit& d) {
+template <int RT, int ST>
+__device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, int s1, DownUnit<RT, ST>& d) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int64_t row = (int64_t)e * a.d + n0;
-  const uint8_t* wc = a.w2c + row * (a.hidden / 2);
-  const uint32_t at = (uint32_t)(r * (a.hidden / 2) + 16 * q);
+  const int64_t row = (int64_t)e * a.d + n0, cols = a.hidden / 2;
+  const uint8_t* wc = a.w2c + row * cols;
+  const uint32_t at = (uint32_t)(r * cols + 16 * q);
 #pragma unroll
-  for (int u = 0; u < kDownSteps; ++u)   // past the unit's end the last step again, unused
-    d.w[u] = load16(wc + min(s0 + u, s1 - 1) * 64, at);
-  d.sw = scale_words(a.w2s + row * (a.hidden / 32), (uint32_t)(r * (a.hidden / 32)), s0, a.hidden / 128);
+  for (int u = 0; u < ST; ++u)   // past the unit's end the last step again, unused
+#pragma unroll
+    for (int i = 0; i < RT; ++i) d.w[u][i] = load16(wc + (16 * i * cols + min(s0 + u, s1 - 1) * 64), at);
+  d.sw = scale_words(a.w2s + row * (a.hidden / 32), (uint32_t)((16 * (q % RT) + r) * (a.hidden / 32)), s0, a.hidden / 128);
 }
 
 // The unit's product with its expert's hidden rows, added with the pairs' weights to this wave's
-// own sums (out[token][16]).
-template <int G>
-__device__ __forceinline__ void down_unit(const Moe& a, const DownUnit& d, int s0, int s1, const uint16_t* list, int n,
-                                          const float* wts, float (*out)[16]) {
+// own sums (out[token][16 RT]).
+template <int G, int RT, int ST>
+__device__ __forceinline__ void down_unit(const Moe& a, const DownUnit<RT, ST>& d, int s0, int s1, const uint16_t* list,
+                                          int n, const float* wts, float (*out)[16 * RT]) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  uint32_t hc[G], hs[G];   // the lane's hidden row (1024 of 64 K bytes at most)
+  // the lane's hidden rows (1024 of 64 K bytes at most), and the one whose scales it loads for all
+  uint32_t hc[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const uint32_t p = list[min(16 * g + r, n - 1)];
-    hc[g] = p * (uint32_t)a.hidden + 16 * q;
-    hs[g] = p * (uint32_t)(a.hidden / 32);
-  }
-  v4f_m acc[G];
+  for (int g = 0; g < G; ++g) hc[g] = list[min(16 * g + r, n - 1)] * (uint32_t)a.hidden + 16 * q;
+  const u32x4_m sh =
+      scale_words(a.hs, list[min(16 * (q % G) + r, n - 1)] * (uint32_t)(a.hidden / 32), s0, a.hidden / 128);
+  v4f_m acc[RT][G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) acc[g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
-  u32x4_m sh[G];
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-  for (int g = 0; g < G; ++g) sh[g] = scale_words(a.hs, hs[g], s0, a.hidden / 128);
+    for (int g = 0; g < G; ++g) acc[i][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int u = 0; u < kDownSteps; ++u) {
+  for (int u = 0; u < ST; ++u) {
     if (s0 + u >= s1) break;
+    uint32_t tile[RT], group[G];
+    spread(d.sw[u], tile);
+    spread(sh[u], group);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint8_t* p = a.hc + (s0 + u) * 128;
-      acc[g] = mma_w4x8(frag4(d.w[u]), frag8(load16(p, hc[g]), load16(p + 64, hc[g])), acc[g], d.sw[u] >> (8 * q), sh[g][u] >> (8 * q));
+      const v8i_m h = frag8(load16(p, hc[g]), load16(p + 64, hc[g]));
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        acc[i][g] = mma_w4x8(frag4(d.w[u][i]), h, acc[i][g], tile[i] >> (8 * q), group[g] >> (8 * q));
     }
   }
 #pragma unroll
   for (int g = 0; g < G; ++g)
     if (16 * g + r < n) {
       const int p = list[16 * g + r];
-      v4f_m* o = reinterpret_cast<v4f_m*>(&out[p / a.topk][4 * q]);
-      *o += wts[p] * acc[g];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        v4f_m* o = reinterpret_cast<v4f_m*>(&out[p / a.topk][16 * i + 4 * q]);
+        *o += wts[p] * acc[i][g];
+      }
     }
 }
 
@@ -431,16 +452,17 @@ __device__ __forceinline__ void store_y(const Moe& a, int t, int col, float v0, 
   else *reinterpret_cast<f32x2_m*>(static_cast<float*>(a.y) + at) = f32x2_m{v0, v1};
 }
 
-// Grid: d / 16 x splits.  Work units are (used expert in rising order, range of its K steps), dealt
+// Grid: d / (16 RT) x splits.  Work units are (used expert in rising order, range of its K steps), dealt
 // in turn to the waves of all the splits; each wave adds into sums of its own.  A workgroup joins
 // its waves in order; with several splits the last workgroup of a row tile to finish joins them in
 // order (their number is fixed by the shape), so the sums do not depend on who that is.
 // TOK: token capacity; G: groups of 16 tokens per pass over an expert's weights; ROUTE: one token, whose
 // weights come from its choices' logits and are written to a.weights.
-template <int TOK, int G, bool ROUTE, bool BF16OUT>
+template <int TOK, int G, int RT, bool ROUTE, bool BF16OUT>
 __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   constexpr int kPairs = 16 * TOK;
-  __shared__ __align__(16) float out[kDownWaves][TOK][16];
+  constexpr int kRows = 16 * RT, ST = down_steps(G);
+  __shared__ __align__(16) float out[kDownWaves][TOK][kRows];
   __shared__ int16_t id[kPairs];
   __shared__ float wts[kPairs];
   __shared__ int count[512];            // by expert: pairs, then the first place in `sorted`
@@ -449,12 +471,12 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   __shared__ int used, last;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = blockIdx.x * 16, pairs = a.tokens * a.topk;
+  const int n0 = blockIdx.x * kRows, pairs = a.tokens * a.topk;
   // K steps per unit: enough units for every wave, at most what one unit's registers hold
   const int nk = a.hidden / 128, workers = kDownWaves * gridDim.y;
-  DownUnit now, next;
+  DownUnit<RT, ST> now, next;
   int u = wave * gridDim.y + blockIdx.y;
-  const auto unit_steps = [&](int active) { return min(max(active * nk / workers, 1), kDownSteps); };
+  const auto unit_steps = [&](int active) { return min(max(active * nk / workers, 1), ST); };
   // One token: its choices are the units' experts as they stand (a repeated one is two units), so
   // nothing is sorted and the first weights travel while the rest is set up.
   const bool single = ROUTE || (TOK == 16 && a.tokens == 1);
@@ -468,14 +490,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   float w = 0.0f;
   if (tid < pairs) {
     e = a.ids[tid];
-    if constexpr (ROUTE) w = a.logits[e];
+    if constexpr (ROUTE) w = logit_of(a.logits, e, a.experts);
     else w = a.weights[tid];
     if (e < 0 || e >= a.experts) e = -1;
     id[tid] = (int16_t)e;
     wts[tid] = w;
   }
   if (tid < 512) count[tid] = 0;
-  for (int i = tid; i < kDownWaves * TOK * 4; i += 64 * kDownWaves)
+  for (int i = tid; i < kDownWaves * TOK * kRows / 4; i += 64 * kDownWaves)
     reinterpret_cast<v4f_m*>(out)[i] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
   __syncthreads();
   int place = 0;
@@ -537,7 +559,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   const int active = __builtin_amdgcn_readfirstlane(used);
   const int per = unit_steps(active), parts = (nk + per - 1) / per;
   const int units = active * parts;
-  const auto load = [&](int u, DownUnit& d) {
+  const auto load = [&](int u, DownUnit<RT, ST>& d) {
     const int s0 = u % parts * per, e = __builtin_amdgcn_readfirstlane(expert[u / parts]);
     if (e != kNone) load_unit(a, e, n0, s0, min(s0 + per, nk), d);
   };
@@ -549,15 +571,16 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
     const int n = __builtin_amdgcn_readfirstlane(start[u / parts + 1]) - first;
     const bool none = __builtin_amdgcn_readfirstlane(expert[u / parts]) == kNone;
     for (int i = 0; i < n && !none; i += 16 * G)
-      down_unit<G>(a, now, s0, s1, sorted + first + i, min(n - i, 16 * G), wts, out[wave]);
+      down_unit<G, RT, ST>(a, now, s0, s1, sorted + first + i, min(n - i, 16 * G), wts, out[wave]);
     now = next;
   }
   __syncthreads();
   const int splits = gridDim.y;
-  float* part = a.partial + ((int64_t)blockIdx.x * splits + blockIdx.y) * (kMaxTokens * 16);
-  const float* parts0 = a.partial + (int64_t)blockIdx.x * splits * (kMaxTokens * 16);
-  for (int i = tid; i < a.tokens * 8; i += 64 * kDownWaves) {   // two neighbouring columns per thread
-    const int t = i >> 3, c = (i & 7) * 2;
+  constexpr int kPer = kRows / 2;   // two neighbouring columns per thread
+  float* joined = a.partial + (int64_t)blockIdx.x * splits * (kMaxTokens * kRows);
+  float* part = joined + blockIdx.y * (kMaxTokens * kRows);
+  for (int i = tid; i < a.tokens * kPer; i += 64 * kDownWaves) {
+    const int t = i / kPer, c = i % kPer * 2;
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int v = 0; v < kDownWaves; ++v) s0 += out[v][t][c], s1 += out[v][t][c + 1];
@@ -579,16 +602,20 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
     last = __hip_atomic_fetch_add(&a.arrived[blockIdx.x], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
   __syncthreads();
   if (!last) return;
-  for (int i = tid; i < a.tokens * 8; i += 64 * kDownWaves) {
+  for (int i = tid; i < a.tokens * kPer; i += 64 * kDownWaves) {
     float s0 = 0.0f, s1 = 0.0f;
     for (int v = 0; v < splits; ++v) {
-      const float* p = parts0 + v * (kMaxTokens * 16) + 2 * i;
+      const float* p = joined + v * (kMaxTokens * kRows) + 2 * i;
       s0 += __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       s1 += __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    store_y<BF16OUT>(a, i >> 3, n0 + (i & 7) * 2, s0, s1);
+    store_y<BF16OUT>(a, i / kPer, n0 + i % kPer * 2, s0, s1);
   }
 }
+
+// Row tiles per workgroup of the down product: with many tokens two, so that each hidden fragment
+// loaded is multiplied twice.
+constexpr int row_tiles(int tokens) { return tokens <= 16 ? 1 : 2; }
 
 // Groups of 16 tokens that a pass over an expert's weights takes: from the mean number of tokens
 // per expert, so that a second pass (from L2) is rare, with as few registers as that allows.
@@ -606,11 +633,11 @@ void run_up(const Moe& a, hipStream_t st) {
   else k_moe_up<G, 4, ROUTE><<<grid, 256, 0, st>>>(a);
 }
 
-template <int TOK, int G, bool ROUTE>
+template <int TOK, int G, int RT, bool ROUTE>
 void run_down(const Moe& a, bool bf16_out, hipStream_t st) {
-  const dim3 grid(a.d / 16, a.splits);
-  if (bf16_out) k_moe_down<TOK, G, ROUTE, true><<<grid, 64 * kDownWaves, 0, st>>>(a);
-  else k_moe_down<TOK, G, ROUTE, false><<<grid, 64 * kDownWaves, 0, st>>>(a);
+  const dim3 grid(a.d / (16 * RT), a.splits);
+  if (bf16_out) k_moe_down<TOK, G, RT, ROUTE, true><<<grid, 64 * kDownWaves, 0, st>>>(a);
+  else k_moe_down<TOK, G, RT, ROUTE, false><<<grid, 64 * kDownWaves, 0, st>>>(a);
 }
 
 void run(const Moe& a, bool bf16_out, hipStream_t st) {
@@ -618,17 +645,17 @@ void run(const Moe& a, bool bf16_out, hipStream_t st) {
   if (g == 1) run_up<1, false>(a, st);
   else if (g == 2) run_up<2, false>(a, st);
   else run_up<4, false>(a, st);
-  if (a.tokens <= 16) run_down<16, 1, false>(a, bf16_out, st);
-  else if (g == 1) run_down<64, 1, false>(a, bf16_out, st);
-  else if (g == 2) run_down<64, 2, false>(a, bf16_out, st);
-  else run_down<64, 4, false>(a, bf16_out, st);
+  if (a.tokens <= 16) run_down<16, 1, row_tiles(16), false>(a, bf16_out, st);
+  else if (g == 1) run_down<64, 1, row_tiles(64), false>(a, bf16_out, st);
+  else if (g == 2) run_down<64, 2, row_tiles(64), false>(a, bf16_out, st);
+  else run_down<64, 4, row_tiles(64), false>(a, bf16_out, st);
 }
 
 // Workgroups that share a row tile of the down product: as many as there are CUs for each tile, but
 // no more than leaves a wave a full unit of work (the join takes 2 us), up to eight.
 int down_splits(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
   const int64_t used = tokens * topk < experts ? tokens * topk : experts;
-  const int64_t cus = kCus / (d / 16), work = used * (hidden / 128) / (kDownSteps * kDownWaves);
+  const int64_t cus = kCus / (d / (16 * row_tiles(tokens))), work = used * (hidden / 128) / (4 * kDownWaves);
   const int64_t s = cus < work ? cus : work;
   return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
@@ -642,11 +669,11 @@ struct Layout {
 Layout layout(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk) {
   Layout l;
   l.logits = 0;
-  l.codes = up16(tokens * experts * 4);
+  l.codes = up16(kQuarters * tokens * experts * 4);
   l.scales = l.codes + up16(tokens * topk * hidden);
   l.partial = l.scales + up16(tokens * topk * (hidden / 32));
   const int splits = down_splits(tokens, d, hidden, experts, topk);
-  l.arrived = l.partial + (splits > 1 ? d / 16 * splits * kMaxTokens * 16 * 4 : 0);
+  l.arrived = l.partial + (splits > 1 ? d * splits * kMaxTokens * 4 : 0);
   l.bytes = l.arrived + up16(d / 16 * 4);
   return l;
 }
@@ -676,17 +703,17 @@ void launch_moe(const MoeArgs& m, hipStream_t st) {
     run(a, m.bf16_out, st);
     return;
   }
-  const dim3 grid((m.experts + 15) / 16, (m.tokens + 15) / 16);
+  const dim3 grid((m.experts + 15) / 16, (m.tokens + 15) / 16, kQuarters);
   if (m.router_bf16)
-    k_moe_logits<uint16_t><<<grid, 1024, 0, st>>>(static_cast<const uint16_t*>(m.router_x),
+    k_moe_logits<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(m.router_x),
                                                   static_cast<const uint16_t*>(m.router_w), m.tokens, m.d, m.experts,
                                                   logits);
   else
-    k_moe_logits<float><<<grid, 1024, 0, st>>>(static_cast<const float*>(m.router_x),
+    k_moe_logits<float><<<grid, 256, 0, st>>>(static_cast<const float*>(m.router_x),
                                                static_cast<const float*>(m.router_w), m.tokens, m.d, m.experts, logits);
   if (m.tokens == 1 && m.topk < m.experts) {   // the expert kernels read the logits themselves: a launch less
     run_up<1, true>(a, st);
-    run_down<16, 1, true>(a, m.bf16_out, st);
+    run_down<16, 1, row_tiles(16), true>(a, m.bf16_out, st);
     return;
   }
   k_moe_topk<<<m.tokens, 64, 0, st>>>(logits, m.experts, m.topk, m.ids, m.weights);

@@ -75,12 +75,20 @@ __device__ __forceinline__ u32x4_m scale_words(const uint8_t* base, uint32_t row
 // From a register whose lanes 16 i .. 16 i + 15 belong to row tile i, four registers with tile i's
 // lanes in all four groups of 16: v_permlane16_swap exchanges the odd groups of its first operand
 // with the even groups of its second, v_permlane32_swap the upper half with the lower half.
-__device__ __forceinline__ void spread4(uint32_t w, uint32_t (&o)[4]) {
+__device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[4]) {
   const auto a = __builtin_amdgcn_permlane16_swap(w, w, false, false);         // 0 0 2 2 and 1 1 3 3
   const auto e = __builtin_amdgcn_permlane32_swap(a[0], a[0], false, false);   // 0 0 0 0 and 2 2 2 2
   const auto f = __builtin_amdgcn_permlane32_swap(a[1], a[1], false, false);
   o[0] = e[0], o[2] = e[1], o[1] = f[0], o[3] = f[1];
 }
+
+// Likewise two, from a register whose even groups belong to tile 0 and odd ones to tile 1; one is its
+// own.
+__device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[2]) {
+  const auto a = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  o[0] = a[0], o[1] = a[1];
+}
+__device__ __forceinline__ void spread(uint32_t w, uint32_t (&o)[1]) { o[0] = w; }
 
 // 16 bytes at `base` (the same for the wave) + `off`: the address costs a lane one register.
 __device__ __forceinline__ u32x4_m load16(const uint8_t* base, uint32_t off) {
