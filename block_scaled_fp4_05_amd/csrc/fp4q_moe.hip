@@ -20,7 +20,8 @@ constexpr int kCus = 256;   // compute units of the GPU
 constexpr int kMaxTokens = 64;
 constexpr int kMaxPairs = kMaxTokens * 16;   // tokens x top-k
 
-// Order of logits as unsigned integers: NaN above everything, -0 equal to +0.
+// Order of logits as unsigned integers: NaN above everything, -0 equal to +0, none of them 0 (the
+// lowest, -infinity, is ~0xFF800000).
 __device__ __forceinline__ uint32_t logit_key(float l) {
   if (l != l) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(l + 0.0f);
@@ -94,32 +95,47 @@ __global__ __launch_bounds__(256) void k_moe_logits(const T* __restrict__ x, con
   }
 }
 
-// Each token's top-k, one wave per token: k rounds of a maximum over (logit, lower index first) that
-// each lane keeps for its experts (lane, lane + 64, ...), then the softmax over the k.
+// The largest of a wave's 64 values, in every lane: neighbours, quads and halves of 16 lanes by DPP,
+// then the groups of 16 by lane swaps.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));    // quad_perm [1,0,3,2]
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));    // quad_perm [2,3,0,1]
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));   // row_half_mirror
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));   // row_mirror
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
+// Each token's top-k, one wave per token: k rounds of a maximum over the logits' keys that each lane
+// keeps for its experts (lane, lane + 64, ...), the lowest expert of those that have it, then the
+// softmax over the k.
 __global__ __launch_bounds__(64) void k_moe_topk(const float* __restrict__ logits, int experts, int topk,
                                                  int32_t* __restrict__ ids, float* __restrict__ weights) {
   constexpr int kPerLane = 512 / 64;
   const int lane = threadIdx.x, t = blockIdx.x, n = gridDim.x * experts;
-  // key of an expert: its logit's order above, the complement of its index below; 0: taken or none
-  uint64_t key[kPerLane];
+  uint32_t key[kPerLane];   // 0: taken, or no expert (a logit's key is larger: see logit_key)
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int e = lane + 64 * i;
-    key[i] = e < experts ? ((uint64_t)logit_key(logit_of(logits, t * experts + e, n)) << 32) | (uint32_t)~e : 0ull;
+    key[i] = e < experts ? logit_key(logit_of(logits, t * experts + e, n)) : 0u;
   }
   int chosen = 0;   // lane j: the j-th choice
   for (int j = 0; j < topk; ++j) {
-    uint64_t best = key[0];
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 1; i < kPerLane; ++i) best = key[i] > best ? key[i] : best;
+    for (int i = 1; i < kPerLane; ++i) best = max(best, key[i]);
+    best = wave_max_u32(best);
+    int e = -1;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, off, 64);
-      best = o > best ? o : best;
+    for (int i = 0; i < kPerLane; ++i) {
+      const uint64_t m = __ballot(key[i] == best);
+      if (e < 0 && m) e = 64 * i + __builtin_ctzll(m);
     }
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) key[i] = key[i] == best ? 0ull : key[i];
-    if (lane == j) chosen = (int)~(uint32_t)best;
+    for (int i = 0; i < kPerLane; ++i) key[i] = lane + 64 * i == e ? 0u : key[i];
+    if (lane == j) chosen = e;
   }
   // every lane adds the exponentials in the order of the choices
   const float own = lane < topk ? logit_of(logits, t * experts + chosen, n) : 0.0f, top = __shfl(own, 0, 64);

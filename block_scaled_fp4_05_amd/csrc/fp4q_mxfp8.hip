@@ -346,7 +346,14 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_dgain(const float* __restrict_
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;   // cols % 32 == 0
   float v = 0.0f;
-  for (int r = ry; r < parts; r += 32) v += partial[(int64_t)r * cols + c];
+  constexpr int U = 16;   // loads in flight per thread; rows past the last add zero
+  for (int r = ry; r < parts; r += 32 * U) {
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = partial[(int64_t)min(r + 32 * u, parts - 1) * cols + c];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v += r + 32 * u < parts ? x[u] : 0.0f;
+  }
   t[ry][cx] = v;
   __syncthreads();
   for (int h = 16; h >= 1; h >>= 1) {
