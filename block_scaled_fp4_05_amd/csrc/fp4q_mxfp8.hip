@@ -171,7 +171,8 @@ __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict
 // t + NT j for thread t), so x is read once; it walks rows blockIdx.x, + gridDim.x, ... with
 // the gain in registers and the next row's loads in flight while this row is reduced.
 // -----------------------------------------------------------------------------------------
-__device__ __forceinline__ float wave_sum(float v) {
+template <typename F>
+__device__ __forceinline__ F wave_sum(F v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
   return v;
@@ -180,15 +181,29 @@ __device__ __forceinline__ float wave_sum(float v) {
 // Sum over the workgroup, the same bits in every thread.  `parity` alternates between calls,
 // so one barrier per call is enough: a buffer is written again only after the barrier of the
 // call in between, which every wave passes after reading it.
-__device__ __forceinline__ float group_sum(float v, float (*part)[16], int parity) {
+template <typename F>
+__device__ __forceinline__ F group_sum(F v, F (*part)[16], int parity) {
   v = wave_sum(v);
   const int waves = (int)blockDim.x >> 6;
   if (waves == 1) return v;
   if ((threadIdx.x & 63) == 0) part[parity][threadIdx.x >> 6] = v;
   lds_barrier();
-  float s = part[parity][0];
+  F s = part[parity][0];
   for (int i = 1; i < waves; ++i) s += part[parity][i];
   return s;
+}
+
+// 1 / sqrt(v) in two parts, to well past fp32: one Newton step in double from the fp32 root.  0,
+// infinity and NaN as the fp32 root gives them.
+struct Root {
+  float hi, lo;
+};
+__device__ __forceinline__ Root inverse_root(double v) {
+  const float r0 = 1.0f / __builtin_sqrtf((float)v);
+  if (!(r0 > 0.0f && r0 < __builtin_inff())) return Root{r0, 0.0f};
+  const double d = (double)r0, r = d + d * 0.5 * (1.0 - v * d * d);
+  const float hi = (float)r;
+  return Root{hi, (float)(r - (double)hi)};
 }
 
 template <typename T, int V>
@@ -197,7 +212,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
                                                   uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, T* sum,
                                                   float* __restrict__ rstd, T* __restrict__ y) {
   constexpr int N = Chunk<T>::N, LANES = Chunk<T>::LANES;
-  __shared__ float part[2][16];
+  __shared__ double part[2][16];
   const int tid = threadIdx.x, nt = blockDim.x, chunks = cols / N;
   float g[V][N];
 #pragma unroll
@@ -218,7 +233,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
       rin[j] = ok && res ? load_chunk_nt(res + at + c * N) : zero;
     }
   };
-  const float inv_n = 1.0f / (float)cols;
+  const double inv_n = 1.0 / (double)cols;
   fetch(blockIdx.x);
   int parity = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
@@ -245,13 +260,19 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
         if (tid + nt * j < chunks) store_chunk_nt(sum + at + (tid + nt * j) * N, pack(s[j]));
     }
     fetch(row + gridDim.x);
-    const float r = 1.0f / __builtin_sqrtf(group_sum(ss, part, parity) * inv_n + eps);
-    if (rstd && tid == 0) rstd[row] = r;
+    const Root r = inverse_root(group_sum((double)ss, part, parity) * inv_n + (double)eps);
+    if (rstd && tid == 0) rstd[row] = r.hi;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = tid + nt * j;
 #pragma unroll
-      for (int i = 0; i < N; ++i) s[j][i] = s[j][i] * r * g[j][i];
+      for (int i = 0; i < N; ++i) {
+        // s r gain, rounded once: p + e is s r to twice the precision.  (A sign of zero is the product's.)
+        const float p = s[j][i] * r.hi;
+        const float e = __builtin_fmaf(s[j][i], r.lo, __builtin_fmaf(s[j][i], r.hi, -p));
+        const float n = __builtin_fmaf(p, g[j][i], e * g[j][i]);
+        s[j][i] = __builtin_copysignf(n, __uint_as_float(__float_as_uint(p) ^ __float_as_uint(g[j][i])));
+      }
       uint32_t w[N / 4];
       const uint32_t code = mx8_encode<T>(s[j], w);
       if (c < chunks) {

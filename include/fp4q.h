@@ -392,16 +392,17 @@ fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, i
  * Residual addition, root-mean-square norm and MXFP8 in one read of x:
  *   s = x + residual (x without one),  r = 1 / sqrt(mean(s^2) + eps),  n = (s r) gain,
  *   codes, scales = MXFP8(n) as fp4q_quantize_mxfp8 writes it.
- * All of it in fp32 from the unrounded s; what is stored is rounded once.  A row's results do not
- * depend on the other rows or their number.
+ * From the unrounded s (an fp32 sum); n is the product of s, r and gain rounded once, with r held to
+ * twice fp32's precision, so codes differ from the exact ones only within an fp32 rounding of a
+ * boundary.  A row's results do not depend on the other rows or their number.
  *   x, residual  [rows][cols] of type dt; residual may be NULL.
  *   gain         device float [cols].        eps >= 0, finite.
  *   sum          s in type dt, or NULL.  It may be x itself or residual itself (in place);
  *                no other overlap.
  *   rstd         device float [rows] or NULL: r, for fp4q_rmsnorm_backward.
  *   y            n in type dt, or NULL (e.g. a router's input).
- * A row with a NaN gives NaN codes throughout; a row whose sum of squares overflows gives
- * r = 0 (its finite elements 0, its infinite ones NaN), as the formula does.
+ * A row with a NaN gives NaN codes throughout; a row with an element whose square overflows fp32
+ * gives r = 0 (its finite elements 0, its infinite ones NaN), as the formula does.
  * Shapes: cols % 32 == 0, cols <= 32768, rows < 2^31.  Alignment: 16 bytes (rstd 4).
  */
 #define FP4Q_NORM_MAX_COLS 32768
