@@ -206,20 +206,37 @@ __device__ __forceinline__ Root inverse_root(double v) {
   return Root{hi, (float)(r - (double)hi)};
 }
 
+// The same pointer, which the compiler takes for another one: what is read through it is not
+// hoisted out of the loop over rows into registers that are not there.
+__device__ __forceinline__ const float* per_row(const float* p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
+template <int N>
+__device__ __forceinline__ void load_gain(const float* __restrict__ gain, int c, int chunks, float (&g)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const f32x4_t v = c < chunks ? *reinterpret_cast<const f32x4_t*>(gain + (int64_t)c * N + i) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) g[i + k] = v[k];
+  }
+}
+
 template <typename T, int V>
 __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int rows, int cols,
-                                                  const float* __restrict__ gain, float eps,
+                                                  const float* gain, float eps,
                                                   uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, T* sum,
                                                   float* __restrict__ rstd, T* __restrict__ y) {
   constexpr int N = Chunk<T>::N, LANES = Chunk<T>::LANES;
+  // The gain stays in registers and the next row is fetched a row ahead; with 32 elements per
+  // thread that would spill, so there the gain comes from L2 for each row.
+  constexpr bool HOLD = V * N < 32;
   __shared__ double part[2][16];
   const int tid = threadIdx.x, nt = blockDim.x, chunks = cols / N;
-  float g[V][N];
+  float g[HOLD ? V : 1][N];
+  if constexpr (HOLD) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = tid + nt * j;
-#pragma unroll
-    for (int i = 0; i < N; ++i) g[j][i] = c < chunks ? gain[c * N + i] : 0.0f;
+    for (int j = 0; j < V; ++j) load_gain(gain, tid + nt * j, chunks, g[j]);
   }
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   u32x4_t xin[V], rin[V];
@@ -234,9 +251,10 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
     }
   };
   const double inv_n = 1.0 / (double)cols;
-  fetch(blockIdx.x);
+  if constexpr (HOLD) fetch(blockIdx.x);
   int parity = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
+    if constexpr (!HOLD) fetch(row);
     float s[V][N];
     float ss = 0.0f;
 #pragma unroll
@@ -259,19 +277,25 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
       for (int j = 0; j < V; ++j)
         if (tid + nt * j < chunks) store_chunk_nt(sum + at + (tid + nt * j) * N, pack(s[j]));
     }
-    fetch(row + gridDim.x);
+    if constexpr (HOLD) fetch(row + gridDim.x);
+    else gain = per_row(gain);
     const Root r = inverse_root(group_sum((double)ss, part, parity) * inv_n + (double)eps);
     if (rstd && tid == 0) rstd[row] = r.hi;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = tid + nt * j;
+      if constexpr (!HOLD) {
+        __builtin_amdgcn_sched_barrier(0);   // one chunk's gain at a time
+        load_gain(gain, c, chunks, g[0]);
+      }
+      const float* gj = g[HOLD ? j : 0];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         // s r gain, rounded once: p + e is s r to twice the precision.  (A sign of zero is the product's.)
         const float p = s[j][i] * r.hi;
         const float e = __builtin_fmaf(s[j][i], r.lo, __builtin_fmaf(s[j][i], r.hi, -p));
-        const float n = __builtin_fmaf(p, g[j][i], e * g[j][i]);
-        s[j][i] = __builtin_copysignf(n, __uint_as_float(__float_as_uint(p) ^ __float_as_uint(g[j][i])));
+        const float n = __builtin_fmaf(p, gj[i], e * gj[i]);
+        s[j][i] = __builtin_copysignf(n, __uint_as_float(__float_as_uint(p) ^ __float_as_uint(gj[i])));
       }
       uint32_t w[N / 4];
       const uint32_t code = mx8_encode<T>(s[j], w);
@@ -288,35 +312,34 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
 // writes one row of partial sums, which k_rmsnorm_dgain adds in a fixed order.
 template <typename T, int V>
 __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T* __restrict__ s_in, const T* dsum,
-                                                           int rows, int cols, const float* __restrict__ gain,
+                                                           int rows, int cols, const float* gain,
                                                            const float* __restrict__ rstd, T* dx,
                                                            float* __restrict__ partial) {
   constexpr int N = Chunk<T>::N;
+  constexpr bool HOLD = V * N < 32;   // as above; where not, dsum is read late too
   __shared__ float part[2][16];
   const int tid = threadIdx.x, nt = blockDim.x, chunks = cols / N;
-  float g[V][N], dg[V][N];
+  float g[HOLD ? V : 1][N], dg[V][N];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int c = tid + nt * j;
+    if constexpr (HOLD) load_gain(gain, tid + nt * j, chunks, g[j]);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      g[j][i] = c < chunks ? gain[c * N + i] : 0.0f;
-      dg[j][i] = 0.0f;
-    }
+    for (int i = 0; i < N; ++i) dg[j][i] = 0.0f;
   }
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   const float inv_n = 1.0f / (float)cols;
   int parity = 0;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
     const int64_t at = row * cols;
-    u32x4_t din[V], sin[V], uin[V];
+    u32x4_t din[V], sin[V], uin[HOLD ? V : 1];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = tid + nt * j;
       din[j] = c < chunks ? load_chunk_nt(dy + at + c * N) : zero;
       sin[j] = c < chunks ? load_chunk_nt(s_in + at + c * N) : zero;
-      uin[j] = c < chunks && dsum ? load_chunk_nt(dsum + at + c * N) : zero;
+      if constexpr (HOLD) uin[j] = c < chunks && dsum ? load_chunk_nt(dsum + at + c * N) : zero;
     }
+    if constexpr (!HOLD) gain = per_row(gain);
     const float r = rstd[row];
     float dot = 0.0f;
 #pragma unroll
@@ -324,13 +347,19 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
       float d[N], s[N], q = 0.0f;
       unpack(din[j], d);
       unpack(sin[j], s);
+      if constexpr (!HOLD) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_gain(gain, tid + nt * j, chunks, g[0]);
+      }
+      const float* gj = g[HOLD ? j : 0];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        q = __builtin_fmaf(d[i] * g[j][i], s[i], q);
+        q = __builtin_fmaf(d[i] * gj[i], s[i], q);
         dg[j][i] = __builtin_fmaf(d[i], s[i] * r, dg[j][i]);
       }
       dot += q;
     }
+    if constexpr (!HOLD) gain = per_row(gain);
     const float k = r * r * r * (group_sum(dot, part, parity) * inv_n);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -338,10 +367,16 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
       float d[N], s[N], u[N];
       unpack(din[j], d);
       unpack(sin[j], s);
-      unpack(uin[j], u);
+      if constexpr (!HOLD) {
+        __builtin_amdgcn_sched_barrier(0);
+        uin[0] = c < chunks && dsum ? load_chunk_nt(dsum + at + c * N) : zero;
+        load_gain(gain, c, chunks, g[0]);
+      }
+      const float* gj = g[HOLD ? j : 0];
+      unpack(uin[HOLD ? j : 0], u);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float t = r * (d[i] * g[j][i]) - s[i] * k;
+        const float t = r * (d[i] * gj[i]) - s[i] * k;
         u[i] = dsum ? t + u[i] : t;
       }
       if (c < chunks) store_chunk_nt(dx + at + c * N, pack(u));
@@ -384,10 +419,10 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_dgain(const float* __restrict_
   if (ry == 0) dgain[c] = t[0][cx];
 }
 
-// Threads and chunks per thread for a row of `chunks` chunks: the fewest chunks per thread
-// (powers of two up to 32 elements, which keeps a row in registers) that fit 256 threads, else
-// 512, else 1024 (FP4Q_NORM_MAX_COLS is 1024 x 32).  From the width alone, so that a row's sums,
-// and with them its results, are the same whatever number of rows it comes with.
+// Threads and chunks per thread for a row of `chunks` chunks: 256 threads with the fewest chunks
+// each (powers of two up to 16 elements) that hold the row in registers, else 512 or 1024 threads
+// of 16 elements, else 1024 of 32 (FP4Q_NORM_MAX_COLS is 1024 x 32).  From the width alone, so
+// that a row's sums, and with them its results, are the same whatever number of rows it comes with.
 struct RowShape {
   int v, threads;
 };
@@ -396,7 +431,7 @@ RowShape row_shape(int64_t cols) {
   const int64_t chunks = cols / Chunk<T>::N;
   constexpr int kMost = 32 / Chunk<T>::N;
   for (int limit : {256, 512, 1024})
-    for (int v = 1; v <= kMost; v *= 2) {
+    for (int v = 1; v < kMost; v *= 2) {
       const int64_t t = (chunks + v - 1) / v;
       if (t <= limit) return RowShape{v, (int)((t + 63) / 64 * 64)};
     }
@@ -419,7 +454,12 @@ struct BackwardKernel {
   static auto fn() { return k_rmsnorm_backward<T, V>; }
 };
 
-constexpr int kBackwardGroups = 1024;   // at most so many partial rows of dgain
+// Workgroups of the gradient, each with its row of partial sums: what the card holds at once (four
+// of 256 threads on each of its 256 units, or as many threads in larger ones).
+int64_t backward_groups(int64_t rows, int64_t cols) {
+  const int64_t most = cols <= 4096 ? 1024 : cols <= 8192 ? 512 : 256;
+  return rows < most ? rows : most;
+}
 
 template <typename T>
 void rmsnorm(const T* x, const T* res, int64_t rows, int64_t cols, const float* gain, float eps, uint8_t* codes,
@@ -433,7 +473,7 @@ template <typename T>
 void rmsnorm_backward(const T* dy, const T* s_in, const T* dsum, int64_t rows, int64_t cols, const float* gain,
                       const float* rstd, T* dx, float* dgain, float* partial, hipStream_t st) {
   const RowShape s = row_shape<T>(cols);
-  const int grid = (int)(rows < kBackwardGroups ? rows : kBackwardGroups);
+  const int grid = (int)backward_groups(rows, cols);
   by_chunks<BackwardKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(dy, s_in, dsum, (int)rows, (int)cols, gain, rstd, dx, partial);
   k_rmsnorm_dgain<<<(unsigned)(cols / 32), 1024, 0, st>>>(partial, grid, (int)cols, dgain);
 }
@@ -468,7 +508,7 @@ void launch_rmsnorm(const void* x, const void* residual, int dtype, int64_t rows
 }
 
 int64_t rmsnorm_backward_scratch(int64_t rows, int64_t cols) {
-  return (rows < kBackwardGroups ? rows : (int64_t)kBackwardGroups) * cols * 4;
+  return backward_groups(rows, cols) * cols * 4;
 }
 
 void launch_rmsnorm_backward(const void* dy, const void* s, const void* dsum, int dtype, int64_t rows, int64_t cols,
