@@ -12,84 +12,137 @@ namespace fp4q {
 namespace {
 
 // -----------------------------------------------------------------------------------------
-// Few rows.  A workgroup takes 16 NT rows of B and every row of A (G groups of 16); its waves
-// split k into contiguous ranges and join their sums in LDS, in wave order.  B's codes go from
-// memory to the matrix core's registers without a stop, since no two waves want the same ones.
+// Few rows.  A workgroup takes 16 NT rows of B and 16 G rows of A; its waves split k into
+// contiguous ranges and join their sums in LDS, in wave order.
+//
+// A matrix instruction's lanes 0..15 hold 16 different rows, and a load in that layout touches 16
+// lines per 16 lanes, which holds a CU at about 13 bytes per clock.  So eight lanes load 128 bytes
+// of a row, and a pass through the wave's own part of LDS (no barrier) deals the rows out: 16-byte
+// chunk c of row i sits at c ^ (i % 8).  (us, loads in the instruction's layout against these: 32 rows
+// of A, n 28672, k 8192 58.5 / 38; 16 rows, n 4096, k 14336 16.5 / 12.5; one row, where A's lines
+// are few either way and DIRECT loads its fragments, n 28672, k 8192 33.4 / 26.2.)
+// Bound by reading B: one row, n 28672, k 8192 (125 MB) at 4.8 TB/s; below some 20 MB by the launch
+// and one trip to memory: one row, n 4096, k 4096 (8.9 MB) 4.2 us.
 // -----------------------------------------------------------------------------------------
-template <int G, int NT, int WAVES, bool BF16OUT>
-__global__ __launch_bounds__(64 * WAVES) void k_gemm8_rows(const uint8_t* __restrict__ ac,
+template <int G, int NT, int WAVES, bool DIRECT, bool BF16OUT>
+__global__ __launch_bounds__(64 * WAVES, G == 1 && NT <= 2 ? 4 : 2) void k_gemm8_rows(const uint8_t* __restrict__ ac,
                                                            const uint8_t* __restrict__ as,
                                                            const uint8_t* __restrict__ bc,
                                                            const uint8_t* __restrict__ bs, int M, int N, int K,
                                                            void* __restrict__ cout) {
-  __shared__ v4f_m sums[WAVES][NT * G][64];
+  // per wave: NT blocks of B (two steps each) and 2 G blocks of A (one step each), 16 rows x 128 bytes
+  constexpr int kBlocks = NT + (DIRECT ? 0 : 2 * G);
+  union Lds {
+    u32x4_m blocks[WAVES][kBlocks][128];
+    v4f_m sums[WAVES][NT * G][64];
+  };
+  __shared__ Lds lds_;
+  auto& sums = lds_.sums;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * (16 * NT);
+  const int m0 = blockIdx.y * (16 * G);
   const int nk = K / 128;
   const int first = (int)((int64_t)nk * wave / WAVES), last = (int)((int64_t)nk * (wave + 1) / WAVES);
-  // rows past an operand's end read its last row; their results are not stored
-  const uint8_t* bcp[NT];
-  const uint8_t* bsp[NT];
+  // Rows past an operand's end read its last row; their results are not stored.
+  const int lr = lane >> 3, lc = (lane & 7) * 16;
+  const uint8_t *b0 = bc + (int64_t)n0 * (K / 2), *a0 = ac + (int64_t)m0 * K;
+  uint32_t bo[NT][2], ao[G][2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t row = min(n0 + 16 * t + r, N - 1);
-    bcp[t] = bc + row * (K / 2) + 16 * q;
-    bsp[t] = bs + row * (K / 32);
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) bo[t][h] = (uint32_t)((min(n0 + 16 * t + 8 * h + lr, N - 1) - n0) * (K / 2));
+#pragma unroll
+    for (int g = 0; g < G; ++g) ao[g][h] = (uint32_t)((min(m0 + 16 * g + (DIRECT ? r : 8 * h + lr), M - 1) - m0) * K);
   }
-  const uint8_t* acp[G];
-  const uint8_t* asp[G];
+  // Scale words likewise: lanes 16 i .. hold row tile i's (B's tiles, then A's), dealt out by lane swaps.
+  constexpr int kTiles = NT + G, kWords = (kTiles + 3) / 4;
+  const uint8_t* sp[kWords];
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    const int64_t row = min(16 * g + r, M - 1);
-    acp[g] = ac + row * K + 16 * q;
-    asp[g] = as + row * (K / 32);
+  for (int i = 0; i < kWords; ++i) {
+    const int tile = 4 * i + q, row = tile < NT ? min(n0 + 16 * tile + r, N - 1) : min(m0 + 16 * (tile - NT) + r, M - 1);
+    sp[i] = (tile < NT ? bs : as) + (int64_t)row * (K / 32);
   }
   v4f_m acc[NT][G];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int g = 0; g < G; ++g) acc[t][g] = v4f_m{0.0f, 0.0f, 0.0f, 0.0f};
-  // Four steps at a time, their B codes in flight together and a row's four scale words in one
-  // load: a load of one word per row costs the address unit as much as one of 16 bytes per lane.
-  constexpr int U = 4;
-  int s = first;
-  for (; s + U <= last; s += U) {
-    u32x4_m b[NT][U];
-    u32x4_w sb[NT], sa[G];
+  // Four steps' loads in flight, the next four's issued before the last two are multiplied.
+  struct Group {
+    u32x4_m b[2][NT][2], a[4][G][2], sc[kWords];
+  } f;
+  const auto fetch = [&](int s) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) b[t][u] = *reinterpret_cast<const u32x4_m*>(bcp[t] + (int64_t)(s + u) * 64);
-      sb[t] = *reinterpret_cast<const u32x4_w*>(bsp[t] + s * 4);
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g) sa[g] = *reinterpret_cast<const u32x4_w*>(asp[g] + s * 4);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const uint8_t* p = acp[g] + (int64_t)(s + u) * 128;
-        const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
+    for (int p = 0; p < 2; ++p)
+      if (s + 2 * p < last)   // (a row that ends within the two steps: its last bytes again, not used)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
-          acc[t][g] = mma_w4x8(frag4(b[t][u]), frag8(lo, hi), acc[t][g], sb[t][u] >> (8 * q), sa[g][u] >> (8 * q));
-      }
-  }
-  for (; s < last; ++s) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint8_t* p = acp[g] + (int64_t)s * 128;
-      const u32x4_m lo = *reinterpret_cast<const u32x4_m*>(p), hi = *reinterpret_cast<const u32x4_m*>(p + 64);
-      const uint32_t sa = *reinterpret_cast<const uint32_t*>(asp[g] + s * 4);
+          for (int h = 0; h < 2; ++h)
+            f.b[p][t][h] = load16(b0, bo[t][h] + (uint32_t)min(s * 64 + 128 * p + lc, K / 2 - 16));
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const u32x4_m b = *reinterpret_cast<const u32x4_m*>(bcp[t] + (int64_t)s * 64);
-        const uint32_t sb = *reinterpret_cast<const uint32_t*>(bsp[t] + s * 4);
-        acc[t][g] = mma_w4x8(frag4(b), frag8(lo, hi), acc[t][g], sb >> (8 * q), sa >> (8 * q));
+    for (int u = 0; u < 4; ++u)
+      if (s + u < last)
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            f.a[u][g][h] = load16(a0, ao[g][h] + (uint32_t)((s + u) * 128 + (DIRECT ? 64 * h + 16 * q : lc)));
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (4 * i + q < kTiles) f.sc[i] = scale_words(sp[i], 0, s, nk);
+  };
+  auto* block = lds_.blocks[wave];
+  const int put = lr * 8 + ((lane & 7) ^ lr);
+  const auto get = [&](int blk, int c) { return block[blk][r * 8 + (c ^ (r & 7))]; };
+  if (first < last) fetch(first);
+  for (int s = first; s < last; s += 4) {
+    u32x4_m a[4][G][2];   // DIRECT: the fragments as loaded
+    if constexpr (DIRECT)
+#pragma unroll
+      for (int i = 0; i < 8 * G; ++i) a[i / (2 * G)][i / 2 % G][i & 1] = f.a[i / (2 * G)][i / 2 % G][i & 1];
+    uint32_t sw[4][4 * kWords];   // by step and tile, the lane's byte first
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        uint32_t o[4];
+        spread(f.sc[i][u], o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sw[u][4 * i + j] = o[j] >> (8 * q);
       }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) block[t][put + 64 * h] = f.b[p][t][h];
+        if constexpr (!DIRECT)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int g = 0; g < G; ++g) block[NT + u * G + g][put + 64 * h] = f.a[2 * p + u][g][h];
+      }
+      if (p == 1 && s + 4 < last) fetch(s + 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (s + 2 * p + u < last) {
+          v8i_m w[NT];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) w[t] = frag4(get(t, 4 * u + q));
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const v8i_m x = DIRECT ? frag8(a[2 * p + u][g][0], a[2 * p + u][g][1])
+                                   : frag8(get(NT + u * G + g, q), get(NT + u * G + g, 4 + q));
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              acc[t][g] = mma_w4x8(w[t], x, acc[t][g], sw[2 * p + u][t], sw[2 * p + u][NT + g]);
+          }
+        }
     }
   }
+  __syncthreads();
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -100,7 +153,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_gemm8_rows(const uint8_t* __rest
     v4f_m v = sums[0][tg][l];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) v += sums[w][tg][l];
-    const int row = 16 * (tg % G) + (l & 15), col = n0 + 16 * (tg / G) + 4 * (l >> 4);
+    const int row = m0 + 16 * (tg % G) + (l & 15), col = n0 + 16 * (tg / G) + 4 * (l >> 4);
     if (row >= M || col >= N) continue;
     const int64_t at = (int64_t)row * N + col;
     const bool whole = (N & 3) == 0;   // then col + 4 <= N and the address is a multiple of four elements
@@ -500,27 +553,37 @@ bool run_tile(const Gemm8& g) {
   return true;
 }
 
-template <int G, int NT, int WAVES, bool BF16OUT>
+template <int G, int NT, int WAVES, bool DIRECT, bool BF16OUT>
 void run_rows(const Gemm8& g) {
   const unsigned grid = (unsigned)((g.n + (int64_t)16 * NT - 1) / (16 * NT));
-  k_gemm8_rows<G, NT, WAVES, BF16OUT><<<grid, 64 * WAVES, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k, g.c);
+  const dim3 grid2(grid, (unsigned)((g.m + 16 * G - 1) / (16 * G)));
+  k_gemm8_rows<G, NT, WAVES, DIRECT, BF16OUT><<<grid2, 64 * WAVES, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k, g.c);
 }
 
 template <bool BF16OUT>
 bool run(const Gemm8& g) {
   if (g.m <= 32 && g.n <= 1 << 26) {   // (a launch has at most 2^32 threads)
-    // Rows of B per workgroup: 16, or more where that leaves a workgroup per CU and the longer
-    // stream per wave pays (us at 16 / 32 / 64: one row of A, n 4096, k 4096 3.6 / 5.4 / 7.6;
-    // n 32768, k 8192 33.7 / 31.4 / 27.9; 16 rows, n 8192, k 8192 14.8 / 12.0 / 15.4).
-    const bool two = g.n >= 32 * kCus, four = g.n >= 128 * kCus && g.m <= 16;
-    if (g.m <= 16) {
-      if (four) run_rows<1, 4, 8, BF16OUT>(g);
-      else if (two) run_rows<1, 2, 8, BF16OUT>(g);
-      else run_rows<1, 1, 8, BF16OUT>(g);
+    // Rows of B per workgroup: 16, or 32 where the workgroups of 16 take more than a round or two
+    // (us at 16 / 32: one row of A, n 4096, k 4096 4.3 / 5.4; n 8192, k 8192 10.3 / 12.0; n 11008,
+    // k 4096 9.1 / 8.5; n 32768, k 8192 32.2 / 28.7; 24 rows, n 4096, k 4096 6.0 / 6.8; n 6144,
+    // k 4096 9.2 / 7.4).  64 took longer than 32 (n 32768, k 8192: 31.5).
+    if (g.m <= 4) {
+      if (g.n >= 40 * kCus) run_rows<1, 2, 4, true, BF16OUT>(g);
+      else run_rows<1, 1, 8, true, BF16OUT>(g);
+    } else if (g.m <= 16) {
+      if (g.n >= 40 * kCus) run_rows<1, 2, 4, false, BF16OUT>(g);
+      else run_rows<1, 1, 8, false, BF16OUT>(g);
     } else {
-      if (two) run_rows<2, 2, 8, BF16OUT>(g);
-      else run_rows<2, 1, 8, BF16OUT>(g);
+      if (g.n > 16 * kCus) run_rows<2, 2, 4, false, BF16OUT>(g);
+      else run_rows<2, 1, 8, false, BF16OUT>(g);
     }
+    return true;
+  }
+  // 64 rows of A likewise where that is one round: a tile's one wave of copies per 64 rows of B leaves
+  // CUs idle then (us, tiles / rows: 64 x 4096 x 14336 36.0 / 23.0, 64 x 4096 x 4096 9.0 / 8.2, 128 x 640
+  // x 8192 13.9 / 10.4).
+  if (((g.n + (int64_t)15) / 16) * ((g.m + (int64_t)63) / 64) <= kCus) {
+    run_rows<4, 1, 8, false, BF16OUT>(g);
     return true;
   }
   // The tile by what a round of one tile per CU takes, in units of a 64 x 64 tile's (measured at

@@ -55,7 +55,9 @@ def test_whole_values_are_exact(m, n, k):
                                    (20000, 65, 128), (3600, 3601, 512), (3600, 3601, 640), (3500, 3700, 1536),
                                    (1000, 3000, 1024), (900, 3001, 2688), (193, 4099, 640), (193, 4099, 1536),
                                    (1, 33000, 256), (16, 8200, 640), (5, 40001, 1152), (32, 8193, 384),
-                                   (20, 8193, 1280), (3, 70000, 512)])
+                                   (20, 8193, 1280), (3, 70000, 512), (4, 10300, 1152), (5, 10241, 640), (1, 300, 16384),
+                                   (17, 4100, 2176), (24, 6145, 896), (33, 4096, 640), (64, 4001, 4480), (70, 1900, 1152),
+                                   (200, 1000, 1536), (449, 500, 384), (1600, 130, 640)])
 def test_whole_values_large(m, n, k):
     _check_whole(m, n, k)
 
