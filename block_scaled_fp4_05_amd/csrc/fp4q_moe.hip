@@ -224,25 +224,22 @@ __device__ int choice_of_one(const Moe& a, int want, RouteLds& r) {
 // (the 17th column spreads the readers over the banks).
 typedef v4f_m UpSums[4][4][17];
 
-// K steps whose codes a wave has in flight: with more groups the registers go to their sums.
-constexpr int up_steps(int g) { return g == 1 ? 2 : 1; }
-
-// The weights of a workgroup's 32 hidden columns: four row tiles of 16, two of gate, two of up.
-template <int U>
+// The weights of a workgroup's 32 hidden columns over two K steps: four row tiles of 16, two of gate,
+// two of up, as loaded (see deal).
 struct UpWeights {
-  u32x4_m w[U][4];
+  u32x4_m w[4][2];
 };
 struct UpRows {
   const uint8_t *codes, *scales;   // of the first tile's first row; the others are uniform distances away
   int64_t up;                      // rows from gate to up
-  uint32_t row;                    // the lane's place in a tile's codes, in bytes
+  uint32_t row;                    // the lane's row of a tile's first eight, in bytes of codes
   uint32_t srow;                   // the scales of row lane % 16 of tile lane / 16
   __device__ __forceinline__ int64_t rows(int i) const { return (i & 1 ? 16 : 0) + (i >> 1 ? up : 0); }
 };
 __device__ __forceinline__ UpRows up_rows(const Moe& a, int e, int h0) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int64_t row = (int64_t)e * 2 * a.hidden + h0;
-  UpRows u{a.w13c + row * (a.d / 2), a.w13s + row * (a.d / 32), a.hidden, (uint32_t)(r * (a.d / 2) + 16 * q), 0};
+  UpRows u{a.w13c + row * (a.d / 2), a.w13s + row * (a.d / 32), a.hidden, (uint32_t)((lane >> 3) * (a.d / 2)), 0};
   u.srow = (uint32_t)((u.rows(q) + r) * (a.d / 32));
   return u;
 }
@@ -251,24 +248,24 @@ template <int W>
 __device__ __forceinline__ int up_first(const Moe& a, int wave) {
   return a.d / 128 * wave / W;
 }
-// Steps s .. s + U - 1 (past `last` the last again, unused).
-template <int U>
-__device__ __forceinline__ void load_up(const Moe& a, const UpRows& u, int s, int last, UpWeights<U>& d) {
+// Steps s and s + 1 (past the row's end its last bytes again, unused).
+__device__ __forceinline__ void load_up(const Moe& a, const UpRows& u, int s, UpWeights& d) {
+  const uint32_t at = u.row + (uint32_t)min(s * 64 + (int)(threadIdx.x & 7) * 16, a.d / 2 - 16);
 #pragma unroll
-  for (int k = 0; k < U; ++k)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d.w[k][i] = load16(u.codes + (u.rows(i) * (a.d / 2) + min(s + k, last - 1) * 64), u.row);
+    for (int h = 0; h < 2; ++h) d.w[i][h] = load16(u.codes + (u.rows(i) + 8 * h) * (a.d / 2), at);
 }
 
 // Gate and up products for G groups of 16 tokens, and the hidden activations of them.  `ahead`: this
 // wave's first weights, loaded.
 template <int G, int W>
 __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_t* list, int n,
-                         UpWeights<up_steps(G)>& ahead, UpSums* sums) {
+                         UpWeights& ahead, UpSums* sums) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr int U = up_steps(G);
+  constexpr int U = G == 1 ? 2 : 1;   // steps whose tokens are in flight: with more groups the registers go to the sums
+  auto* block = reinterpret_cast<u32x4_m*>(sums[wave]);
   const int nk = a.d / 128, first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1);
   // the lane's tokens (64 of 64 K bytes at most; columns past n repeat the last and are not stored),
   // and the one of group q % G whose scales it loads for all
@@ -286,21 +283,26 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
     const u32x4_m sw = scale_words(rows.scales, rows.srow, s, nk);   // the four tiles' at once
     const u32x4_m sx = scale_words(a.xs, xs, s, nk);
 #pragma unroll
-    for (int h = 0; h < 4; h += U) {
+    for (int h = 0; h < 4; h += 2) {
       if (s + h >= last) break;
-      u32x4_m xl[U][G], xh[U][G];
-#pragma unroll
-      for (int k = 0; k < U; ++k)
+      u32x4_m xl[U][G], xh[U][G], w[2][4];
+      const auto load_x = [&](int k, int to) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const uint8_t* p = a.xc + min(s + h + k, last - 1) * 128;
-          xl[k][g] = load16(p, xc[g]);
-          xh[k][g] = load16(p + 64, xc[g]);
+          xl[to][g] = load16(p, xc[g]);
+          xh[to][g] = load16(p + 64, xc[g]);
         }
-      if (s + h > first) load_up<U>(a, rows, s + h, last, ahead);
+      };
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
+      for (int k = 0; k < U; ++k) load_x(k, k);
+      if (s + h > first) load_up(a, rows, s + h, ahead);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) deal(block + 128 * (i & 1), ahead.w[i][0], ahead.w[i][1], w[0][i], w[1][i]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
         if (s + h + k >= last) break;
+        if (U == 1 && k == 1) load_x(1, 0);
         uint32_t tile[4], group[G];
         spread(sw[h + k], tile);
         spread(sx[h + k], group);
@@ -308,7 +310,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
         for (int g = 0; g < G; ++g)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            acc[i][g] = mma_w4x8(frag4(ahead.w[k][i]), frag8(xl[k][g], xh[k][g]), acc[i][g], tile[i] >> (8 * q),
+            acc[i][g] = mma_w4x8(frag4(w[k][i]), frag8(xl[k % U][g], xh[k % U][g]), acc[i][g], tile[i] >> (8 * q),
                                  group[g] >> (8 * q));
       }
     }
@@ -352,7 +354,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 // ROUTE: one token, whose choices come from the logits and are written to a.ids.
 template <int G, int W, bool ROUTE>
 __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
-  __shared__ UpSums sums[W];
+  __shared__ __align__(16) UpSums sums[W];   // until a wave's sums are there: its place to deal weights out
   __shared__ RouteLds r;
   // the arrival counts of the launch that follows; any workgroups do, before the first can leave
   for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < a.d / 16;
@@ -372,8 +374,8 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
   // out to have none (2 choices per expert: one in seven).
   const bool early = ROUTE || a.tokens * a.topk >= 2 * a.experts;
   const UpRows rows = up_rows(a, e, h0);
-  UpWeights<up_steps(G)> ahead;
-  if (early && first < last) load_up<up_steps(G)>(a, rows, first, last, ahead);
+  UpWeights ahead;
+  if (early && first < last) load_up(a, rows, first, ahead);
   int n;
   if constexpr (ROUTE) {
     if (threadIdx.x == 0) {
@@ -387,7 +389,8 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
     if (n == 0 || (by_choice && r.list[0] != blockIdx.y)) return;
   }
   for (int i = 0; i < n; i += 16 * G) {
-    if ((i > 0 || !early) && first < last) load_up<up_steps(G)>(a, rows, first, last, ahead);
+    if (i > 0) __syncthreads();   // the sums' places take weights again
+    if ((i > 0 || !early) && first < last) load_up(a, rows, first, ahead);
     up_tiles<G, W>(a, rows, h0, r.list + i, min(n - i, 16 * G), ahead, sums);
   }
 }
@@ -401,7 +404,7 @@ constexpr int kNone = 0xFFFF;   // no expert
 // Weights of one unit of work: up to ST K steps of one expert's RT tiles of 16 output rows.
 template <int RT, int ST>
 struct DownUnit {
-  u32x4_m w[ST][RT];
+  u32x4_m w[ST][RT];   // as loaded (see deal)
   u32x4_m sw;   // of row lane % 16 of tile lane / 16 % RT
 };
 template <int RT, int ST>
@@ -409,7 +412,7 @@ __device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, i
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int64_t row = (int64_t)e * a.d + n0, cols = a.hidden / 2;
   const uint8_t* wc = a.w2c + row * cols;
-  const uint32_t at = (uint32_t)(r * cols + 16 * q);
+  const uint32_t at = (uint32_t)((lane >> 2) * cols + 16 * (lane & 3));
 #pragma unroll
   for (int u = 0; u < ST; ++u)   // past the unit's end the last step again, unused
 #pragma unroll
@@ -421,7 +424,7 @@ __device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, i
 // own sums (out[token][16 RT]).
 template <int G, int RT, int ST>
 __device__ __forceinline__ void down_unit(const Moe& a, const DownUnit<RT, ST>& d, int s0, int s1, const uint16_t* list,
-                                          int n, const float* wts, float (*out)[16 * RT]) {
+                                          int n, const float* wts, float (*out)[16 * RT], u32x4_m* block) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   // the lane's hidden rows (1024 of 64 K bytes at most), and the one whose scales it loads for all
   uint32_t hc[G];
@@ -440,13 +443,16 @@ __device__ __forceinline__ void down_unit(const Moe& a, const DownUnit<RT, ST>& 
     uint32_t tile[RT], group[G];
     spread(d.sw[u], tile);
     spread(sh[u], group);
+    v8i_m w[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) w[i] = frag4(deal(block, d.w[u][i]));
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint8_t* p = a.hc + (s0 + u) * 128;
       const v8i_m h = frag8(load16(p, hc[g]), load16(p + 64, hc[g]));
 #pragma unroll
       for (int i = 0; i < RT; ++i)
-        acc[i][g] = mma_w4x8(frag4(d.w[u][i]), h, acc[i][g], tile[i] >> (8 * q), group[g] >> (8 * q));
+        acc[i][g] = mma_w4x8(w[i], h, acc[i][g], tile[i] >> (8 * q), group[g] >> (8 * q));
     }
   }
 #pragma unroll
@@ -479,6 +485,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   constexpr int kPairs = 16 * TOK;
   constexpr int kRows = 16 * RT, ST = down_steps(G);
   __shared__ __align__(16) float out[kDownWaves][TOK][kRows];
+  __shared__ u32x4_m place16[kDownWaves][64];   // each wave's to deal weights out
   __shared__ int16_t id[kPairs];
   __shared__ float wts[kPairs];
   __shared__ int count[512];            // by expert: pairs, then the first place in `sorted`
@@ -587,7 +594,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
     const int n = __builtin_amdgcn_readfirstlane(start[u / parts + 1]) - first;
     const bool none = __builtin_amdgcn_readfirstlane(expert[u / parts]) == kNone;
     for (int i = 0; i < n && !none; i += 16 * G)
-      down_unit<G, RT, ST>(a, now, s0, s1, sorted + first + i, min(n - i, 16 * G), wts, out[wave]);
+      down_unit<G, RT, ST>(a, now, s0, s1, sorted + first + i, min(n - i, 16 * G), wts, out[wave], place16[wave]);
     now = next;
   }
   __syncthreads();

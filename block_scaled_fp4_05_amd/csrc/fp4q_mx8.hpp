@@ -95,6 +95,26 @@ __device__ __forceinline__ u32x4_m load16(const uint8_t* base, uint32_t off) {
   return *reinterpret_cast<const u32x4_m*>(base + off);
 }
 
+// 16 rows x 128 bytes that were loaded by lines (lane l: 16-byte chunk l % 8 of row l / 8, and of row
+// 8 + l / 8) to the matrix instruction's layout (lane l: chunks l / 16 and 4 + l / 16 of row l % 16),
+// through 2 KB of the wave's own LDS, with no barrier.  Chunk c of row i sits at c ^ (i % 8): neither
+// side has bank conflicts.
+__device__ __forceinline__ void deal(u32x4_m* block, u32x4_m top, u32x4_m bottom, u32x4_m& lo, u32x4_m& hi) {
+  const int l = threadIdx.x & 63, r = l & 15, q = l >> 4, put = (l & 56) + ((l & 7) ^ (l >> 3));
+  block[put] = top;
+  block[put + 64] = bottom;
+  lo = block[r * 8 + (q ^ (r & 7))];
+  hi = block[r * 8 + ((q + 4) ^ (r & 7))];
+}
+
+// Likewise 16 rows x 64 bytes (lane l: chunk l % 4 of row l / 4) to one fragment, through 1 KB; chunk c of
+// row i sits at c ^ (i / 2 % 4).
+__device__ __forceinline__ u32x4_m deal(u32x4_m* block, u32x4_m v) {
+  const int l = threadIdx.x & 63, r = l & 15, q = l >> 4;
+  block[(l & 60) + ((l & 3) ^ ((l >> 3) & 3))] = v;
+  return block[r * 4 + (q ^ ((r >> 1) & 3))];
+}
+
 // Two fp32 values to packed bf16, nearest even (v_cvt_pk_bf16_f32; NaN stays NaN).
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_m{a, b}), bf16x2_m));
