@@ -124,6 +124,7 @@ __global__ __launch_bounds__(64 * WAVES, G == 1 && NT <= 2 ? 4 : 2) void k_gemm8
 #pragma unroll
             for (int g = 0; g < G; ++g) block[NT + u * G + g][put + 64 * h] = f.a[2 * p + u][g][h];
       }
+      wave_lds_fence();
       if (p == 1 && s + 4 < last) fetch(s + 4);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -140,6 +141,7 @@ __global__ __launch_bounds__(64 * WAVES, G == 1 && NT <= 2 ? 4 : 2) void k_gemm8
               acc[t][g] = mma_w4x8(w[t], x, acc[t][g], sw[2 * p + u][t], sw[2 * p + u][NT + g]);
           }
         }
+      wave_lds_fence();
     }
   }
   __syncthreads();

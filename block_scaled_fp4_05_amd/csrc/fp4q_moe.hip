@@ -230,6 +230,11 @@ __device__ int choice_of_one(const Moe& a, int want, RouteLds& r) {
 // Sums of a workgroup's waves on their way to one: [wave][row tile][q][17 columns] of four rows each
 // (the 17th column spreads the readers over the banks).
 typedef v4f_m UpSums[4][4][17];
+// A wave's LDS: its weights on their way to the matrix instruction's layout, then its sums.
+union UpPlace {
+  u32x4_m tiles[4][128];
+  UpSums sums;
+};
 
 // The weights of a workgroup's 32 hidden columns over two K steps: four row tiles of 16, two of gate,
 // two of up, as loaded (see deal).
@@ -268,11 +273,10 @@ __device__ __forceinline__ void load_up(const Moe& a, const UpRows& u, int s, Up
 // wave's first weights, loaded.
 template <int G, int W>
 __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_t* list, int n,
-                         UpWeights& ahead, UpSums* sums) {
+                         UpWeights& ahead, UpPlace* places) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int U = G == 1 ? 2 : 1;   // steps whose tokens are in flight: with more groups the registers go to the sums
-  auto* block = reinterpret_cast<u32x4_m*>(sums[wave]);
   const int nk = a.d / 128, first = up_first<W>(a, wave), last = up_first<W>(a, wave + 1);
   // the lane's tokens (64 of 64 K bytes at most; columns past n repeat the last and are not stored),
   // and the one of group q % G whose scales it loads for all
@@ -304,8 +308,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 #pragma unroll
       for (int k = 0; k < U; ++k) load_x(k, k);
       if (s + h > first) load_up(a, rows, s + h, ahead);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) deal(block + 128 * (i & 1), ahead.w[i][0], ahead.w[i][1], w[0][i], w[1][i]);
+      deal(places[wave].tiles, ahead.w, w[0], w[1]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (s + h + k >= last) break;
@@ -326,7 +329,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
   for (int g = 0; g < G; ++g) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sums[wave][i][q][r] = acc[i][g];
+    for (int i = 0; i < 4; ++i) places[wave].sums[i][q][r] = acc[i][g];
     __syncthreads();
     // thread -> token column c, hidden column i; 32 neighbouring lanes hold one MXFP8 block
     const int i = threadIdx.x & 31;
@@ -335,8 +338,8 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
       float gate = 0.0f, up = 0.0f;
 #pragma unroll
       for (int v = 0; v < W; ++v) {
-        gate += sums[v][i >> 4][(i >> 2) & 3][c][i & 3];
-        up += sums[v][2 + (i >> 4)][(i >> 2) & 3][c][i & 3];
+        gate += places[v].sums[i >> 4][(i >> 2) & 3][c][i & 3];
+        up += places[v].sums[2 + (i >> 4)][(i >> 2) & 3][c][i & 3];
       }
       const float h = gate / (1.0f + expf(-gate)) * up;
       float m = __builtin_fabsf(h);
@@ -364,7 +367,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 // ROUTE: one token, whose choices come from the logits and are written to a.ids.
 template <int G, int W, bool ROUTE>
 __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
-  __shared__ __align__(16) UpSums sums[W];   // until a wave's sums are there: its place to deal weights out
+  __shared__ UpPlace places[W];
   __shared__ RouteLds r;
   // the arrival counts of the launch that follows; any workgroups do, before the first can leave
   for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x; i < a.d / 16;
@@ -401,7 +404,7 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
   for (int i = 0; i < n; i += 16 * G) {
     if (i > 0) __syncthreads();   // the sums' places take weights again
     if ((i > 0 || !early) && first < last) load_up(a, rows, first, ahead);
-    up_tiles<G, W>(a, rows, h0, r.list + i, min(n - i, 16 * G), ahead, sums);
+    up_tiles<G, W>(a, rows, h0, r.list + i, min(n - i, 16 * G), ahead, places);
   }
 }
 
@@ -453,9 +456,11 @@ __device__ __forceinline__ void down_unit(const Moe& a, const DownUnit<RT, ST>& 
     uint32_t tile[RT], group[G];
     spread(d.sw[u], tile);
     spread(sh[u], group);
+    u32x4_m dealt[RT];
+    deal(block, d.w[u], dealt);
     v8i_m w[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w[i] = frag4(deal(block, d.w[u][i]));
+    for (int i = 0; i < RT; ++i) w[i] = frag4(dealt[i]);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const uint8_t* p = a.hc + (s0 + u) * 128;

@@ -95,24 +95,40 @@ __device__ __forceinline__ u32x4_m load16(const uint8_t* base, uint32_t off) {
   return *reinterpret_cast<const u32x4_m*>(base + off);
 }
 
-// 16 rows x 128 bytes that were loaded by lines (lane l: 16-byte chunk l % 8 of row l / 8, and of row
-// 8 + l / 8) to the matrix instruction's layout (lane l: chunks l / 16 and 4 + l / 16 of row l % 16),
-// through 2 KB of the wave's own LDS, with no barrier.  Chunk c of row i sits at c ^ (i % 8): neither
-// side has bank conflicts.
-__device__ __forceinline__ void deal(u32x4_m* block, u32x4_m top, u32x4_m bottom, u32x4_m& lo, u32x4_m& hi) {
-  const int l = threadIdx.x & 63, r = l & 15, q = l >> 4, put = (l & 56) + ((l & 7) ^ (l >> 3));
-  block[put] = top;
-  block[put + 64] = bottom;
-  lo = block[r * 8 + (q ^ (r & 7))];
-  hi = block[r * 8 + ((q + 4) ^ (r & 7))];
+// Orders a wave's LDS writes before its other lanes' reads, and those before the next writes: no
+// instruction (the hardware keeps a wave's LDS accesses in order), only a limit on the compiler.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
 }
 
-// Likewise 16 rows x 64 bytes (lane l: chunk l % 4 of row l / 4) to one fragment, through 1 KB; chunk c of
-// row i sits at c ^ (i / 2 % 4).
-__device__ __forceinline__ u32x4_m deal(u32x4_m* block, u32x4_m v) {
+// T tiles of 16 rows x 128 bytes that were loaded by lines (lane l: w[i][0] is 16-byte chunk l % 8 of row
+// l / 8 of tile i, w[i][1] that of row 8 + l / 8) to the matrix instruction's layout (lane l: chunks l / 16,
+// in lo, and 4 + l / 16, in hi, of row l % 16), through 2 KB each of the wave's own LDS, with no barrier
+// of the workgroup.  Chunk c of row i sits at c ^ (i % 8): neither side has bank conflicts.
+template <int T>
+__device__ __forceinline__ void deal(u32x4_m (*block)[128], const u32x4_m (&w)[T][2], u32x4_m (&lo)[T], u32x4_m (&hi)[T]) {
+  const int l = threadIdx.x & 63, r = l & 15, q = l >> 4, put = (l & 56) + ((l & 7) ^ (l >> 3));
+  wave_lds_fence();
+#pragma unroll
+  for (int i = 0; i < T; ++i) block[i][put] = w[i][0], block[i][put + 64] = w[i][1];
+  wave_lds_fence();
+#pragma unroll
+  for (int i = 0; i < T; ++i) lo[i] = block[i][r * 8 + (q ^ (r & 7))], hi[i] = block[i][r * 8 + ((q + 4) ^ (r & 7))];
+}
+
+// Likewise T tiles of 16 rows x 64 bytes (lane l: chunk l % 4 of row l / 4) to one fragment each, through 1 KB
+// for one tile after the other; chunk c of row i sits at c ^ (i / 2 % 4).
+template <int T>
+__device__ __forceinline__ void deal(u32x4_m* block, const u32x4_m (&w)[T], u32x4_m (&frag)[T]) {
   const int l = threadIdx.x & 63, r = l & 15, q = l >> 4;
-  block[(l & 60) + ((l & 3) ^ ((l >> 3) & 3))] = v;
-  return block[r * 4 + (q ^ ((r >> 1) & 3))];
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    wave_lds_fence();
+    block[(l & 60) + ((l & 3) ^ ((l >> 3) & 3))] = w[i];
+    wave_lds_fence();
+    frag[i] = block[r * 4 + (q ^ ((r >> 1) & 3))];
+  }
 }
 
 // Two fp32 values to packed bf16, nearest even (v_cvt_pk_bf16_f32; NaN stays NaN).
