@@ -366,7 +366,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 // which the down product takes it.  G: groups of 16 tokens per pass over the expert's weights.
 // ROUTE: one token, whose choices come from the logits and are written to a.ids.
 template <int G, int W, bool ROUTE>
-__global__ __launch_bounds__(64 * W, G == 4 ? 2 : 4) void k_moe_up(Moe a) {
+__global__ __launch_bounds__(64 * W, G == 4 ? 2 : G == 2 ? 3 : 4) void k_moe_up(Moe a) {
   __shared__ UpPlace places[W];
   __shared__ RouteLds r;
   // the arrival counts of the launch that follows; any workgroups do, before the first can leave
