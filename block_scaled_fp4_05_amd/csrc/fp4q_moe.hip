@@ -365,6 +365,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 // four waves the weights of one travel while another multiplies.  The activation stays fp32 until its one rounding to MXFP8, the form in
 // which the down product takes it.  G: groups of 16 tokens per pass over the expert's weights.
 // ROUTE: one token, whose choices come from the logits and are written to a.ids.
+// (Bounds: 128 registers spill with G = 2: 64 tokens, 4 of 16 experts, d 4096 took 91 us against 84.)
 template <int G, int W, bool ROUTE>
 __global__ __launch_bounds__(64 * W, G == 4 ? 2 : G == 2 ? 3 : 4) void k_moe_up(Moe a) {
   __shared__ UpPlace places[W];
@@ -665,11 +666,12 @@ int groups(const Moe& a) {
 
 template <int G, bool ROUTE>
 void run_up(const Moe& a, hipStream_t st) {
-  // Waves per workgroup: eight where each has four K steps then, or where there are too few workgroups
-  // to fill the GPU with four (us of the whole layer, four / eight waves: 64 tokens, d 4096, 4 of 32
-  // experts 104.3 / 101.2; 64 tokens, d 2048, 8 of 64 73.3 / 81.3, 4 of 8 39.2 / 37.7).
+  // Waves per workgroup: eight where each has four K steps then and 16 waves fit a CU (G = 1), or where
+  // there are too few workgroups to fill the GPU with four (us of the whole layer, four / eight waves: 64
+  // tokens, d 4096, 4 of 32 experts 104.3 / 101.2, 4 of 16 (G = 2) 78.3 / 82.7; 64 tokens, d 2048, 8 of 64
+  // 73.3 / 81.3, 4 of 8 39.2 / 37.7).
   const dim3 grid(a.hidden / 32, a.slots);
-  if (a.d >= 8 * 4 * 128 || (int64_t)grid.x * grid.y <= 2 * kCus) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
+  if ((G == 1 && a.d >= 8 * 4 * 128) || (int64_t)grid.x * grid.y <= 2 * kCus) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
   else k_moe_up<G, 4, ROUTE><<<grid, 256, 0, st>>>(a);
 }
 
