@@ -60,7 +60,8 @@ __global__ __launch_bounds__(64 * WAVES, G == 1 && NT <= 2 ? 4 : 2) void k_gemm8
   const uint8_t* sp[kWords];
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
-    const int tile = 4 * i + q, row = tile < NT ? min(n0 + 16 * tile + r, N - 1) : min(m0 + 16 * (tile - NT) + r, M - 1);
+    const int tile = 4 * i + q;
+    const int row = tile < NT ? min(n0 + 16 * tile + r, N - 1) : min(m0 + 16 * (tile - NT) + r, M - 1);
     sp[i] = (tile < NT ? bs : as) + (int64_t)row * (K / 32);
   }
   v4f_m acc[NT][G];
@@ -258,8 +259,8 @@ struct TileLds {
     Loop loop;
     uint16_t out[4][32 * MI * 32 * NJ];   // each wave's block of C on its way out, bf16
   };
-  static constexpr int kSlices = (MI + NJ + 3) / 4;                            // words: slices per step
-  static constexpr int kLoads = 2 * MI + NJ + (WIDE ? 0 : kSlices);            // at least so many copies per wave and step
+  static constexpr int kSlices = (MI + NJ + 3) / 4;                   // words: slices per step
+  static constexpr int kLoads = 2 * MI + NJ + (WIDE ? 0 : kSlices);   // at least so many copies per wave and step
 };
 
 template <int P>
@@ -562,7 +563,8 @@ template <int G, int NT, int WAVES, bool DIRECT, bool BF16OUT>
 void run_rows(const Gemm8& g) {
   const unsigned grid = (unsigned)((g.n + (int64_t)16 * NT - 1) / (16 * NT));
   const dim3 grid2(grid, (unsigned)((g.m + 16 * G - 1) / (16 * G)));
-  k_gemm8_rows<G, NT, WAVES, DIRECT, BF16OUT><<<grid2, 64 * WAVES, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k, g.c);
+  k_gemm8_rows<G, NT, WAVES, DIRECT, BF16OUT><<<grid2, 64 * WAVES, 0, g.st>>>(g.ac, g.as, g.bc, g.bs, g.m, g.n, g.k,
+                                                                              g.c);
 }
 
 template <bool BF16OUT>

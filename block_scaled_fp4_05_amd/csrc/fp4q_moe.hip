@@ -14,7 +14,7 @@
 // 62 us for the up product below and 39 for the down product.
 //
 // Measured, 64 tokens, 4 of 32 experts, d 4096, hidden 2048 (428 MB of weights), us: logits 4.7, top-k 4.7,
-// up 56 (285 MB, 5.1 TB/s), down 37 (143 MB, 3.8 TB/s).  One token, 4 of 64 experts, d 2048, hidden 1024
+// up 55 (285 MB, 5.2 TB/s), down 37 (143 MB, 3.8 TB/s).  One token, 4 of 64 experts, d 2048, hidden 1024
 // (14 MB): 3.2, -, 6.5, 5.8, each a launch and one trip to memory.
 #include "fp4q_dev.hpp"
 #include "fp4q_mx8.hpp"
@@ -360,10 +360,10 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
   }
 }
 
-// Grid: hidden / 32 tiles x slots: 32 columns of gate and of up make one MXFP8 block, so a workgroup rounds
-// its activations without help from others.  The waves split d, and with some 2000 workgroups of eight or
-// four waves the weights of one travel while another multiplies.  The activation stays fp32 until its one rounding to MXFP8, the form in
-// which the down product takes it.  G: groups of 16 tokens per pass over the expert's weights.
+// Grid: hidden / 32 tiles x slots: 32 columns of gate and of up make one MXFP8 block, so a workgroup
+// rounds its activations without help from others.  The waves split d; the weights of one workgroup
+// travel while another's are multiplied.  The activation stays fp32 until its one rounding to MXFP8, the
+// form in which the down product takes it.  G: groups of 16 tokens per pass over the expert's weights.
 // ROUTE: one token, whose choices come from the logits and are written to a.ids.
 // (Bounds: 128 registers spill with G = 2: 64 tokens, 4 of 16 experts, d 4096 took 91 us against 84.)
 template <int G, int W, bool ROUTE>
@@ -431,7 +431,8 @@ __device__ __forceinline__ void load_unit(const Moe& a, int e, int n0, int s0, i
   for (int u = 0; u < ST; ++u)   // past the unit's end the last step again, unused
 #pragma unroll
     for (int i = 0; i < RT; ++i) d.w[u][i] = load16(wc + (16 * i * cols + min(s0 + u, s1 - 1) * 64), at);
-  d.sw = scale_words(a.w2s + row * (a.hidden / 32), (uint32_t)((16 * (q % RT) + r) * (a.hidden / 32)), s0, a.hidden / 128);
+  d.sw = scale_words(a.w2s + row * (a.hidden / 32), (uint32_t)((16 * (q % RT) + r) * (a.hidden / 32)), s0,
+                     a.hidden / 128);
 }
 
 // The unit's product with its expert's hidden rows, added with the pairs' weights to this wave's
@@ -549,7 +550,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
       for (int j = 0; j < a.topk; ++j) total += expf(wts[p0 + j] - top);
       w = expf(w - top) / total;
       if (blockIdx.x == 0 && blockIdx.y == 0) a.weights[tid] = w;
-    } else if (e >= 0 && !single) {   // the first place of an expert takes the weights of its repeats, which take no part
+    } else if (e >= 0 && !single) {   // an expert's first place takes its repeats' weights; they take no part
       for (int f = p0; f < tid; ++f)
         if (id[f] == e) e = -1;
       if (e >= 0)
@@ -658,7 +659,8 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
 constexpr int row_tiles(int tokens) { return tokens <= 16 ? 1 : 2; }
 
 // Groups of 16 tokens that a pass over an expert's weights takes: from the mean number of tokens
-// per expert, so that a second pass (from L2) is rare, with as few registers as that allows.
+// per expert, so that a second pass (from L2) is rare, with as few registers as that allows (us with
+// one / two groups at a mean of 8: 64 tokens, 4 of 32 experts, d 4096 104 / 119).
 int groups(const Moe& a) {
   const int mean = a.tokens * a.topk / a.experts;
   return a.tokens <= 16 || mean <= 8 ? 1 : a.tokens <= 32 || mean <= 20 ? 2 : 4;
@@ -671,7 +673,8 @@ void run_up(const Moe& a, hipStream_t st) {
   // tokens, d 4096, 4 of 32 experts 104.3 / 101.2, 4 of 16 (G = 2) 78.3 / 82.7; 64 tokens, d 2048, 8 of 64
   // 73.3 / 81.3, 4 of 8 39.2 / 37.7).
   const dim3 grid(a.hidden / 32, a.slots);
-  if ((G == 1 && a.d >= 8 * 4 * 128) || (int64_t)grid.x * grid.y <= 2 * kCus) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
+  const bool eight = (G == 1 && a.d >= 8 * 4 * 128) || (int64_t)grid.x * grid.y <= 2 * kCus;
+  if (eight) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
   else k_moe_up<G, 4, ROUTE><<<grid, 256, 0, st>>>(a);
 }
 

@@ -107,7 +107,8 @@ __device__ __forceinline__ void wave_lds_fence() {
 // in lo, and 4 + l / 16, in hi, of row l % 16), through 2 KB each of the wave's own LDS, with no barrier
 // of the workgroup.  Chunk c of row i sits at c ^ (i % 8): neither side has bank conflicts.
 template <int T>
-__device__ __forceinline__ void deal(u32x4_m (*block)[128], const u32x4_m (&w)[T][2], u32x4_m (&lo)[T], u32x4_m (&hi)[T]) {
+__device__ __forceinline__ void deal(u32x4_m (*block)[128], const u32x4_m (&w)[T][2], u32x4_m (&lo)[T],
+                                     u32x4_m (&hi)[T]) {
   const int l = threadIdx.x & 63, r = l & 15, q = l >> 4, put = (l & 56) + ((l & 7) ^ (l >> 3));
   wave_lds_fence();
 #pragma unroll

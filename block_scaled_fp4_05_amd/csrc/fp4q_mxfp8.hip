@@ -222,7 +222,8 @@ template <int N>
 __device__ __forceinline__ void load_gain(const float* __restrict__ gain, int c, int chunks, float (&g)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
-    const f32x4_t v = c < chunks ? *reinterpret_cast<const f32x4_t*>(gain + (int64_t)c * N + i) : f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const f32x4_t none = {0.0f, 0.0f, 0.0f, 0.0f};
+    const f32x4_t v = c < chunks ? *reinterpret_cast<const f32x4_t*>(gain + (int64_t)c * N + i) : none;
 #pragma unroll
     for (int k = 0; k < 4; ++k) g[i + k] = v[k];
   }
@@ -475,7 +476,8 @@ void rmsnorm(const T* x, const T* res, int64_t rows, int64_t cols, const float* 
              uint8_t* scales, T* sum, float* rstd, T* y, hipStream_t st) {
   const RowShape s = row_shape<T>(cols);
   const int grid = (int)(rows < 2048 ? rows : 2048);
-  by_chunks<NormKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(x, res, (int)rows, (int)cols, gain, eps, codes, scales, sum, rstd, y);
+  by_chunks<NormKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(x, res, (int)rows, (int)cols, gain, eps, codes, scales, sum,
+                                                            rstd, y);
 }
 
 template <typename T>
@@ -483,7 +485,8 @@ void rmsnorm_backward(const T* dy, const T* s_in, const T* dsum, int64_t rows, i
                       const float* rstd, T* dx, float* dgain, float* partial, hipStream_t st) {
   const RowShape s = row_shape<T>(cols);
   const int grid = (int)backward_groups(rows, cols);
-  by_chunks<BackwardKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(dy, s_in, dsum, (int)rows, (int)cols, gain, rstd, dx, partial);
+  by_chunks<BackwardKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(dy, s_in, dsum, (int)rows, (int)cols, gain, rstd, dx,
+                                                                partial);
   k_rmsnorm_dgain<<<(unsigned)(cols / 32), 1024, 0, st>>>(partial, grid, (int)cols, dgain);
 }
 
