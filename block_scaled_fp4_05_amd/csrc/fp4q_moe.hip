@@ -518,8 +518,9 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
   DownUnit<RT, ST> now, next;
   int u = wave * gridDim.y + blockIdx.y;
   const auto unit_steps = [&](int active) { return min(max(active * nk / workers, 1), ST); };
-  // One token: its choices are the units' experts as they stand (a repeated one is two units), so
-  // nothing is sorted and the first weights travel while the rest is set up.
+  // One token: its choices are the units' experts as they stand, so nothing is sorted and the first
+  // weights travel while the rest is set up.  (An expert's repeats become kNone below: their units are
+  // skipped, k_moe_up has written the hidden row of its first place only.)
   const bool single = ROUTE || (TOK == 16 && a.tokens == 1);
   if (single) {
     const int per = unit_steps(a.topk), parts = (nk + per - 1) / per, s0 = u % parts * per;
@@ -550,7 +551,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
       for (int j = 0; j < a.topk; ++j) total += expf(wts[p0 + j] - top);
       w = expf(w - top) / total;
       if (blockIdx.x == 0 && blockIdx.y == 0) a.weights[tid] = w;
-    } else if (e >= 0 && !single) {   // an expert's first place takes its repeats' weights; they take no part
+    } else if (e >= 0) {   // an expert's first place takes its repeats' weights; they take no part
       for (int f = p0; f < tid; ++f)
         if (id[f] == e) e = -1;
       if (e >= 0)
