@@ -511,6 +511,7 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+    wave_lds_fence();   // the rows are read by other lanes of the wave than wrote them
     uint16_t* c16 = static_cast<uint16_t*>(cout);
     const bool vec = (N & 7) == 0;
     for (int it = 0; it < 32 * MI * LPR / 64; ++it) {
