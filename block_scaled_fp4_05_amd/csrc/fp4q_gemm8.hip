@@ -519,7 +519,7 @@ __global__ __launch_bounds__(256) void k_gemm8_tile(const uint8_t* __restrict__ 
       if (br + row >= M) continue;
       uint16_t* dst = c16 + (int64_t)(br + row) * N + bc0 + c8;
       const uint16_t* src = e + row * W + c8;
-      if (vec && bc0 + c8 + 8 <= N) {
+      if (vec && bc0 + c8 <= N - 8) {   // (bc0 + c8 + 8 may pass 2^31)
         *reinterpret_cast<u32x4_m*>(dst) = *reinterpret_cast<const u32x4_m*>(src);
       } else {
         for (int x = 0; x < 8 && bc0 + c8 + x < N; ++x) dst[x] = src[x];
