@@ -315,8 +315,9 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
   }
 }
 
-// Gradient: a = dy gain, dx = r a - s r^3 mean(a s) + dsum, dgain = sum over rows of dy s r.  The same
-// walk; each workgroup also adds up dy s r over its rows in registers and
+// Gradient: a = dy gain, dx = r a - s r^3 mean(a s) + dsum, dgain = sum over rows of dy s r.  With x = s r,
+// of size 1 whatever the row's, dx = r (a - x mean(a x)) + dsum: r^3 would leave fp32's range for rows of
+// 1e13 and more, or 1e-13 and less.  The same walk; each workgroup also adds up dy s r over its rows in registers and
 // writes one row of partial sums, which k_rmsnorm_dgain adds in a fixed order.
 // Bound by memory: bf16 8192 x 4096 with dsum (268 MB) in 51 us, 5.3 TB/s, and 4.9 us for the partial sums
 // (16.8 MB from the last-level cache).
@@ -364,13 +365,14 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
       const float* gj = g[HOLD ? j : 0];
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        q = __builtin_fmaf(d[i] * gj[i], s[i], q);
-        dg[j][i] = __builtin_fmaf(d[i], s[i] * r, dg[j][i]);
+        const float x = s[i] * r;
+        q = __builtin_fmaf(d[i] * gj[i], x, q);
+        dg[j][i] = __builtin_fmaf(d[i], x, dg[j][i]);
       }
       dot += q;
     }
     if constexpr (!HOLD) gain = per_row(gain);
-    const float k = r * r * r * (group_sum(dot, part, parity) * inv_n);
+    const float k = group_sum(dot, part, parity) * inv_n;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = tid + nt * j;
@@ -386,7 +388,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
       unpack(uin[HOLD ? j : 0], u);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float t = r * (d[i] * gj[i]) - s[i] * k;
+        const float t = r * (d[i] * gj[i] - s[i] * r * k);
         u[i] = dsum ? t + u[i] : t;
       }
       if (c < chunks) store_chunk_nt(dx + at + c * N, pack(u));
