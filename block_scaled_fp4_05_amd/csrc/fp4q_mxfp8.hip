@@ -317,10 +317,13 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
 
 // Gradient: a = dy gain, dx = r a - s r^3 mean(a s) + dsum, dgain = sum over rows of dy s r.  With x = s r,
 // of size 1 whatever the row's, dx = r (a - x mean(a x)) + dsum: r^3 would leave fp32's range for rows of
-// 1e13 and more, or 1e-13 and less.  The same walk; each workgroup also adds up dy s r over its rows in registers and
-// writes one row of partial sums, which k_rmsnorm_dgain adds in a fixed order.
+// 1e13 and more, or 1e-13 and less.  The same walk; each workgroup also adds up dy s r over its rows, in registers
+// for kRun rows at a time and these runs in its row of partial sums (one running sum was off by 3400
+// roundings after 2^24 equal rows; runs keep that below 360), which k_rmsnorm_dgain adds in a fixed order.
 // Bound by memory: bf16 8192 x 4096 with dsum (268 MB) in 51 us, 5.3 TB/s, and 4.9 us for the partial sums
 // (16.8 MB from the last-level cache).
+constexpr int kRun = 64;
+
 template <typename T, int V>
 __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T* __restrict__ s_in, const T* dsum,
                                                            int rows, int cols, const float* gain,
@@ -339,7 +342,28 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
   }
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   const float inv_n = 1.0f / (float)cols;
-  int parity = 0;
+  int parity = 0, run = 0;   // rows in dg
+  bool later = false;        // earlier runs are in `partial`
+  const auto end_run = [&]() {
+    float* to = partial + (int64_t)blockIdx.x * cols;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = tid + nt * j;
+      if (c < chunks) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          f32x4_t v = {dg[j][i], dg[j][i + 1], dg[j][i + 2], dg[j][i + 3]};
+          f32x4_t* p = reinterpret_cast<f32x4_t*>(to + c * N + i);
+          if (later) v += *p;
+          *p = v;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) dg[j][i] = 0.0f;
+    }
+    later = true;
+    run = 0;
+  };
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, parity ^= 1) {
     const int64_t at = row * cols;
     u32x4_t din[V], sin[V], uin[HOLD ? V : 1];
@@ -393,17 +417,9 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
       }
       if (c < chunks) store_chunk_nt(dx + at + c * N, pack(u));
     }
+    if (++run == kRun) end_run();
   }
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = tid + nt * j;
-    if (c < chunks) {
-#pragma unroll
-      for (int i = 0; i < N; i += 4)
-        *reinterpret_cast<f32x4_t*>(partial + (int64_t)blockIdx.x * cols + c * N + i) =
-            f32x4_t{dg[j][i], dg[j][i + 1], dg[j][i + 2], dg[j][i + 3]};
-    }
-  }
+  if (run > 0) end_run();   // (every workgroup has a row: see backward_groups)
 }
 
 // dgain[c] = sum over the partial rows: 32 columns per workgroup, 32 threads per column, each

@@ -419,7 +419,8 @@ fp4q_status fp4q_rmsnorm_mxfp8(const void* x, const void* residual, fp4q_dtype d
  *   dsum   [rows][cols] of type dt or NULL: the gradient that reaches s from elsewhere (the
  *          residual stream).
  *   dx     [rows][cols] of type dt; may be dy or dsum itself (in place).
- *   dgain  device float [cols].  Summed in a fixed order: the same inputs give the same bits.
+ *   dgain  device float [cols].  Summed in a fixed order (the same inputs give the same bits) and in runs of
+ *          rows: within 103 + rows / 2^14 fp32 roundings of the sum of the terms' magnitudes.
  *   scratch  device memory of at least fp4q_rmsnorm_backward_scratch(rows, cols) bytes, 16-byte
  *          aligned; its contents before and after the call mean nothing.
  * Shapes and alignment as fp4q_rmsnorm_mxfp8.
