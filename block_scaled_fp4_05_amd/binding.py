@@ -517,7 +517,10 @@ def _at(stream, dev: int, *made) -> int:
     not handed out again by the allocator before that stream has passed the call."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
-    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if not isinstance(stream, int):
+        s = stream
+    else:   # (an ExternalStream of 0 would be a new stream)
+        s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(dev)
     for t in made:
         if t is not None:
             t.record_stream(s)
