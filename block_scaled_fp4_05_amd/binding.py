@@ -512,19 +512,36 @@ def _matrix(name: str, t, dtypes) -> tuple[int, int, int]:
     return rows, cols, dev
 
 
-def _at(stream, dev: int, *made) -> int:
-    """The stream's handle.  Memory `made` for a call on a stream that is not the current one is
-    not handed out again by the allocator before that stream has passed the call."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+def _tensors(values):
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            if v.is_cuda:
+                yield v
+        elif isinstance(v, dict):
+            yield from _tensors(v.values())
+
+
+def _elsewhere(stream, helper, *args):
+    """helper(*args) on a stream (or its handle) that need not be the current one.  The call's memory comes
+    from that stream: what the allocator hands out for the current one may still be in use there.
+    It hands out the arguments' memory, and the results', only after both streams have passed their uses."""
     if not isinstance(stream, int):
         s = stream
     else:   # (an ExternalStream of 0 would be a new stream)
-        s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(dev)
-    for t in made:
-        if t is not None:
-            t.record_stream(s)
-    return s.cuda_stream
+        s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    caller = torch.cuda.current_stream(s.device)
+    with torch.cuda.stream(s):
+        out = helper(*args)
+    for t in _tensors(args):
+        t.record_stream(s)
+    for t in _tensors((out,) if isinstance(out, (torch.Tensor, dict)) else out):
+        t.record_stream(caller)
+    return out
+
+
+def _here(dev: int) -> int:
+    """The current stream's handle."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _done(fn: str, status: int) -> None:
@@ -534,23 +551,27 @@ def _done(fn: str, status: int) -> None:
 
 def quantize_mxfp8(x: torch.Tensor, stream=None) -> dict:
     """MXFP8: codes [rows][cols] (E4M3), E8M0 scales [rows][cols/32]."""
+    if stream is not None:
+        return _elsewhere(stream, quantize_mxfp8, x)
     rows, cols, dev = _matrix("x", x, _NAMES)
     codes = torch.empty_like(x, dtype=_U8)
     scales = codes.new_empty(rows, cols // 32)
     _done("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
         x.data_ptr(), _NAMES[x.dtype], rows, cols, codes.data_ptr(), scales.data_ptr(),
-        _at(stream, dev, codes, scales)))
+        _here(dev)))
     return {"codes": codes, "scales": scales}
 
 
 def dequantize_mxfp8(q: dict, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """The values of MXFP8 codes and scales as quantize_mxfp8 returns them."""
+    if stream is not None:
+        return _elsewhere(stream, dequantize_mxfp8, q, out_dtype)
     codes = q["codes"]
     rows, cols, dev = _matrix("codes", codes, (_U8,))
     scales = _need("scales", q["scales"], _U8, (rows, cols // 32), dev)
     y = torch.empty_like(codes, dtype=out_dtype)
     _done("fp4q_dequantize_mxfp8", lib().fp4q_dequantize_mxfp8(
-        codes.data_ptr(), scales, rows, cols, _dt(y), y.data_ptr(), _at(stream, dev, y)))
+        codes.data_ptr(), scales, rows, cols, _dt(y), y.data_ptr(), _here(dev)))
     return y
 
 
@@ -560,6 +581,8 @@ def rmsnorm_mxfp8(x: torch.Tensor, gain: torch.Tensor, residual: torch.Tensor | 
 
     Returns codes, scales, rstd, sum (x + residual in x's type; x itself without a residual)
     and, with ``with_y``, the unquantized y.  ``in_place`` writes the sum over `residual`."""
+    if stream is not None:
+        return _elsewhere(stream, rmsnorm_mxfp8, x, gain, residual, eps, with_y, in_place)
     rows, cols, dev = _matrix("x", x, _NAMES)
     gp = _need("gain", gain, _F32, (cols,), dev)
     rp = None if residual is None else _need("residual", residual, x.dtype, x.shape, dev)
@@ -571,7 +594,7 @@ def rmsnorm_mxfp8(x: torch.Tensor, gain: torch.Tensor, residual: torch.Tensor | 
     _done("fp4q_rmsnorm_mxfp8", lib().fp4q_rmsnorm_mxfp8(
         x.data_ptr(), rp, _NAMES[x.dtype], rows, cols, gp, eps, codes.data_ptr(), scales.data_ptr(),
         None if rp is None else total.data_ptr(), rstd.data_ptr(), None if y is None else y.data_ptr(),
-        _at(stream, dev, codes, scales, rstd, total, y)))
+        _here(dev)))
     out = {"codes": codes, "scales": scales, "rstd": rstd, "sum": total}
     if with_y:
         out["y"] = y
@@ -582,6 +605,8 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gain: torch.Tensor, rstd
                      dsum: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """(dx, dgain) of rmsnorm_mxfp8 from its `sum` and `rstd`; `dsum` is the gradient that reaches
     the sum from elsewhere, added to dx."""
+    if stream is not None:
+        return _elsewhere(stream, rmsnorm_backward, dy, s, gain, rstd, dsum)
     rows, cols, dev = _matrix("dy", dy, _NAMES)
     sp = _need("s", s, dy.dtype, dy.shape, dev)
     gp = _need("gain", gain, _F32, (cols,), dev)
@@ -592,13 +617,15 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gain: torch.Tensor, rstd
     scratch = gain.new_empty(need // 4)
     _done("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
         dy.data_ptr(), sp, up, _NAMES[dy.dtype], rows, cols, gp, rp, dx.data_ptr(), dgain.data_ptr(),
-        scratch.data_ptr(), need, _at(stream, dev, dx, dgain, scratch)))
+        scratch.data_ptr(), need, _here(dev)))
     return dx, dgain
 
 
 def gemm_mxfp8_mxfp4(a: dict, b: dict, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """C = A B^T for an MXFP8 operand (quantize_mxfp8, rmsnorm_mxfp8) and a row-wise MXFP4 one
     (quantize_mxfp4); k (a multiple of 128) is the columns of both."""
+    if stream is not None:
+        return _elsewhere(stream, gemm_mxfp8_mxfp4, a, b, out_dtype)
     ac, bc = a["codes"], b["codes"]
     m, k, dev = _matrix("a codes", ac, (_U8,))
     n = bc.shape[0] if isinstance(bc, torch.Tensor) and bc.dim() == 2 else 0
@@ -607,7 +634,7 @@ def gemm_mxfp8_mxfp4(a: dict, b: dict, out_dtype=torch.float32, stream=None) -> 
     bsp = _need("b scales", b["scales"], _U8, (n, k // 32), dev)
     c = torch.empty(m, n, dtype=out_dtype, device=ac.device)
     _done("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
-        ac.data_ptr(), asp, bcp, bsp, m, n, k, _dt(c), c.data_ptr(), _at(stream, dev, c)))
+        ac.data_ptr(), asp, bcp, bsp, m, n, k, _dt(c), c.data_ptr(), _here(dev)))
     return c
 
 
@@ -620,6 +647,8 @@ def moe_mxfp4(x: dict, w13: dict, w2: dict, topk: int, router_x: torch.Tensor | 
     [experts][d][hidden/2] with their scales [..][/32].  Either `router_x` [tokens][d] and
     `router_w` [experts][d] (bfloat16 or float32): the layer routes; or `ids` (int32) and
     `weights` (float32) [tokens][topk], as another router chose them.  Returns y, ids, weights."""
+    if stream is not None:
+        return _elsewhere(stream, moe_mxfp4, x, w13, w2, topk, router_x, router_w, ids, weights, out_dtype)
     xc, w2c = x["codes"], w2["codes"]
     tokens, d, dev = _matrix("x codes", xc, (_U8,))
     if not isinstance(w2c, torch.Tensor) or w2c.dim() != 3:
@@ -649,5 +678,5 @@ def moe_mxfp4(x: dict, w13: dict, w2: dict, topk: int, router_x: torch.Tensor | 
     scratch = xc.new_empty(need)
     _done("fp4q_moe_mxfp4", lib().fp4q_moe_mxfp4(
         xc.data_ptr(), xsp, rxp, rwp, rdt, w13p, w13sp, w2p, w2sp, tokens, d, hidden, experts, topk, mode, ip, wp,
-        _dt(y), y.data_ptr(), scratch.data_ptr(), need, _at(stream, dev, y, ids, weights, scratch)))
+        _dt(y), y.data_ptr(), scratch.data_ptr(), need, _here(dev)))
     return {"y": y, "ids": ids, "weights": weights}
