@@ -393,9 +393,9 @@ fp4q_status fp4q_dequantize(fp4q_format fmt, const uint8_t* codes, const uint8_t
 
 fp4q_status fp4q_quantize_mxfp8(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, uint8_t* codes,
                                 uint8_t* scales, hipStream_t stream) {
+  if (!mx_shape(rows, cols)) return FP4Q_E_SHAPE;   // before the pointers: an empty tensor may have none
   if (!x || !codes || !scales) return FP4Q_E_NULL;
   if (!valid_dtype(dt)) return FP4Q_E_ARG;
-  if (!mx_shape(rows, cols)) return FP4Q_E_SHAPE;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return FP4Q_E_ALIGN;
   fp4q::launch_mxfp8(x, dt, rows, cols, codes, scales, stream);
   return after_launch();
@@ -403,9 +403,9 @@ fp4q_status fp4q_quantize_mxfp8(const void* x, fp4q_dtype dt, int64_t rows, int6
 
 fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                                   fp4q_dtype out_dt, void* y, hipStream_t stream) {
+  if (!mx_shape(rows, cols)) return FP4Q_E_SHAPE;
   if (!codes || !scales || !y) return FP4Q_E_NULL;
   if (!valid_dtype(out_dt)) return FP4Q_E_ARG;
-  if (!mx_shape(rows, cols)) return FP4Q_E_SHAPE;
   if (!aligned16(codes) || !aligned16(scales) || !aligned16(y)) return FP4Q_E_ALIGN;
   fp4q::launch_dequant_mxfp8(codes, scales, rows, cols, out_dt, y, stream);
   return after_launch();
@@ -414,9 +414,9 @@ fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, i
 fp4q_status fp4q_rmsnorm_mxfp8(const void* x, const void* residual, fp4q_dtype dt, int64_t rows, int64_t cols,
                                const float* gain, float eps, uint8_t* codes, uint8_t* scales, void* sum,
                                float* rstd, void* y, hipStream_t stream) {
+  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return FP4Q_E_SHAPE;
   if (!x || !gain || !codes || !scales) return FP4Q_E_NULL;
   if (!valid_dtype(dt) || !(eps >= 0.0f) || eps > FLT_MAX) return FP4Q_E_ARG;
-  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return FP4Q_E_SHAPE;
   if (!aligned16(x) || !aligned16(residual) || !aligned16(gain) || !aligned16(codes) || !aligned16(scales) ||
       !aligned16(sum) || !aligned4(rstd) || !aligned16(y))
     return FP4Q_E_ALIGN;
@@ -432,9 +432,9 @@ int64_t fp4q_rmsnorm_backward_scratch(int64_t rows, int64_t cols) {
 fp4q_status fp4q_rmsnorm_backward(const void* dy, const void* s, const void* dsum, fp4q_dtype dt, int64_t rows,
                                   int64_t cols, const float* gain, const float* rstd, void* dx, float* dgain,
                                   void* scratch, int64_t scratch_bytes, hipStream_t stream) {
+  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return FP4Q_E_SHAPE;
   if (!dy || !s || !gain || !rstd || !dx || !dgain || !scratch) return FP4Q_E_NULL;
   if (!valid_dtype(dt)) return FP4Q_E_ARG;
-  if (!mx_shape(rows, cols) || cols > FP4Q_NORM_MAX_COLS) return FP4Q_E_SHAPE;
   if (scratch_bytes < fp4q::rmsnorm_backward_scratch(rows, cols)) return FP4Q_E_ARG;
   if (!aligned16(dy) || !aligned16(s) || !aligned16(dsum) || !aligned16(gain) || !aligned4(rstd) || !aligned16(dx) ||
       !aligned16(dgain) || !aligned16(scratch))
@@ -446,11 +446,11 @@ fp4q_status fp4q_rmsnorm_backward(const void* dy, const void* s, const void* dsu
 fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* b_codes,
                                   const uint8_t* b_scales, int64_t m, int64_t n, int64_t k, fp4q_dtype out_dt,
                                   void* c, hipStream_t stream) {
-  if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return FP4Q_E_NULL;
-  if (!valid_dtype(out_dt)) return FP4Q_E_ARG;
   const int64_t lim = (int64_t)1 << 31;
   if (m <= 0 || n <= 0 || k < 128 || k % 128 != 0 || m >= lim || n >= lim || k > ((int64_t)1 << 25))
     return FP4Q_E_SHAPE;
+  if (!a_codes || !a_scales || !b_codes || !b_scales || !c) return FP4Q_E_NULL;
+  if (!valid_dtype(out_dt)) return FP4Q_E_ARG;
   if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(c))
     return FP4Q_E_ALIGN;
   if (!fp4q::launch_gemm_mxfp8_mxfp4(a_codes, a_scales, b_codes, b_scales, m, n, k, out_dt == FP4Q_BF16, c, stream))
@@ -469,12 +469,12 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
                            unsigned route_mode, int32_t* ids, float* weights, fp4q_dtype out_dt, void* y,
                            void* scratch, int64_t scratch_bytes, hipStream_t stream) {
   const bool route = route_mode == FP4Q_ROUTE_COMPUTE;
+  if (!moe_shape(tokens, d, hidden, experts, topk)) return FP4Q_E_SHAPE;
   if (!x_codes || !x_scales || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !ids || !weights || !y ||
       !scratch || (route && (!router_x || !router_w)))
     return FP4Q_E_NULL;
   if (!valid_dtype(out_dt) || (!route && route_mode != FP4Q_ROUTE_GIVEN) || (route && !valid_dtype(router_dt)))
     return FP4Q_E_ARG;
-  if (!moe_shape(tokens, d, hidden, experts, topk)) return FP4Q_E_SHAPE;
   if (scratch_bytes < fp4q::moe_scratch(tokens, d, hidden, experts, topk)) return FP4Q_E_ARG;
   if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w13_codes) || !aligned16(w13_scales) ||
       !aligned16(w2_codes) || !aligned16(w2_scales) || !aligned4(ids) || !aligned4(weights) || !aligned16(y) ||
