@@ -36,3 +36,15 @@ def test_nothing_is_written_past_the_last_row():
     assert torch.equal(c[m * n - 300:m * n], B.gemm_mxfp8_mxfp4(a, last, torch.bfloat16)[0])
     del codes, scales, c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 4096), (16, 4096, 1152), (32, 8200, 4096), (64, 4096, 2048), (193, 4099, 4224),
+                                   (1000, 1000, 1024), (2048, 4096, 4096)])
+def test_the_same_bits_on_every_call(m, n, k):
+    g = torch.Generator(device=DEV).manual_seed(m)
+    a = B.quantize_mxfp8(torch.randn(m, k, device=DEV, generator=g))
+    b = B.quantize_mxfp4(torch.randn(n, k, device=DEV, generator=g))
+    print("gemm8", m, n, k, flush=True)
+    c = B.gemm_mxfp8_mxfp4(a, b)
+    for _ in range(8):
+        assert torch.equal(B.gemm_mxfp8_mxfp4(a, b), c)
