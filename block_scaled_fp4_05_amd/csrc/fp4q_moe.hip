@@ -384,8 +384,9 @@ __global__ __launch_bounds__(64 * W, G == 4 ? 2 : G == 2 ? 3 : 4) void k_moe_up(
   if constexpr (ROUTE) e = choice_of_one(a, blockIdx.y, r);
   else if (by_choice) e = a.ids[blockIdx.y];
   if (e < 0 || e >= a.experts) return;
-  // The first weights travel while the expert's tokens are looked up, where few workgroups turn
-  // out to have none (2 choices per expert: one in seven).
+  // The first weights travel while the expert's tokens are looked up, where few workgroups turn out to
+  // have none (2 choices per expert: one in seven).  us of the layer without / with, 64 tokens: 4 of 32, d
+  // 4096 95.8 / 93.5; 4, 3 and 2 of 128, d 2048 82.1 / 81.6, 73.2 / 76.6 and 62.2 / 69.0.
   const bool early = ROUTE || a.tokens * a.topk >= 2 * a.experts;
   const UpRows rows = up_rows(a, e, h0);
   UpWeights ahead;
@@ -656,15 +657,26 @@ __global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(Moe a) {
 }
 
 // Row tiles per workgroup of the down product: with many tokens two, so that each hidden fragment
-// loaded is multiplied twice.
+// loaded is multiplied twice (us of the layer with one / two, 4 of 32 experts, d 4096: 64 tokens 97.7 / 94,
+// 24 tokens 88.2 / 86; 16 tokens 84.5 / 81.7, 4 tokens 44.8 / 45.1, 2 tokens 25.7 / 27.0).
 constexpr int row_tiles(int tokens) { return tokens <= 16 ? 1 : 2; }
 
-// Groups of 16 tokens that a pass over an expert's weights takes: from the mean number of tokens
-// per expert, so that a second pass (from L2) is rare, with as few registers as that allows (us with
-// one / two groups at a mean of 8: 64 tokens, 4 of 32 experts, d 4096 104 / 119).
+// Groups of 16 tokens that a pass over an expert's weights takes, from the mean number of tokens per
+// expert: a further pass reads them from L2, more groups take registers from the loads in flight (and
+// multiply columns that few experts fill).  us of the layer with one / two / four groups, 64 tokens, d 4096
+// and hidden 2048, then d 2048 and hidden 1024:
+//   mean  8 (4 of 32, 8 of 64)  94 / 109 / -      59 / 73 / 95
+//   mean 16 (4 of 16)           69 /  71 / 82     32 / 36 / 42
+//   mean 21, 25 (4 of 12, of 10)  - / 57 / 77     33 / 36 / 43
+//   mean 32 (4 of 8)            55 /  59 / 58     30 / 31 / 32
+//   mean 42 (4 of 6)            63 /  68 / 65     33 / 33 / 32
+//   mean 64 (8 of 8)            79 /  81 / 78     45 / 43 / 45
+//   mean 64 (4 of 4)            52 /  48 / 47     32 / 29 / 30
+// (32 tokens, d 4096, mean 32, 4 of 4: 34 / 32.)  A hot expert costs little: that all 64 tokens of 4 of 32
+// choose one, which takes four passes over it, 99 us against 94.
 int groups(const Moe& a) {
   const int mean = a.tokens * a.topk / a.experts;
-  return a.tokens <= 16 || mean <= 8 ? 1 : a.tokens <= 32 || mean <= 20 ? 2 : 4;
+  return a.tokens <= 16 || mean <= 16 ? 1 : a.tokens <= 32 || mean <= 32 ? 2 : 4;
 }
 
 template <int G, bool ROUTE>

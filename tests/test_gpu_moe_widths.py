@@ -71,11 +71,14 @@ def _exact(x, w13, w2, ids, weights):
 
 #  tokens, d, hidden, experts, topk, hot (every token's first choice is one expert)
 CASES = [
-    (64, 1024, 2048, 16, 4, False),   # two groups of tokens, four waves, two K steps each; down in four parts
-    (64, 4096, 2048, 16, 4, False),   # eight steps each
-    (64, 1152, 2048, 16, 4, True),    # nine steps over four waves; a hot expert
-    (64, 4096, 512, 16, 4, False),    # two groups, eight waves
-    (64, 2304, 2176, 8, 4, False),    # four groups, four waves, 18 steps; down in two parts
+    (64, 1024, 2048, 16, 4, False), (64, 4096, 2048, 16, 4, False), (64, 1152, 2048, 16, 4, True),
+    (64, 4096, 512, 16, 4, False), (64, 2304, 2176, 8, 4, False),
+    (64, 1024, 2048, 12, 4, False),   # two groups of tokens, four waves, two K steps each; down in three parts
+    (64, 4096, 2048, 12, 4, False),   # eight steps each; down in two parts
+    (64, 1152, 2048, 12, 4, True),    # nine steps over four waves; a hot expert
+    (64, 4096, 512, 12, 4, False),    # two groups, eight waves
+    (32, 1280, 4352, 4, 4, False),    # two groups, 32 tokens, four waves
+    (64, 2304, 2816, 6, 4, False),    # four groups, four waves, 18 steps; down in two parts
     (64, 4096, 1024, 8, 8, False),    # four groups, eight waves
     (64, 2816, 1024, 32, 4, False),   # one group, four waves, 22 steps
     (64, 2816, 1024, 32, 4, True),    # one group, four passes over a hot expert
