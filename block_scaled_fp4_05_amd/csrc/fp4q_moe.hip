@@ -365,7 +365,7 @@ __device__ void up_tiles(const Moe& a, const UpRows& rows, int h0, const uint16_
 // travel while another's are multiplied.  The activation stays fp32 until its one rounding to MXFP8, the
 // form in which the down product takes it.  G: groups of 16 tokens per pass over the expert's weights.
 // ROUTE: one token, whose choices come from the logits and are written to a.ids.
-// (Bounds: 128 registers spill with G = 2: 64 tokens, 4 of 16 experts, d 4096 took 91 us against 84.)
+// (Bounds: 128 registers spill with G = 2: 64 tokens, 4 of 12 experts, d 4096 took 67.5 us against 57.2.)
 template <int G, int W, bool ROUTE>
 __global__ __launch_bounds__(64 * W, G == 4 ? 2 : G == 2 ? 3 : 4) void k_moe_up(Moe a) {
   __shared__ UpPlace places[W];
@@ -665,15 +665,16 @@ constexpr int row_tiles(int tokens) { return tokens <= 16 ? 1 : 2; }
 // expert: a further pass reads them from L2, more groups take registers from the loads in flight (and
 // multiply columns that few experts fill).  us of the layer with one / two / four groups, 64 tokens, d 4096
 // and hidden 2048, then d 2048 and hidden 1024:
-//   mean  8 (4 of 32, 8 of 64)  94 / 109 / -      59 / 73 / 95
-//   mean 16 (4 of 16)           69 /  71 / 82     32 / 36 / 42
-//   mean 21, 25 (4 of 12, of 10)  - / 57 / 77     33 / 36 / 43
-//   mean 32 (4 of 8)            55 /  59 / 58     30 / 31 / 32
-//   mean 42 (4 of 6)            63 /  68 / 65     33 / 33 / 32
-//   mean 64 (8 of 8)            79 /  81 / 78     45 / 43 / 45
-//   mean 64 (4 of 4)            52 /  48 / 47     32 / 29 / 30
-// (32 tokens, d 4096, mean 32, 4 of 4: 34 / 32.)  A hot expert costs little: that all 64 tokens of 4 of 32
-// choose one, which takes four passes over it, 99 us against 94.
+//   mean  8 (4 of 32, 8 of 64)   92 / 109 / 139    60 / 73 / 94
+//   mean 16 (4 of 16)            68 /  71 / 82      32 / 31 / 37
+//   mean 19 (4 of 13)            67 /  65 / 78      37 / 35 / 44
+//   mean 25 (4 of 10)            61 /  56 / 70      33 / 33 / 39
+//   mean 32 (4 of 8)             56 /  55 / 53      30 / 31 / 32
+//   mean 42 (4 of 6)             62 /  62 / 61      33 / 33 / 32
+//   mean 64 (8 of 8)             79 /  71 / 67      45 / 43 / 45
+//   mean 64 (4 of 4)             53 /  48 / 47      32 / 29 / 30
+// (32 tokens, d 4096, mean 32, 4 of 4: 33.7 / 31.6.)  A hot expert costs little: that all 64 tokens of 4
+// of 32 choose one, which takes four passes over it, 98 us against 92.
 int groups(const Moe& a) {
   const int mean = a.tokens * a.topk / a.experts;
   return a.tokens <= 16 || mean <= 16 ? 1 : a.tokens <= 32 || mean <= 32 ? 2 : 4;
@@ -681,12 +682,14 @@ int groups(const Moe& a) {
 
 template <int G, bool ROUTE>
 void run_up(const Moe& a, hipStream_t st) {
-  // Waves per workgroup: eight where each has four K steps then and 16 waves fit a CU (G = 1), or where
-  // there are too few workgroups to fill the GPU with four (us of the whole layer, four / eight waves: 64
-  // tokens, d 4096, 4 of 32 experts 104.3 / 101.2, 4 of 16 (G = 2) 78.3 / 82.7; 64 tokens, d 2048, 8 of 64
-  // 73.3 / 81.3, 4 of 8 39.2 / 37.7).
+  // Waves per workgroup: eight where all workgroups are on the GPU at once then (16 waves of G = 1 fit a
+  // CU by their registers, 12 or 8 of the others, and so two workgroups of eight or one); else four, which
+  // leave a CU fewer waves at a time without loads in flight.  us of the layer with four / eight, 64 tokens, d 4096:
+  // G = 1, hidden 2048, 8 of 64, 4 of 32, 4 of 16 172 / 181, 92 / 94, 68 / 69, hidden 1024, 4 of 16 42.7 / 41.3; G = 2,
+  // hidden 2048, 4 of 12, 4 of 8 57 / 65, 55 / 60, hidden 1024, 4 of 8 43 / 39; G = 4, hidden 2048, 8 of 8, 4 of 4
+  // 67 / 78, 53 / 48.  One token, 4 of 32: 20.0 / 19.5.
   const dim3 grid(a.hidden / 32, a.slots);
-  const bool eight = (G == 1 && a.d >= 8 * 4 * 128) || (int64_t)grid.x * grid.y <= 2 * kCus;
+  const bool eight = (int64_t)grid.x * grid.y <= (G == 1 ? 2 : 1) * kCus;
   if (eight) k_moe_up<G, 8, ROUTE><<<grid, 512, 0, st>>>(a);
   else k_moe_up<G, 4, ROUTE><<<grid, 256, 0, st>>>(a);
 }

@@ -76,13 +76,14 @@ CASES = [
     (64, 1024, 2048, 12, 4, False),   # two groups of tokens, four waves, two K steps each; down in three parts
     (64, 4096, 2048, 12, 4, False),   # eight steps each; down in two parts
     (64, 1152, 2048, 12, 4, True),    # nine steps over four waves; a hot expert
-    (64, 4096, 512, 12, 4, False),    # two groups, eight waves
+    (64, 4096, 512, 12, 4, False),    # two groups, eight waves, four steps each
     (32, 1280, 4352, 4, 4, False),    # two groups, 32 tokens, four waves
     (64, 2304, 2816, 6, 4, False),    # four groups, four waves, 18 steps; down in two parts
     (64, 4096, 1024, 8, 8, False),    # four groups, eight waves
     (64, 2816, 1024, 32, 4, False),   # one group, four waves, 22 steps
     (64, 2816, 1024, 32, 4, True),    # one group, four passes over a hot expert
-    (64, 4096, 1024, 32, 4, False),   # one group, eight waves, four steps each
+    (64, 4096, 1024, 32, 4, False),   # one group, four waves, eight steps each
+    (64, 8192, 512, 30, 4, False),    # one group, eight waves, eight steps each
     (24, 8192, 256, 32, 4, True),     # eight steps each; two passes
     (33, 4224, 640, 24, 3, False),    # 33 steps over eight waves
     (17, 2048, 1024, 64, 8, False), (8, 4096, 2048, 32, 4, False), (3, 2944, 1024, 16, 2, False),
