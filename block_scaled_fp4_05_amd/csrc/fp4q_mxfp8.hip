@@ -324,7 +324,8 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
 // (16.8 MB from the last-level cache).
 constexpr int kRun = 64;
 
-template <typename T, int V>
+// RUNS: more than one run (see BackwardRuns).
+template <typename T, int V, bool RUNS>
 __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T* __restrict__ s_in, const T* dsum,
                                                            int rows, int cols, const float* gain,
                                                            const float* __restrict__ rstd, T* dx,
@@ -354,7 +355,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
         for (int i = 0; i < N; i += 4) {
           f32x4_t v = {dg[j][i], dg[j][i + 1], dg[j][i + 2], dg[j][i + 3]};
           f32x4_t* p = reinterpret_cast<f32x4_t*>(to + c * N + i);
-          if (later) v += *p;
+          if (RUNS && later) v += *p;
           *p = v;
         }
       }
@@ -417,9 +418,10 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_backward(const T* dy, const T*
       }
       if (c < chunks) store_chunk_nt(dx + at + c * N, pack(u));
     }
-    if (++run == kRun) end_run();
+    if constexpr (RUNS)
+      if (++run == kRun) end_run();
   }
-  if (run > 0) end_run();   // (every workgroup has a row: see backward_groups)
+  if (!RUNS || run > 0) end_run();   // (every workgroup has a row: see backward_groups)
 }
 
 // dgain[c] = sum over the partial rows: 32 columns per workgroup, 32 threads per column, each
@@ -477,9 +479,16 @@ template <typename T, int V>
 struct NormKernel {
   static auto fn() { return k_rmsnorm<T, V>; }
 };
+// The gradient with more than one run: where a workgroup has more than kRun rows, and for fp32 rows of more
+// than 16384 columns, whose registers spill less in that form (4096 x 20000 351 us, one run 433). Elsewhere
+// it costs registers: bf16 4096 x 20000 177 us, one run 158.
 template <typename T, int V>
-struct BackwardKernel {
-  static auto fn() { return k_rmsnorm_backward<T, V>; }
+struct BackwardRuns {
+  static auto fn() { return k_rmsnorm_backward<T, V, true>; }
+};
+template <typename T, int V>
+struct BackwardOnce {
+  static auto fn() { return k_rmsnorm_backward<T, V, V == 8>; }
 };
 
 // Workgroups of the gradient, each with its row of partial sums: what the card holds at once (four
@@ -503,8 +512,8 @@ void rmsnorm_backward(const T* dy, const T* s_in, const T* dsum, int64_t rows, i
                       const float* rstd, T* dx, float* dgain, float* partial, hipStream_t st) {
   const RowShape s = row_shape<T>(cols);
   const int grid = (int)backward_groups(rows, cols);
-  by_chunks<BackwardKernel, T>(s.v)<<<grid, s.threads, 0, st>>>(dy, s_in, dsum, (int)rows, (int)cols, gain, rstd, dx,
-                                                                partial);
+  const auto kernel = rows > (int64_t)kRun * grid ? by_chunks<BackwardRuns, T>(s.v) : by_chunks<BackwardOnce, T>(s.v);
+  kernel<<<grid, s.threads, 0, st>>>(dy, s_in, dsum, (int)rows, (int)cols, gain, rstd, dx, partial);
   k_rmsnorm_dgain<<<(unsigned)(cols / 32), 1024, 0, st>>>(partial, grid, (int)cols, dgain);
 }
 
