@@ -392,17 +392,20 @@ fp4q_status fp4q_dequantize_mxfp8(const uint8_t* codes, const uint8_t* scales, i
  * Residual addition, root-mean-square norm and MXFP8 in one read of x:
  *   s = x + residual (x without one),  r = 1 / sqrt(mean(s^2) + eps),  n = (s r) gain,
  *   codes, scales = MXFP8(n) as fp4q_quantize_mxfp8 writes it.
- * From the unrounded s (an fp32 sum); n is the product of s, r and gain rounded once, with r held to
- * twice fp32's precision, so codes differ from the exact ones only within an fp32 rounding of a
- * boundary.  A row's results do not depend on the other rows or their number.
+ * From the unrounded s (an fp32 sum).  n is the product of s, r and gain, with r held to twice fp32's
+ * precision; codes and scales are rounded from that product and not from its fp32 rounding, so they differ
+ * from the exact ones only where the fp32 sum of squares moves n across a boundary (about one code in 10^7).
+ * A row's results do not depend on the other rows or their number.
  *   x, residual  [rows][cols] of type dt; residual may be NULL.
  *   gain         device float [cols].        eps >= 0, finite.
  *   sum          s in type dt, or NULL.  It may be x itself or residual itself (in place);
  *                no other overlap.
  *   rstd         device float [rows] or NULL: r, for fp4q_rmsnorm_backward.
- *   y            n in type dt, or NULL (e.g. a router's input).
- * A row with a NaN gives NaN codes throughout; a row with an element whose square overflows fp32
- * gives r = 0 (its finite elements 0, its infinite ones NaN), as the formula does.
+ *   y            n in type dt (rounded to nearest from its fp32 rounding), or NULL (e.g. a router's input).
+ * A row with a NaN gives NaN codes throughout.  Squares are added in fp32, 32 at most at a time: a row with
+ * elements past 3.2e18 may give r = 0 (its finite elements 0, its infinite ones NaN), which it does from
+ * 1.9e19 on, and elements below 1e-18 count for less than their squares, which only eps = 0 lets matter.
+ * A row of zeros with eps = 0 gives NaN codes (r is infinite).
  * Shapes: cols % 32 == 0, cols <= 32768, rows < 2^31.  Alignment: 16 bytes (rstd 4).
  */
 #define FP4Q_NORM_MAX_COLS 32768
