@@ -111,7 +111,7 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t (&w)[1]) 
 // -----------------------------------------------------------------------------------------
 // Quantizer: a stream over the chunks of the whole tensor (cols % 32 == 0, so blocks and
 // chunks ignore the row boundaries).  Four chunks per thread, all loads first.  Bound by memory: bf16
-// 16384 x 4096 (203 MB) in 32.4 us, 6.3 TB/s; a few rows take one launch (2.9 us).
+// 16384 x 4096 (203 MB) in 32.3 us, 6.3 TB/s; fp32 (338 MB) 54 us, 6.2 TB/s; a few rows take one launch (2.9 us).
 // -----------------------------------------------------------------------------------------
 constexpr int kQuantChunks = 4;   // chunks per thread
 
@@ -140,7 +140,8 @@ __global__ __launch_bounds__(256) void k_mxfp8(const T* __restrict__ x, int64_t 
   }
 }
 
-// Eight codes per lane.
+// Eight codes per lane.  Bound by memory: 16384 x 4096 to bf16 33 us, 6.1 TB/s; to fp32, two 16-byte stores 32
+// bytes apart per lane, 99 us, 3.4 TB/s.
 template <bool BF16OUT>
 __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales, int64_t n8,
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict
 // t + NT j for thread t), so x is read once; it walks rows blockIdx.x, + gridDim.x, ... with
 // the gain in registers and the next row's loads in flight while this row is reduced.
 // Bound by memory: bf16 8192 x 4096 with residual and sum (236 MB) in 43 us, 5.5 TB/s; bf16 4096 x 8192
-// 41 us; fp32 8192 x 4096 73 us, 5.9 TB/s; one row 3.4 us, a launch and one trip to memory.  A row whose
+// 46 us; fp32 8192 x 4096 74 us, 5.8 TB/s; one row 3.7 us, a launch and one trip to memory.  A row whose
 // 32 elements per thread would need more than 256 threads is spread over more threads first: held by
 // 256, 4096 x 8192 took 77 us, with its registers spilled.
 // -----------------------------------------------------------------------------------------
@@ -216,26 +217,30 @@ __device__ __forceinline__ Root inverse_root(double v) {
 //
 // Rounded to fp32 and then to a code it would be rounded twice: n just past a point halfway between two
 // codes can land on it and go to the even one.  Those points, and the scale's boundaries (1.75 2^k), have at
-// most five significant bits, so only an n whose kBelowHalf bits are all zero can be wrong (one in 2^19); it
-// is moved to the next fp32 number on the side of the exact product, which rounds as that would.  Of the 33.5
+// most five significant bits, so only an n whose kBelowHalf last bits are all zero can be wrong (one in 2^19);
+// it is moved to the next fp32 number on the side of the exact product, which rounds as that would.  Of the 33.5
 // million codes of bf16 8192 x 4096 that leaves 2 or 3 other than the exact ones (the sum of squares is fp32),
-// where rounding twice left some 20, now and then with a scale and its block.  us without / with: 44.5 / 44.6
-// there, 44.0 / 45.9 for bf16 4096 x 8192, 51.3 / 55.7 for 1024 x 32768.
-constexpr uint32_t kBelowHalf = 0x7FFFFu;
+// where rounding twice left some 20, now and then with a scale and its block.  us without / with, with a residual:
+// bf16 8192 x 4096 44.2 / 42.4, 16384 x 2048 47.2 / 46.4, 4096 x 8192 44.0 / 44.6, 2048 x 16384 50.6 / 53.3, 1024 x 32768
+// 51 / 52.5; without one 16384 x 2048 29.9 / 31.4.
+constexpr int kBelowHalf = 19;
 struct Product {
   float p, e, gain;
   __device__ __forceinline__ Product(float s, Root r, float g)
       : p(s * r.hi), e(__builtin_fmaf(s, r.lo, __builtin_fmaf(s, r.hi, -(s * r.hi)))), gain(g) {}
-  // To nearest; zero without its sign.
-  __device__ __forceinline__ float rounded() const { return __builtin_fmaf(p, gain, e * gain); }
-  // With the sign of the product.
-  __device__ __forceinline__ float signed_zero(float n) const {
+  // To nearest; `zeros` rises to its trailing zeros, which a zero has none of (v_ffbl_b32 gives -1; a zero
+  // is common where a residual cancels).  The sign of a zero is the product's.
+  __device__ __forceinline__ float rounded(int& zeros) const {
+    const float n = __builtin_fmaf(p, gain, e * gain);
+    int t;   // (in place of a count that the compiler guards against zero)
+    asm("v_ffbl_b32 %0, %1" : "=v"(t) : "v"(n));
+    zeros = max(zeros, t);
     return __builtin_copysignf(n, __uint_as_float(__float_as_uint(p) ^ __float_as_uint(gain)));
   }
   __device__ __forceinline__ float beside_boundary(float n) const {
     const uint32_t b = __float_as_uint(n);
     const float over = __builtin_fmaf(e, gain, __builtin_fmaf(p, gain, -n)), m = __builtin_fabsf(n);   // over: what n leaves out
-    if ((b & kBelowHalf) != 0u || !(m > 0.0f && m < __builtin_inff()) || over == 0.0f) return n;
+    if ((b & ((1u << kBelowHalf) - 1u)) != 0u || !(m > 0.0f && m < __builtin_inff()) || over == 0.0f) return n;
     return __uint_as_float((over > 0.0f) == (n > 0.0f) ? b + 1u : b - 1u);
   }
 };
@@ -325,19 +330,15 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
       }
       const float* gj = g[HOLD ? j : 0];
       float n[N];
-      uint32_t low = ~0u;   // 0 where an n may be next to a boundary, or zero
+      int zeros = 0;   // most trailing zeros of an n
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        n[i] = Product(s[j][i], r, gj[i]).rounded();
-        low = min(low, __float_as_uint(n[i]) & kBelowHalf);
-      }
+      for (int i = 0; i < N; ++i) n[i] = Product(s[j][i], r, gj[i]).rounded(zeros);
       if (y && c < chunks) store_chunk_nt(y + at + c * N, pack(n));
-      if (__builtin_expect(__any(low == 0u && c < chunks), 0)) {
+      if (__builtin_expect(__any(zeros >= kBelowHalf), 0)) {
+        Root again = r;   // taken for another: the products are formed again, not kept in registers for this
+        asm volatile("" : "+v"(again.hi), "+v"(again.lo));
 #pragma unroll
-        for (int i = 0; i < N; ++i) n[i] = Product(s[j][i], r, gj[i]).signed_zero(n[i]);
-        if (y && c < chunks) store_chunk_nt(y + at + c * N, pack(n));
-#pragma unroll
-        for (int i = 0; i < N; ++i) n[i] = Product(s[j][i], r, gj[i]).beside_boundary(n[i]);
+        for (int i = 0; i < N; ++i) n[i] = Product(s[j][i], again, gj[i]).beside_boundary(n[i]);
       }
       uint32_t w[N / 4];
       const uint32_t code = mx8_encode<T>(n, w);
@@ -354,8 +355,8 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(const T* x, const T* res, int 
 // 1e13 and more, or 1e-13 and less.  The same walk; each workgroup also adds up dy s r over its rows, in registers
 // for kRun rows at a time and these runs in its row of partial sums (one running sum was off by 3400
 // roundings after 2^24 equal rows; runs keep that below 360), which k_rmsnorm_dgain adds in a fixed order.
-// Bound by memory: bf16 8192 x 4096 with dsum (268 MB) in 51 us, 5.3 TB/s, and 4.9 us for the partial sums
-// (16.8 MB from the last-level cache).
+// Bound by memory: bf16 8192 x 4096 with dsum (268 MB) in 51 us, 5.3 TB/s, and 5.0 us for the partial sums
+// (16.8 MB from the last-level cache); fp32 92 us, 5.8 TB/s, and 4.8.
 constexpr int kRun = 64;
 
 // RUNS: more than one run (see BackwardRuns).
