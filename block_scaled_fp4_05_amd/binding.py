@@ -108,7 +108,7 @@ def _p(t) -> int | None:
 
 
 def _s(stream) -> int | None:
-    if stream is None:   # the handle alone: building a Stream object takes 2.6 us, a third of a small call
+    if stream is None:   # the handle alone, by torch's own call for it: a Stream object takes 2.6 us, a third of a small call
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
@@ -477,6 +477,8 @@ def dequantize_variant(var: int, codes, scales, tensor_scale, rows: int, cols: i
 # These helpers check what the C entry points cannot see (the tensors' types, shapes, devices
 # and strides) before any address is passed on.  A decode step makes several such calls in a few
 # microseconds each, so they call the library directly and each check has a short way through.
+# Like the helpers above they take no part in autograd: results carry no gradient, whatever the
+# arguments require; rmsnorm_backward is called for one.
 
 _NAMES = {torch.float32: F32, torch.bfloat16: BF16}
 _U8, _F32 = torch.uint8, torch.float32
@@ -540,7 +542,7 @@ def _elsewhere(stream, helper, *args):
 
 
 def _here(dev: int) -> int:
-    """The current stream's handle."""
+    """The current stream's handle (see _s)."""
     return torch._C._cuda_getCurrentRawStream(dev)
 
 

@@ -22,7 +22,7 @@ namespace {
 // of A, n 28672, k 8192 58.5 / 38; 16 rows, n 4096, k 14336 16.5 / 12.5; one row, where A's lines
 // are few either way and DIRECT loads its fragments, n 28672, k 8192 33.4 / 26.2.)
 // Bound by reading B: one row, n 28672, k 8192 (125 MB) at 4.8 TB/s; below some 20 MB by the launch
-// and one trip to memory: one row, n 4096, k 4096 (8.9 MB) 4.2 us.
+// and one trip to memory: one row, n 4096, k 4096 (8.9 MB) 3.9 us.
 // -----------------------------------------------------------------------------------------
 template <int G, int NT, int WAVES, bool DIRECT, bool BF16OUT>
 __global__ __launch_bounds__(64 * WAVES, G == 1 && NT <= 2 ? 4 : 2) void k_gemm8_rows(const uint8_t* __restrict__ ac,
@@ -189,8 +189,9 @@ __global__ __launch_bounds__(64 * WAVES, G == 1 && NT <= 2 ? 4 : 2) void k_gemm8
 // elements: 128 bytes of A and 64 of B per row, copied straight into one of S LDS stages by
 // global_load_lds.
 // Bound, on large shapes, by the matrix cores with their copies beside them (an E4M3 operand runs at
-// the 8-bit rate): 8192^3 in 393 us, 2.8 PFLOP/s, MFMA busy 64 % of the cycles; on few tiles by the bytes
-// that a CU's copies bring in (about 32 per clock): 193 x 4099 x 4224 in 16.4 us on 132 of the 256 CUs.
+// the 8-bit rate): 8192^3 in 388 to 408 us from run to run, 2.7 to 2.8 PFLOP/s, MFMA busy 65 % of the cycles (to
+// fp32 415); with few tiles by each workgroup's own chain of K steps: 193 x 4099 x 4224 in 16.7 us, 33 steps of
+// half a microsecond on 132 of the 256 CUs, each bringing in 14 bytes per clock of the 32 it could.
 // -----------------------------------------------------------------------------------------
 
 // 16-byte chunk c of staged row r sits at position c ^ swz: 16 consecutive rows at one chunk

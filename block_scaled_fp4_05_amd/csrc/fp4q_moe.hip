@@ -13,9 +13,15 @@
 // matrix instruction's layout through LDS (deal): loads in that layout, 16 rows per 16 lanes, took
 // 62 us for the up product below and 39 for the down product.
 //
-// Measured, 64 tokens, 4 of 32 experts, d 4096, hidden 2048 (428 MB of weights), us: logits 4.7, top-k 4.7,
-// up 55 (285 MB, 5.2 TB/s), down 37 (143 MB, 3.8 TB/s).  One token, 4 of 64 experts, d 2048, hidden 1024
-// (14 MB): 3.2, -, 6.5, 5.8, each a launch and one trip to memory.
+// The 8-bit matrix arithmetic cuts a product about 13 bits below the largest of its group (fp4q_mx8.hpp).
+// In the gate and up sums (5e-6 to 1.2e-5 of their norm) that moves one hidden code of about a thousand across
+// a boundary of MXFP8: y before its rounding is 0.8e-3 (64 tokens) to 1.4e-3 (one) of its norm from the exact layer's,
+// and 1.8e-3 to 2.1e-3 after the rounding to bf16, which alone is 1.65e-3 away.  Sums that cut nothing would need
+// both operands widened to bf16 in registers first, and half of the matrix rate.
+//
+// Measured, 64 tokens, 4 of 32 experts, d 4096, hidden 2048 (428 MB of weights), us: logits 4.8, top-k 4.7,
+// up 52 (285 MB, 5.4 TB/s), down 37 (143 MB, 3.9 TB/s).  One token, 4 of 64 experts, d 2048, hidden 1024
+// (14 MB): 3.2, -, 7.3, 5.8, each a launch and one trip to memory, up and down on 128 of the 256 CUs.
 #include "fp4q_dev.hpp"
 #include "fp4q_mx8.hpp"
 

@@ -173,8 +173,8 @@ __global__ __launch_bounds__(256) void k_dequant_mxfp8(const uint8_t* __restrict
 // A workgroup keeps one row at a time in registers (V chunks per thread, chunk
 // t + NT j for thread t), so x is read once; it walks rows blockIdx.x, + gridDim.x, ... with
 // the gain in registers and the next row's loads in flight while this row is reduced.
-// Bound by memory: bf16 8192 x 4096 with residual and sum (236 MB) in 43 us, 5.5 TB/s; bf16 4096 x 8192
-// 46 us; fp32 8192 x 4096 74 us, 5.8 TB/s; one row 3.7 us, a launch and one trip to memory.  A row whose
+// Bound by memory: bf16 8192 x 4096 with residual and sum (236 MB) in 42 us, 5.6 TB/s; bf16 4096 x 8192
+// 44 us; fp32 8192 x 4096 74 us, 5.8 TB/s; one row 3.4 us, a launch and one trip to memory.  A row whose
 // 32 elements per thread would need more than 256 threads is spread over more threads first: held by
 // 256, 4096 x 8192 took 77 us, with its registers spilled.
 // -----------------------------------------------------------------------------------------
