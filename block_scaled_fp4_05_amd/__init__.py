@@ -11,4 +11,7 @@ from .binding import (  # noqa: F401
     fp4q_rht, fp4q_rht_signs_from_seed, fp4q_rmsnorm_backward, fp4q_rmsnorm_backward_scratch, fp4q_rmsnorm_mxfp8,
     fp4q_status_string, gemm_mxfp8_mxfp4, lib, moe_mxfp4, quantize_if4, quantize_mxfp4, quantize_mxfp8,
     quantize_nvfp4, quantize_nvfp4_2d, rht, rmsnorm_backward, rmsnorm_mxfp8, stream_workspace,
+    ATTN_ALL, ATTN_CAUSAL, ROTARY_BACKWARD, ROTARY_HALF, ROTARY_INTERLEAVED, attention_paged, fp4q_attention_paged,
+    fp4q_attention_paged_scratch, fp4q_kv_append, fp4q_rotary, fp4q_rotary_table, kv_append, kv_cache, rotary,
+    rotary_table,
 )

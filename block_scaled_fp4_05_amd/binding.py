@@ -32,7 +32,8 @@ EXPORTS = ["fp4q_workspace_create", "fp4q_workspace_destroy", "fp4q_workspace_se
            "fp4q_rht_signs_from_seed", "fp4q_status_string", "fp4q_abi_version",
            "fp4q_quantize_mxfp8", "fp4q_dequantize_mxfp8", "fp4q_rmsnorm_mxfp8", "fp4q_rmsnorm_backward",
            "fp4q_rmsnorm_backward_scratch", "fp4q_gemm_mxfp8_mxfp4", "fp4q_moe_mxfp4",
-           "fp4q_moe_scratch"]
+           "fp4q_moe_scratch", "fp4q_rotary", "fp4q_rotary_table", "fp4q_kv_append", "fp4q_attention_paged",
+           "fp4q_attention_paged_scratch"]
 
 
 class Fp4qError(RuntimeError):
@@ -43,7 +44,19 @@ class Fp4qError(RuntimeError):
 
 _lib = None
 _P, _I64, _U64, _I, _U = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64, ctypes.c_int, ctypes.c_uint
-_F = ctypes.c_float
+_F, _D = ctypes.c_float, ctypes.c_double
+
+
+class KvCache(ctypes.Structure):
+    """fp4q_kv_cache."""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("pages", _I64), ("page_size", _I64),
+                ("kv_heads", _I64), ("head_dim", _I64)]
+
+
+class KvBatch(ctypes.Structure):
+    """fp4q_kv_batch."""
+    _fields_ = [("q_starts", _P), ("kv_lens", _P), ("page_table", _P), ("seqs", _I64), ("max_pages", _I64), ("max_q_len", _I64),
+                ("max_kv_len", _I64), ("group_starts", _P), ("shared_lens", _P), ("groups", _I64), ("max_shared_len", _I64)]
 
 
 def lib() -> ctypes.CDLL:
@@ -84,6 +97,11 @@ def lib() -> ctypes.CDLL:
             "fp4q_moe_mxfp4": [_P, _P, _P, _P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _U, _P, _P, _I, _P,
                                _P, _I64, _P],
             "fp4q_moe_scratch": [_I64, _I64, _I64, _I64, _I64],
+            "fp4q_rotary": [_P, _I, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _U, _P, _I64, _I64, _P],
+            "fp4q_rotary_table": [_I64, _I64, _D, _D, _D, _D, _D, _D, _P, _P],
+            "fp4q_kv_append": [_P, _P, _I, _I64, _I64, _I64, _I64, _I64, _P, _I64, _I64, _U, _P, _P, _P, _P],
+            "fp4q_attention_paged": [_P, _I64, _I64, _I64, _I64, _P, _P, _F, _I64, _U, _P, _P, _P, _I64, _P],
+            "fp4q_attention_paged_scratch": [_P, _P, _I64, _I64, _I64],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -92,6 +110,7 @@ def lib() -> ctypes.CDLL:
         L.fp4q_rht_signs_from_seed.restype = None
         L.fp4q_rmsnorm_backward_scratch.restype = _I64
         L.fp4q_moe_scratch.restype = _I64
+        L.fp4q_attention_paged_scratch.restype = _I64
         L.fp4q_status_string.restype = ctypes.c_char_p
         _lib = L
     return _lib
@@ -315,6 +334,44 @@ def fp4q_moe_mxfp4(x_codes, x_scales, router_x, router_w, router_dt, w13_codes, 
 
 def fp4q_moe_scratch(tokens: int, d: int, hidden: int, experts: int, topk: int) -> int:
     return lib().fp4q_moe_scratch(tokens, d, hidden, experts, topk)
+
+
+ROTARY_HALF, ROTARY_INTERLEAVED, ROTARY_BACKWARD = 0, 1, 2
+ATTN_CAUSAL, ATTN_ALL = 0, 1
+
+
+def fp4q_rotary(x, dt, tokens, heads, head_dim, rot_dim, x_token_stride, x_head_stride, positions, table, table_rows,
+                mode, y, y_token_stride, y_head_stride, stream=None) -> int:
+    return _check("fp4q_rotary", lib().fp4q_rotary(
+        _p(x), dt, tokens, heads, head_dim, rot_dim, x_token_stride, x_head_stride, _p(positions), _p(table), table_rows,
+        mode, _p(y), y_token_stride, y_head_stride, _s(stream)))
+
+
+def fp4q_rotary_table(positions, rot_dim, base, factor, original, low, high, amplitude, table, stream=None) -> int:
+    return _check("fp4q_rotary_table", lib().fp4q_rotary_table(
+        positions, rot_dim, base, factor, original, low, high, amplitude, _p(table), _s(stream)))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def fp4q_kv_append(k, v, dt, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, table, table_rows,
+                   rot_dim, mode, positions, cache: KvCache, batch: KvBatch, stream=None) -> int:
+    return _check("fp4q_kv_append", lib().fp4q_kv_append(
+        _p(k), _p(v), dt, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride, _p(table), table_rows,
+        rot_dim, mode, _p(positions), _ref(cache), _ref(batch), _s(stream)))
+
+
+def fp4q_attention_paged(q, tokens, q_heads, q_token_stride, q_head_stride, cache: KvCache, batch: KvBatch, scale, window,
+                         mask, out, lse, scratch, scratch_bytes, stream=None) -> int:
+    return _check("fp4q_attention_paged", lib().fp4q_attention_paged(
+        _p(q), tokens, q_heads, q_token_stride, q_head_stride, _ref(cache), _ref(batch), scale, window, mask, _p(out),
+        _p(lse), _p(scratch), scratch_bytes, _s(stream)))
+
+
+def fp4q_attention_paged_scratch(cache: KvCache, batch: KvBatch, tokens: int, q_heads: int, window: int) -> int:
+    return lib().fp4q_attention_paged_scratch(_ref(cache), _ref(batch), tokens, q_heads, window)
 
 
 # --- allocation helpers --------------------------------------------------------------
@@ -682,3 +739,155 @@ def moe_mxfp4(x: dict, w13: dict, w2: dict, topk: int, router_x: torch.Tensor | 
         xc.data_ptr(), xsp, rxp, rwp, rdt, w13p, w13sp, w2p, w2sp, tokens, d, hidden, experts, topk, mode, ip, wp,
         _dt(y), y.data_ptr(), scratch.data_ptr(), need, _here(dev)))
     return {"y": y, "ids": ids, "weights": weights}
+
+
+# --- rotary positions, the paged MXFP8 cache and its attention ------------------------------
+#
+# A cache is a dict of k_codes, v_codes (uint8 [pages][kv heads][page size][head dim]) and k_scales,
+# v_scales ([..][head dim / 32]); a batch a dict of q_starts (int32 [sequences + 1]), kv_lens
+# ([sequences]), page_table ([sequences][pages per sequence]) and the bounds max_q_len and
+# max_kv_len, and for prefixes that groups of neighbouring sequences share also group_starts
+# ([groups + 1]), shared_lens ([groups]) and max_shared_len.  include/fp4q.h says what they mean.
+
+_I32 = torch.int32
+
+
+def _heads(name: str, t, dtypes) -> tuple[int, int, int, int, int, int]:
+    """(tokens, heads, head_dim, token stride, head stride, device index) of [tokens][heads][head_dim] on the current
+    device, the heads dense inside; the stride of an axis of one is 0."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name}: a tensor of {' or '.join(str(d) for d in dtypes)} is needed")
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name}: a tensor [tokens][heads][head_dim] on the GPU is needed")
+    (n, h, d), (sn, sh, sd) = t.shape, t.stride()
+    if sd != 1 and d > 1:
+        raise ValueError(f"{name}: the elements of a head have to be dense")
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: is on {t.device}, but device {torch.cuda.current_device()} is current "
+                         "(use torch.cuda.device)")
+    return n, h, d, sn if n > 1 else 0, sh if h > 1 else 0, dev
+
+
+def _table_rows(table, dev: int) -> tuple[int, int, int]:
+    """(address, rows, rotated elements) of a rotary table."""
+    if not isinstance(table, torch.Tensor) or table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError("table: a tensor [positions][pairs][2] of cosines and sines is needed")
+    return _need("table", table, _F32, table.shape, dev), table.shape[0], 2 * table.shape[1]
+
+
+def _kv_cache(cache: dict, dev: int) -> KvCache:
+    kc = cache["k_codes"]
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
+        raise ValueError("k_codes: a tensor [pages][kv heads][page size][head dim] is needed")
+    shape = kc.shape
+    pages, heads, page, dim = shape
+    scales = (pages, heads, page, dim // 32)
+    return KvCache(_need("k_codes", kc, _U8, shape, dev), _need("k_scales", cache["k_scales"], _U8, scales, dev),
+                   _need("v_codes", cache["v_codes"], _U8, shape, dev), _need("v_scales", cache["v_scales"], _U8, scales, dev),
+                   pages, page, heads, dim)
+
+
+def _kv_batch(batch: dict, dev: int) -> KvBatch:
+    table = batch["page_table"]
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("page_table: a tensor [sequences][pages] is needed")
+    seqs, width = table.shape
+    b = KvBatch(_need("q_starts", batch["q_starts"], _I32, (seqs + 1,), dev),
+                _need("kv_lens", batch["kv_lens"], _I32, (seqs,), dev), _need("page_table", table, _I32, (seqs, width), dev),
+                seqs, width, batch["max_q_len"], batch["max_kv_len"])
+    shared = batch.get("shared_lens")
+    if shared is not None:
+        groups = shared.shape[0] if isinstance(shared, torch.Tensor) and shared.dim() == 1 else 0
+        b.shared_lens = _need("shared_lens", shared, _I32, (groups,), dev)
+        b.group_starts = _need("group_starts", batch["group_starts"], _I32, (groups + 1,), dev)
+        b.groups, b.max_shared_len = groups, batch["max_shared_len"]
+    return b
+
+
+def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> dict:
+    """An empty paged MXFP8 cache (zeros)."""
+    out = {}
+    for n in ("k", "v"):
+        out[n + "_codes"] = torch.zeros(pages, kv_heads, page_size, head_dim, dtype=_U8, device=device)
+        out[n + "_scales"] = torch.zeros(pages, kv_heads, page_size, head_dim // 32, dtype=_U8, device=device)
+    return out
+
+
+def rotary_table(positions: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0, original: float = 0.0,
+                 low: float = 0.0, high: float = 1.0, amplitude: float = 1.0, device="cuda", stream=None) -> torch.Tensor:
+    """Cosines and sines [positions][rot_dim / 2][2] (float32) for rotary and kv_append.  With `factor` other than
+    1, pairs that turn at most `low` times over the `original` positions turn that much slower, those that turn
+    `high` times or more are kept (the defaults slow all of them)."""
+    if stream is not None:
+        return _elsewhere(stream, rotary_table, positions, rot_dim, base, factor, original, low, high, amplitude, device)
+    table = torch.empty(max(positions, 0), max(rot_dim // 2, 0), 2, dtype=_F32, device=device)
+    dev = table.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"device: {table.device} is not the current one (use torch.cuda.device)")
+    _done("fp4q_rotary_table", lib().fp4q_rotary_table(
+        positions, rot_dim, base, factor, original, low, high, amplitude, table.data_ptr(), _here(dev)))
+    return table
+
+
+def rotary(x: torch.Tensor, table: torch.Tensor, positions: torch.Tensor, layout: int = ROTARY_HALF,
+           backward: bool = False, in_place: bool = False, stream=None) -> torch.Tensor:
+    """x [tokens][heads][head_dim] (bfloat16 or float32, any token and head strides) turned by `table` at `positions`
+    (int32); with ``backward`` the gradient of x from that of the result.  A dense result, or x itself with ``in_place``.
+    Tokens whose position has no row in the table are padding: their rows are not written."""
+    if stream is not None:
+        return _elsewhere(stream, rotary, x, table, positions, layout, backward, in_place)
+    n, h, d, sn, sh, dev = _heads("x", x, _NAMES)
+    tp, rows, rot = _table_rows(table, dev)
+    pp = _need("positions", positions, _I32, (n,), dev)
+    if layout not in (ROTARY_HALF, ROTARY_INTERLEAVED):
+        raise ValueError("layout: ROTARY_HALF or ROTARY_INTERLEAVED is needed")
+    y, yn, yh = (x, sn, sh) if in_place else (x.new_empty(n, h, d), h * d, d)
+    _done("fp4q_rotary", lib().fp4q_rotary(
+        x.data_ptr(), _NAMES[x.dtype], n, h, d, rot, sn, sh, pp, tp, rows, layout | (ROTARY_BACKWARD if backward else 0),
+        y.data_ptr(), yn, yh, _here(dev)))
+    return y
+
+
+def kv_append(cache: dict, batch: dict, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor | None = None,
+              positions: torch.Tensor | None = None, layout: int = ROTARY_HALF, stream=None) -> dict:
+    """Writes the batch's keys and values [tokens][kv heads][head_dim] (bfloat16 or float32, any token and head
+    strides) to their places in the cache, the keys turned by `table` at `positions` (their places in the
+    sequences, if None) when there is a table.  Returns the cache."""
+    if stream is not None:
+        return _elsewhere(stream, kv_append, cache, batch, k, v, table, positions, layout)
+    n, h, d, kn, kh, dev = _heads("k", k, _NAMES)
+    vs = _heads("v", v, (k.dtype,))
+    c, b = _kv_cache(cache, dev), _kv_batch(batch, dev)
+    if vs[:3] != (n, h, d) or (h, d) != (c.kv_heads, c.head_dim):
+        raise ValueError(f"k, v: shape ({n}, {c.kv_heads}, {c.head_dim}) is needed, got {tuple(k.shape)} and {tuple(v.shape)}")
+    tp, rows, rot = (None, 0, 0) if table is None else _table_rows(table, dev)
+    pp = None if positions is None else _need("positions", positions, _I32, (n,), dev)
+    _done("fp4q_kv_append", lib().fp4q_kv_append(
+        k.data_ptr(), v.data_ptr(), _NAMES[k.dtype], n, kn, kh, vs[3], vs[4], tp, rows, rot, layout, pp,
+        ctypes.addressof(c), ctypes.addressof(b), _here(dev)))
+    return cache
+
+
+def attention_paged(q: torch.Tensor, cache: dict, batch: dict, scale: float | None = None, window: int = 0,
+                    causal: bool = True, with_lse: bool = False, stream=None):
+    """Attention of the batch's queries [tokens][q heads][head_dim] (bfloat16, any token and head strides) to the
+    cache: bfloat16 [tokens][q heads][head_dim], and with ``with_lse`` also the logarithm of the softmax's sum, float32
+    [tokens][q heads].  `scale` is 1 / sqrt(head_dim) if None; with `window` a token sees that many keys at most.
+    Rows of tokens behind the last sequence are not written."""
+    if stream is not None:
+        return _elsewhere(stream, attention_paged, q, cache, batch, scale, window, causal, with_lse)
+    n, h, d, sn, sh, dev = _heads("q", q, (torch.bfloat16,))
+    c, b = _kv_cache(cache, dev), _kv_batch(batch, dev)
+    if d != c.head_dim:
+        raise ValueError(f"q: heads of {c.head_dim} elements are needed, got {d}")
+    L = lib()
+    cp, bp = ctypes.addressof(c), ctypes.addressof(b)
+    need = L.fp4q_attention_paged_scratch(cp, bp, n, h, window)
+    out = q.new_empty(n, h, d)
+    lse = q.new_empty(n, h, dtype=_F32) if with_lse else None
+    scratch = q.new_empty(max(need, 16), dtype=_U8)
+    _done("fp4q_attention_paged", L.fp4q_attention_paged(
+        q.data_ptr(), n, h, sn, sh, cp, bp, max(d, 1) ** -0.5 if scale is None else scale, window, ATTN_CAUSAL if causal else ATTN_ALL,
+        out.data_ptr(), None if lse is None else lse.data_ptr(), scratch.data_ptr(), need, _here(dev)))
+    return (out, lse) if with_lse else out

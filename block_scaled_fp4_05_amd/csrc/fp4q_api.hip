@@ -39,6 +39,55 @@ bool moe_shape(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64
          topk <= FP4Q_MOE_MAX_TOPK && topk <= experts;
 }
 
+// Shapes, pointers and strides of the paged cache's calls.
+bool token_shape(int64_t tokens) { return tokens >= 1 && tokens < ((int64_t)1 << 24); }
+bool table_shape(int64_t rows, int64_t rot, int64_t head_dim) {
+  return rows >= 1 && rows <= INT32_MAX && rot >= 2 && rot % 2 == 0 && rot <= head_dim;
+}
+bool stride16(int64_t stride, int dt) { return stride % (dt == FP4Q_BF16 ? 8 : 4) == 0; }
+bool cache_shape(const fp4q_kv_cache& c) {
+  return c.pages >= 1 && c.pages <= INT32_MAX && c.page_size >= 16 && c.page_size <= 1024 &&
+         (c.page_size & (c.page_size - 1)) == 0 && c.kv_heads >= 1 && c.kv_heads <= 1024 && c.head_dim >= 32 &&
+         c.head_dim <= 512 && c.head_dim % 32 == 0;
+}
+bool cache_present(const fp4q_kv_cache& c) { return c.k_codes && c.k_scales && c.v_codes && c.v_scales; }
+bool cache_aligned(const fp4q_kv_cache& c) {
+  return aligned16(c.k_codes) && aligned16(c.k_scales) && aligned16(c.v_codes) && aligned16(c.v_scales);
+}
+bool batch_shape(const fp4q_kv_batch& b, const fp4q_kv_cache& c) {
+  return b.seqs >= 1 && b.seqs <= 65536 && b.max_pages >= 1 && b.max_pages <= INT32_MAX && b.max_q_len >= 1 &&
+         b.max_q_len <= INT32_MAX && b.max_kv_len >= 1 && b.max_kv_len <= INT32_MAX &&
+         b.max_kv_len <= b.max_pages * c.page_size && b.groups >= 0 && b.groups <= b.seqs &&
+         (b.groups == 0 || (b.max_shared_len >= 0 && b.max_shared_len <= b.max_kv_len));
+}
+bool batch_present(const fp4q_kv_batch& b) {
+  return b.q_starts && b.kv_lens && b.page_table && (b.groups == 0 || (b.group_starts && b.shared_lens));
+}
+bool batch_aligned(const fp4q_kv_batch& b) {
+  return aligned4(b.q_starts) && aligned4(b.kv_lens) && aligned4(b.page_table) &&
+         (b.groups == 0 || (aligned4(b.group_starts) && aligned4(b.shared_lens)));
+}
+fp4q::KvCache kv_cache(const fp4q_kv_cache& c) {
+  return fp4q::KvCache{c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.pages, c.kv_heads, c.head_dim,
+                       __builtin_ctzll((unsigned long long)c.page_size)};
+}
+fp4q::KvBatch kv_batch(const fp4q_kv_batch& b) {
+  return fp4q::KvBatch{b.q_starts, b.kv_lens, b.page_table, b.seqs, b.max_pages, b.max_q_len, b.max_kv_len,
+                       b.group_starts, b.shared_lens, b.groups, b.groups > 0 ? b.max_shared_len : 0};
+}
+fp4q::Attention attn_call(int64_t tokens, int64_t q_heads, int64_t window) {
+  fp4q::Attention a{};
+  a.tokens = tokens, a.q_heads = q_heads, a.window = window;
+  return a;
+}
+bool attn_shape(const fp4q_kv_cache& c, const fp4q_kv_batch& b, int64_t tokens, int64_t q_heads, int64_t window) {
+  if (!cache_shape(c) || !batch_shape(b, c) || !token_shape(tokens) || q_heads < 1 || q_heads > 4096 ||
+      q_heads % c.kv_heads != 0 || tokens * q_heads >= ((int64_t)1 << 26) || window < 0 || window > INT32_MAX ||
+      (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256))
+    return false;
+  return fp4q::attention_fits(kv_cache(c), kv_batch(b), attn_call(tokens, q_heads, window));
+}
+
 // Sink of a two-pass call's amax pass and the matching source for its quantizer: the
 // workspace's two-pass state when there is one, else the caller's float (which the
 // amax pass zeroes first).
@@ -485,6 +534,88 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
                                  (int)d, (int)hidden, (int)experts, (int)topk, ids, weights, out_dt == FP4Q_BF16, y,
                                  scratch},
                    stream);
+  return after_launch();
+}
+
+fp4q_status fp4q_rotary_table(int64_t positions, int64_t rot_dim, double base, double factor, double original,
+                              double low, double high, double amplitude, float* table, hipStream_t stream) {
+  if (positions < 1 || positions > INT32_MAX || rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0)
+    return FP4Q_E_SHAPE;
+  if (!table) return FP4Q_E_NULL;
+  if (!(base > 0.0 && base <= DBL_MAX) || !(factor > 0.0 && factor <= DBL_MAX) || !(amplitude >= -DBL_MAX && amplitude <= DBL_MAX))
+    return FP4Q_E_ARG;
+  if (factor != 1.0 && (!(original >= 0.0 && original <= DBL_MAX) || !(low < high) || !(low >= -DBL_MAX) || !(high <= DBL_MAX)))
+    return FP4Q_E_ARG;
+  if (!aligned16(table)) return FP4Q_E_ALIGN;
+  fp4q::launch_rotary_table(positions, (int)rot_dim, base, factor, original, low, high, amplitude, table, stream);
+  return after_launch();
+}
+
+fp4q_status fp4q_rotary(const void* x, fp4q_dtype dt, int64_t tokens, int64_t heads, int64_t head_dim, int64_t rot_dim,
+                        int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions, const float* table,
+                        int64_t table_rows, unsigned mode, void* y, int64_t y_token_stride, int64_t y_head_stride,
+                        hipStream_t stream) {
+  if (!token_shape(tokens) || heads < 1 || heads > 4096 || head_dim < 8 || head_dim > 1024 || head_dim % 8 != 0 ||
+      !table_shape(table_rows, rot_dim, head_dim))
+    return FP4Q_E_SHAPE;
+  if (!x || !positions || !table || !y) return FP4Q_E_NULL;
+  if (!valid_dtype(dt) || mode > 3u) return FP4Q_E_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(table) || !aligned4(positions) || !stride16(x_token_stride, dt) ||
+      !stride16(x_head_stride, dt) || !stride16(y_token_stride, dt) || !stride16(y_head_stride, dt))
+    return FP4Q_E_ALIGN;
+  fp4q::launch_rotary(fp4q::Rotary{x, dt, tokens, (int)heads, (int)head_dim, (int)rot_dim, x_token_stride,
+                                   x_head_stride, y_token_stride, y_head_stride, positions, table, table_rows,
+                                   (mode & FP4Q_ROTARY_INTERLEAVED) != 0, (mode & FP4Q_ROTARY_BACKWARD) != 0, y},
+                      stream);
+  return after_launch();
+}
+
+fp4q_status fp4q_kv_append(const void* k, const void* v, fp4q_dtype dt, int64_t tokens, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const float* table,
+                           int64_t table_rows, int64_t rot_dim, unsigned mode, const int32_t* positions,
+                           const fp4q_kv_cache* cache, const fp4q_kv_batch* batch, hipStream_t stream) {
+  if (!cache || !batch) return FP4Q_E_NULL;
+  if (!token_shape(tokens) || !cache_shape(*cache) || !batch_shape(*batch, *cache) ||
+      (table && !table_shape(table_rows, rot_dim, cache->head_dim)))
+    return FP4Q_E_SHAPE;
+  if (!k || !v || !cache_present(*cache) || !batch_present(*batch)) return FP4Q_E_NULL;
+  if (!valid_dtype(dt) || (table && mode > FP4Q_ROTARY_INTERLEAVED)) return FP4Q_E_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(table) || !aligned4(positions) || !cache_aligned(*cache) ||
+      !batch_aligned(*batch) || !stride16(k_token_stride, dt) || !stride16(k_head_stride, dt) ||
+      !stride16(v_token_stride, dt) || !stride16(v_head_stride, dt))
+    return FP4Q_E_ALIGN;
+  fp4q::launch_kv_append(kv_cache(*cache), kv_batch(*batch),
+                         fp4q::KvAppend{k, v, dt, tokens, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                                        table, table_rows, (int)rot_dim, mode == FP4Q_ROTARY_INTERLEAVED, positions},
+                         stream);
+  return after_launch();
+}
+
+int64_t fp4q_attention_paged_scratch(const fp4q_kv_cache* cache, const fp4q_kv_batch* batch, int64_t tokens,
+                                     int64_t q_heads, int64_t window) {
+  if (!cache || !batch || !attn_shape(*cache, *batch, tokens, q_heads, window)) return 0;
+  return fp4q::attention_scratch(kv_cache(*cache), kv_batch(*batch), attn_call(tokens, q_heads, window));
+}
+
+fp4q_status fp4q_attention_paged(const void* q, int64_t tokens, int64_t q_heads, int64_t q_token_stride,
+                                 int64_t q_head_stride, const fp4q_kv_cache* cache, const fp4q_kv_batch* batch,
+                                 float scale, int64_t window, unsigned mask, void* out, float* lse, void* scratch,
+                                 int64_t scratch_bytes, hipStream_t stream) {
+  if (!cache || !batch) return FP4Q_E_NULL;
+  if (!attn_shape(*cache, *batch, tokens, q_heads, window)) return FP4Q_E_SHAPE;
+  if (!q || !out || !scratch || !cache_present(*cache) || !batch_present(*batch)) return FP4Q_E_NULL;
+  if (!(scale > 0.0f) || scale > FLT_MAX || mask > FP4Q_ATTN_ALL || (mask == FP4Q_ATTN_ALL && window != 0))
+    return FP4Q_E_ARG;
+  fp4q::Attention a = attn_call(tokens, q_heads, window);
+  const fp4q::KvCache c = kv_cache(*cache);
+  const fp4q::KvBatch b = kv_batch(*batch);
+  if (scratch_bytes < fp4q::attention_scratch(c, b, a)) return FP4Q_E_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned4(lse) || !aligned16(scratch) || !cache_aligned(*cache) ||
+      !batch_aligned(*batch) || !stride16(q_token_stride, FP4Q_BF16) || !stride16(q_head_stride, FP4Q_BF16))
+    return FP4Q_E_ALIGN;
+  a.q = q, a.q_token = q_token_stride, a.q_head = q_head_stride, a.scale = scale, a.causal = mask == FP4Q_ATTN_CAUSAL;
+  a.out = out, a.lse = lse, a.scratch = scratch;
+  fp4q::launch_attention(c, b, a, stream);
   return after_launch();
 }
 

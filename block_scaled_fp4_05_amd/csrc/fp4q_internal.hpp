@@ -155,4 +155,59 @@ struct MoeArgs {
 int64_t moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk);
 void launch_moe(const MoeArgs& a, hipStream_t st);
 
+// Rotary positions and the append to a paged MXFP8 cache -- fp4q_rotary.hip.
+struct Rotary {
+  const void* x;
+  int dtype;
+  int64_t tokens;
+  int heads, head_dim, rot;
+  int64_t x_token, x_head, y_token, y_head;   // strides in elements
+  const int32_t* positions;
+  const float* table;
+  int64_t table_rows;
+  bool interleaved, backward;
+  void* y;
+};
+void launch_rotary_table(int64_t positions, int rot, double base, double factor, double original, double low,
+                         double high, double amplitude, float* table, hipStream_t st);
+void launch_rotary(const Rotary& r, hipStream_t st);
+
+struct KvCache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  int64_t pages, heads, head_dim;
+  int page_shift;   // a page has 2^page_shift rows
+};
+struct KvBatch {
+  const int32_t *q_starts, *kv_lens, *page_table;
+  int64_t seqs, max_pages, max_q_len, max_kv_len;
+  const int32_t *group_starts, *shared_lens;   // groups > 0
+  int64_t groups, max_shared_len;
+};
+struct KvAppend {   // table NULL: keys are not rotated
+  const void *k, *v;
+  int dtype;
+  int64_t tokens, k_token, k_head, v_token, v_head;   // strides in elements
+  const float* table;
+  int64_t table_rows;
+  int rot;
+  bool interleaved;
+  const int32_t* positions;   // NULL: a token's place in its sequence
+};
+void launch_kv_append(const KvCache& c, const KvBatch& b, const KvAppend& p, hipStream_t st);
+
+// Attention over that cache -- fp4q_attn.hip.  Shapes that attention_fits refuses have no launch.
+struct Attention {
+  const void* q;
+  int64_t tokens, q_heads, q_token, q_head;
+  float scale;
+  int64_t window;   // 0: none
+  bool causal;
+  void* out;
+  float* lse;
+  void* scratch;
+};
+bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a);
+int64_t attention_scratch(const KvCache& c, const KvBatch& b, const Attention& a);
+void launch_attention(const KvCache& c, const KvBatch& b, const Attention& a, hipStream_t st);
+
 }  // namespace fp4q

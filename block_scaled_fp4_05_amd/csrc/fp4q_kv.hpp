@@ -1,0 +1,45 @@
+// fp4q_kv.hpp -- device pieces shared by the kernels that write and read the paged MXFP8 cache
+// (fp4q_rotary.hip, fp4q_attn.hip).
+//
+// Lengths, starts and page ids are device data that the host never sees, so every kernel clamps or
+// skips what lies outside the arrays instead of trusting it.
+#pragma once
+#include "fp4q_internal.hpp"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp4q {
+namespace {
+
+// The last i in 0 .. n-1 with starts[i] <= t, or -1: 64 places at a time by the whole wave (t the same
+// in all of its lanes), so one trip to memory for up to 64 sequences and two for 4096, where halving takes
+// six and twelve.  Starts do not fall; where they do, some place in range comes back.
+__device__ __forceinline__ int wave_find(const int32_t* __restrict__ starts, int n, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  for (;;) {
+    const int step = (n + 63) >> 6, at = lane * step;
+    const bool below = at < n && starts[lo + min(at, n - 1)] <= t;
+    const int count = __popcll(__ballot(below));
+    if (count == 0) return lo - 1;
+    const int skip = min((count - 1) * step, n - 1);
+    lo += skip;
+    n = min(step, n - skip);
+    if (step == 1) return lo;
+  }
+}
+
+// The same by one lane for its own t.
+__device__ __forceinline__ int lane_find(const int32_t* __restrict__ starts, int n, int t) {
+  int lo = -1, hi = n;   // starts[lo] <= t < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace
+}  // namespace fp4q

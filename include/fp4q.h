@@ -501,6 +501,131 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
 /* Bytes of scratch for that call (0 for a shape it refuses).  Host only. */
 int64_t fp4q_moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t experts, int64_t topk);
 
+/*
+ * Rotary positions.  A head of head_dim elements has rot_dim/2 pairs that turn by the angle of the
+ * token's position, the other elements stay:
+ *   y1 = x1 cos - x2 sin,   y2 = x2 cos + x1 sin,
+ * pairs (i, i + rot_dim/2) with FP4Q_ROTARY_HALF and (2i, 2i+1) with FP4Q_ROTARY_INTERLEAVED.
+ * With FP4Q_ROTARY_BACKWARD or-ed to either, the transpose (-sin): x is the gradient of y and y that of x.
+ *   x, y       [tokens][heads][head_dim] of type dt, elements of a head dense, tokens and heads at the
+ *              given strides (in elements), e.g. the query and key heads inside the rows of a fused
+ *              projection.  y may be x with the same strides (in place); no other overlap.
+ *   positions  device int32 [tokens].  A token whose position is outside 0 .. table_rows-1 is padding: its rows
+ *              of y are not written.
+ *   table      device float [table_rows][rot_dim/2][2], cosine and sine, e.g. from fp4q_rotary_table.
+ * fp32 arithmetic, one rounding to bf16.
+ * Shapes: 1 <= tokens < 2^24, 1 <= heads <= 4096, head_dim a multiple of 8 up to 1024, rot_dim even, 2 .. head_dim,
+ * table_rows < 2^31; strides are whole multiples of 16 bytes (FP4Q_E_ALIGN).  Alignment: 16 bytes (positions 4).
+ */
+#define FP4Q_ROTARY_HALF 0u
+#define FP4Q_ROTARY_INTERLEAVED 1u
+#define FP4Q_ROTARY_BACKWARD 2u
+fp4q_status fp4q_rotary(const void* x, fp4q_dtype dt, int64_t tokens, int64_t heads, int64_t head_dim, int64_t rot_dim,
+                        int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions, const float* table,
+                        int64_t table_rows, unsigned mode, void* y, int64_t y_token_stride, int64_t y_head_stride,
+                        hipStream_t stream);
+
+/*
+ * The table of fp4q_rotary for positions 0 .. positions-1, computed in binary64 and rounded once:
+ *   table[p][i] = amplitude (cos(p f_i), sin(p f_i)),   f_i = base^(-2i / rot_dim) (g_i + (1 - g_i) / factor),
+ *   g_i = clamp((original base^(-2i / rot_dim) / 2 pi - low) / (high - low), 0, 1).
+ * For contexts longer than the `original` one: a pair that turned at least `high` times over it keeps its
+ * frequency, one that turned at most `low` times has it divided by factor, between them it changes evenly with
+ * the turns.  factor 1: no scaling, the other three are not read; to divide every frequency pass
+ * original 0, low 0, high 1.
+ * base > 0, factor > 0, original >= 0, low < high, amplitude: finite (FP4Q_E_ARG).
+ * Shapes: 1 <= positions < 2^31, rot_dim even, 2 .. 1024.  Alignment: 16 bytes.
+ */
+fp4q_status fp4q_rotary_table(int64_t positions, int64_t rot_dim, double base, double factor, double original,
+                              double low, double high, double amplitude, float* table, hipStream_t stream);
+
+/*
+ * A paged cache of keys and values in MXFP8 (as fp4q_quantize_mxfp8 writes it, blocks along the head):
+ *   k_codes, v_codes    [pages][kv_heads][page_size][head_dim]
+ *   k_scales, v_scales  [pages][kv_heads][page_size][head_dim/32]
+ * page_size: a power of two, 16 .. 1024.  head_dim: a multiple of 32 up to 512 (fp4q_attention_paged: 64, 128, 256).
+ * kv_heads <= 1024, pages < 2^31.  Pointers 16-byte aligned.
+ */
+typedef struct {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+    int64_t pages, page_size, kv_heads, head_dim;
+} fp4q_kv_cache;
+
+/*
+ * The sequences of a call.  The arrays are device int32, read by the kernels: a captured call follows
+ * their changes, within the bounds max_*.
+ *   q_starts    [seqs+1], not falling: tokens q_starts[s] .. q_starts[s+1]-1 of the call are sequence s's,
+ *               its last ones.  Tokens of the call behind q_starts[seqs] belong to none.
+ *   kv_lens     [seqs]: positions of the sequence, those tokens included.
+ *   page_table  [seqs][max_pages]: position p is in row p % page_size of page page_table[s][p / page_size].
+ *               Entries past a sequence's length are not read.
+ *   max_q_len, max_kv_len   at least the largest number of query tokens and of positions of a sequence;
+ *               max_kv_len <= max_pages * page_size.
+ *   groups      0, or a number of groups of neighbouring sequences that share their first keys:
+ *               sequences group_starts[g] .. group_starts[g+1]-1 ([groups+1], not falling) have the same
+ *               first shared_lens[g] / page_size pages (rounded down).  fp4q_attention_paged then reads those keys
+ *               once for all of a group's queries; what is computed is the same.  fp4q_kv_append ignores it.
+ *   max_shared_len          at least the largest shared_lens; 0 <= max_shared_len <= max_kv_len.
+ * Shapes: 1 <= seqs <= 65536, groups <= seqs, max_pages >= 1, max_q_len >= 1, max_kv_len >= 1, all < 2^31.
+ * Alignment: 4 bytes.
+ */
+typedef struct {
+    const int32_t *q_starts, *kv_lens, *page_table;
+    int64_t seqs, max_pages, max_q_len, max_kv_len;
+    const int32_t *group_starts, *shared_lens;
+    int64_t groups, max_shared_len;
+} fp4q_kv_batch;
+
+/*
+ * Keys and values of a call's tokens into the cache, the keys rotated on the way (fp4q_rotary's forward
+ * formula) and both rounded to MXFP8.  A rotated key is rounded once, from the formula's value; without a table (NULL)
+ * keys are stored as they come.
+ *   k, v       [tokens][kv_heads][head_dim] of type dt at the given strides (elements; heads dense inside).
+ *   table      as fp4q_rotary, or NULL; rot_dim and mode (without FP4Q_ROTARY_BACKWARD) are read only with it.
+ *   positions  device int32 [tokens]: the rows of the table; NULL: each token's place in its sequence.
+ *              A position that the table has no row for gives a key of NaN codes.
+ * A token of no sequence is skipped, and so is one whose place is outside the page table or whose page is
+ * outside the cache.  No two tokens of a call may have the same place: their bytes would mix.
+ * max_q_len, max_kv_len and the groups are not used.  Shapes: 1 <= tokens < 2^24, table_rows < 2^31, rot_dim even, 2 .. head_dim;
+ * strides whole multiples of 16 bytes (FP4Q_E_ALIGN).  Alignment: 16 bytes (positions 4).
+ */
+fp4q_status fp4q_kv_append(const void* k, const void* v, fp4q_dtype dt, int64_t tokens, int64_t k_token_stride,
+                           int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride, const float* table,
+                           int64_t table_rows, int64_t rot_dim, unsigned mode, const int32_t* positions,
+                           const fp4q_kv_cache* cache, const fp4q_kv_batch* batch, hipStream_t stream);
+
+/*
+ * Attention of a call's query tokens to the cache (their own keys and values appended before):
+ *   s_j = scale q . k_j,   out = sum_j exp(s_j - lse) v_j,   lse = ln sum_j exp(s_j),
+ * over the keys j that the token sees.  With p its position, kv_len - q_len + its place among the call's
+ * tokens of the sequence: j <= p with FP4Q_ATTN_CAUSAL, and j > p - window where window > 0; every j < kv_len with
+ * FP4Q_ATTN_ALL (window 0 only).
+ *   q      bf16 [tokens][q_heads][head_dim] at the given strides (elements), rotated already; query head h reads
+ *          key/value head h / (q_heads / kv_heads).
+ *   scale  > 0, finite.
+ *   out    bf16 [tokens][q_heads][head_dim];  lse  float [tokens][q_heads] or NULL.
+ *   scratch  device memory of at least fp4q_attention_paged_scratch bytes, 16-byte aligned; its contents before
+ *            and after the call mean nothing.  Calls that may run at the same time need their own.
+ * Scores, sums and the output are fp32 (in a fixed order: the same inputs give the same bits), probabilities are rounded to
+ * bf16 for their product with the values: out is within 2e-3 of its norm of the exact value before its own rounding.
+ * A token that sees no key gets out = 0 and lse = -infinity; one that sees only scores of -infinity, NaN.
+ * What a token does not see has no effect, whatever its codes.  A value that is not finite makes the elements
+ * of out of the tokens that see it NaN or infinite, a key that is none makes their whole rows NaN.  A page outside the cache counts as
+ * NaN keys, a kv_len outside 0 .. max_kv_len makes the sequence's rows NaN.  Query tokens past a sequence's first max_q_len,
+ * and tokens of no sequence, are left as they were.
+ * Shapes: head_dim 64, 128 or 256, q_heads a multiple of kv_heads up to 4096, 1 <= tokens < 2^24, tokens * q_heads < 2^26, 0 <= window < 2^31;
+ * strides whole multiples of 16 bytes (FP4Q_E_ALIGN).  Alignment: 16 bytes (lse 4).
+ */
+#define FP4Q_ATTN_CAUSAL 0u
+#define FP4Q_ATTN_ALL 1u
+fp4q_status fp4q_attention_paged(const void* q, int64_t tokens, int64_t q_heads, int64_t q_token_stride,
+                                 int64_t q_head_stride, const fp4q_kv_cache* cache, const fp4q_kv_batch* batch,
+                                 float scale, int64_t window, unsigned mask, void* out, float* lse, void* scratch,
+                                 int64_t scratch_bytes, hipStream_t stream);
+/* Bytes of scratch for that call (0 for a shape it refuses).  Host only; reads no device memory. */
+int64_t fp4q_attention_paged_scratch(const fp4q_kv_cache* cache, const fp4q_kv_batch* batch, int64_t tokens,
+                                     int64_t q_heads, int64_t window);
+
 /* max |x| over the whole matrix, written to device float *amax. */
 fp4q_status fp4q_amax(const void* x, fp4q_dtype dt, int64_t rows, int64_t cols, float* amax,
                       hipStream_t stream);

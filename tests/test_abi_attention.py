@@ -1,0 +1,133 @@
+"""Refusals of the rotary, cache and attention entry points and their helpers (no GPU needed): bad arguments
+fail before anything is enqueued."""
+import ctypes
+
+import pytest
+import torch
+
+from block_scaled_fp4_05_amd import binding as B
+
+A, MIS = 0x10000, 0x10004
+
+TABLE = dict(positions=64, rot=128, base=1e4, factor=1.0, original=0.0, low=0.0, high=0.0, amplitude=1.0, table=A, stream=0)
+ROTARY = dict(x=A, dt=B.BF16, tokens=4, heads=2, head_dim=128, rot=128, xt=256, xh=128, positions=A, table=A, rows=64, mode=0, y=A,
+              yt=256, yh=128, stream=0)
+CACHE = dict(k_codes=A, k_scales=A, v_codes=A, v_scales=A, pages=10, page_size=16, kv_heads=2, head_dim=128)
+BATCH = dict(q_starts=A, kv_lens=A, page_table=A, seqs=3, max_pages=5, max_q_len=4, max_kv_len=80, group_starts=None, shared_lens=None,
+             groups=0, max_shared_len=0)
+APPEND = dict(k=A, v=A, dt=B.BF16, tokens=4, kt=256, kh=128, vt=256, vh=128, table=A, rows=64, rot=128, mode=0, positions=None)
+ATTEND = dict(q=A, tokens=4, q_heads=8, qt=1024, qh=128)
+TAIL = dict(scale=0.1, window=0, mask=0, out=A, lse=A, scratch=A, scratch_bytes=1 << 30)
+
+
+def _call(name, base, kw):
+    args = dict(base)
+    args.update(kw)
+    return getattr(B.lib(), name)(*args.values())
+
+
+def _split(kw, *parts):
+    """kw dealt out to the parts that know its names."""
+    out = []
+    for p in parts:
+        d = dict(p)
+        d.update({k: v for k, v in kw.items() if k in p})
+        out.append(d)
+    assert all(any(k in p for p in parts) for k in kw)
+    return out
+
+
+def _append(**kw):
+    a, c, b = _split(kw, APPEND, CACHE, BATCH)
+    c, b = B.KvCache(*c.values()), B.KvBatch(*b.values())
+    return B.lib().fp4q_kv_append(*a.values(), ctypes.addressof(c), ctypes.addressof(b), 0)
+
+
+def _attend(**kw):
+    a, c, b, t = _split(kw, ATTEND, CACHE, BATCH, TAIL)
+    c, b = B.KvCache(*c.values()), B.KvBatch(*b.values())
+    return B.lib().fp4q_attention_paged(*a.values(), ctypes.addressof(c), ctypes.addressof(b), *t.values(), 0)
+
+
+def _need(window=0, **kw):
+    a, c, b = _split(kw, ATTEND, CACHE, BATCH)
+    return B.fp4q_attention_paged_scratch(B.KvCache(*c.values()), B.KvBatch(*b.values()), a["tokens"], a["q_heads"], window)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(positions=0), 2), (dict(positions=1 << 31), 2), (dict(rot=0), 2), (dict(rot=3), 2), (dict(rot=1026), 2), (dict(table=None), 1),
+    (dict(table=MIS), 3), (dict(base=0.0), 4), (dict(base=-1.0), 4), (dict(base=float("nan")), 4), (dict(base=float("inf")), 4),
+    (dict(factor=0.0), 4), (dict(factor=float("nan")), 4), (dict(amplitude=float("inf")), 4), (dict(factor=2.0), 4),
+    (dict(factor=2.0, low=1.0, high=0.5), 4), (dict(factor=2.0, high=1.0, original=-1.0), 4), (dict(factor=2.0, high=float("nan")), 4)])
+def test_table(kw, status):
+    assert _call("fp4q_rotary_table", TABLE, kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), 1), (dict(y=None), 1), (dict(positions=None), 1), (dict(table=None), 1), (dict(dt=2), 4), (dict(mode=4), 4),
+    (dict(tokens=0), 2), (dict(tokens=1 << 24), 2), (dict(heads=0), 2), (dict(heads=4097), 2), (dict(head_dim=100), 2), (dict(head_dim=0), 2),
+    (dict(head_dim=1032), 2), (dict(rot=0), 2), (dict(rot=127), 2), (dict(rot=130), 2), (dict(rows=0), 2), (dict(rows=1 << 31), 2),
+    (dict(x=MIS), 3), (dict(y=MIS), 3), (dict(table=MIS), 3), (dict(positions=A + 2), 3), (dict(xt=257), 3), (dict(xh=4), 3), (dict(yt=-1), 3),
+    (dict(yh=129), 3), (dict(dt=B.F32, yh=130), 3)])
+def test_rotary(kw, status):
+    assert _call("fp4q_rotary", ROTARY, kw) == status
+
+
+CACHE_AND_BATCH = [
+    (dict(k_codes=None), 1), (dict(k_scales=None), 1), (dict(v_codes=None), 1), (dict(v_scales=None), 1), (dict(q_starts=None), 1),
+    (dict(kv_lens=None), 1), (dict(page_table=None), 1), (dict(groups=1), 1), (dict(pages=0), 2), (dict(pages=1 << 31), 2),
+    (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=2048, max_pages=1), 2), (dict(kv_heads=0), 2), (dict(head_dim=0), 2),
+    (dict(head_dim=100), 2), (dict(head_dim=544), 2), (dict(seqs=0), 2), (dict(seqs=65537), 2), (dict(max_pages=0), 2), (dict(max_q_len=0), 2),
+    (dict(max_kv_len=0), 2), (dict(max_kv_len=81), 2), (dict(groups=4), 2), (dict(groups=-1), 2),
+    (dict(groups=2, group_starts=A, shared_lens=A, max_shared_len=81), 2), (dict(groups=2, group_starts=A, shared_lens=A, max_shared_len=-1), 2),
+    (dict(k_codes=MIS), 3), (dict(k_scales=MIS), 3), (dict(v_codes=MIS), 3), (dict(v_scales=MIS), 3), (dict(q_starts=A + 2), 3),
+    (dict(kv_lens=A + 1), 3), (dict(page_table=A + 2), 3), (dict(groups=1, group_starts=A + 2, shared_lens=A), 3),
+    (dict(groups=1, group_starts=A, shared_lens=A + 1), 3)]
+
+
+@pytest.mark.parametrize("kw,status", CACHE_AND_BATCH + [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(dt=2), 4), (dict(mode=2), 4), (dict(tokens=0), 2), (dict(tokens=1 << 24), 2),
+    (dict(rot=0), 2), (dict(rot=130), 2), (dict(rot=5), 2), (dict(rows=0), 2), (dict(k=MIS), 3), (dict(v=MIS), 3), (dict(table=MIS), 3),
+    (dict(positions=A + 2), 3), (dict(kt=129), 3), (dict(kh=4), 3), (dict(vt=100), 3), (dict(vh=2), 3),
+    (dict(table=None, rot=5, mode=9, rows=-3, v=MIS), 3)])          # without a table its arguments are not looked at
+def test_append(kw, status):
+    assert _append(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", CACHE_AND_BATCH + [
+    (dict(q=None), 1), (dict(out=None), 1), (dict(scratch=None), 1), (dict(tokens=0), 2), (dict(tokens=1 << 24), 2), (dict(q_heads=0), 2),
+    (dict(q_heads=7), 2), (dict(q_heads=4098), 2), (dict(tokens=1 << 20, q_heads=64), 2), (dict(head_dim=96), 2), (dict(head_dim=512), 2),
+    (dict(window=-1), 2), (dict(window=1 << 31), 2), (dict(scale=0.0), 4), (dict(scale=-1.0), 4), (dict(scale=float("inf")), 4),
+    (dict(scale=float("nan")), 4), (dict(mask=2), 4), (dict(mask=1, window=5), 4), (dict(scratch_bytes=15), 4), (dict(q=MIS), 3),
+    (dict(out=MIS), 3), (dict(lse=A + 2), 3), (dict(scratch=MIS), 3), (dict(qt=1025), 3), (dict(qh=4), 3), (dict(lse=None, q=MIS), 3)])
+def test_attention(kw, status):
+    assert _attend(**kw) == status
+
+
+def test_missing_descriptions():
+    assert B.lib().fp4q_kv_append(*APPEND.values(), None, None, 0) == 1
+    assert B.lib().fp4q_attention_paged(*ATTEND.values(), None, None, *TAIL.values(), 0) == 1
+    assert B.lib().fp4q_attention_paged_scratch(None, None, 4, 8, 0) == 0
+
+
+def test_scratch():
+    for kw in (dict(tokens=0), dict(q_heads=7), dict(head_dim=96), dict(max_kv_len=81), dict(window=-1)):
+        assert _need(**kw) == 0
+    for kw in (dict(), dict(max_pages=10000, max_kv_len=160000), dict(max_pages=10000, max_kv_len=160000, window=100),
+               dict(max_pages=10000, max_kv_len=160000, groups=2, max_shared_len=100000),
+               dict(tokens=60000, max_q_len=60000, max_pages=10000, max_kv_len=160000)):
+        need = _need(**kw)
+        assert need >= 16 and _attend(**kw, **({"group_starts": A, "shared_lens": A} if "groups" in kw else {}), scratch_bytes=need - 1) == 4
+    # the longest contexts: a bounded number of pieces
+    assert _need(tokens=1, page_size=1024, max_pages=1 << 18, max_kv_len=1 << 28) <= 600 * 8 * (128 + 2) * 4
+    assert _need(seqs=64, tokens=64, max_q_len=1, max_pages=8192, max_kv_len=131072) <= 64 * 70 * 8 * 130 * 4
+
+
+def test_helpers_refuse_what_the_library_cannot_see():
+    for t, err in ((torch.zeros(4, 2, 64, dtype=torch.float16), TypeError), (torch.zeros(4, 2, 64), ValueError), (None, TypeError)):
+        with pytest.raises(err):
+            B.rotary(t, None, None)
+        with pytest.raises(err):
+            B.kv_append({}, {}, t, t)
+    with pytest.raises(TypeError):
+        B.attention_paged(torch.zeros(4, 2, 64), {}, {})
