@@ -42,7 +42,7 @@ struct AttnArgs {
   int64_t pages, max_kv, max_shared;
   int max_q, tokens, seqs, groups, kv_heads, per_kv, page_shift, max_pages, window;
   bool causal, shared_pass;   // shared_pass: the items are groups and their shared keys
-  int chunk, chunks, row_tiles;             // keys per workgroup, workgroups per row tile, row tiles per item
+  int items, chunk, chunks, row_tiles;      // keys per workgroup of the own pass, workgroups per row tile, row tiles per item
   int most_chunks, shared_chunk;            // of the own pass; keys per workgroup of the shared pass
   float scale_log2;                         // scale log2(e)
   uint16_t* out;
@@ -62,11 +62,10 @@ __device__ __forceinline__ int shared_keys(const AttnArgs& a, int group) {
   return n >> a.page_shift << a.page_shift;
 }
 
-// The group of sequence s, or -1.
+// The group of sequence s (the same in the whole wave), or -1.
 __device__ __forceinline__ int group_of(const AttnArgs& a, int s) {
   if (a.groups == 0) return -1;
-  const int g = lane_find(a.group_starts, a.groups, s);
-  return g >= 0 && s < a.group_starts[g + 1] ? g : -1;
+  return wave_sequence(a.group_starts, a.groups, s);
 }
 
 // Own keys of a sequence: what its group does not share, from the first that its window's first query sees.
@@ -135,6 +134,19 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t v) {
   return lo | hi;
 }
 
+// Four pairs of bf16 with zeros in place of what is infinite or NaN.
+__device__ __forceinline__ u32x4_m only_finite(u32x4_m v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] &= ~odd_halves(v[e]);
+  return v;
+}
+// Two pairs of bf16 values of a key that a row sees: NaN in the sums of those that are infinite or NaN.
+__device__ __forceinline__ void poison(u32x2_m v, float& a, float& b, float& c, float& d) {
+  const uint32_t x = odd_halves(v.x), y = odd_halves(v.y);
+  a = x & 0xFFFFu ? __builtin_nanf("") : a, b = x >> 16 ? __builtin_nanf("") : b;
+  c = y & 0xFFFFu ? __builtin_nanf("") : c, d = y >> 16 ? __builtin_nanf("") : d;
+}
+
 // Four rows and 16 columns of bf16 in LDS, transposed: lane i of 16 gives the place of columns 4 (i % 4) .. + 3 of
 // row i / 4 and gets column i of the four rows.
 __device__ __forceinline__ v4s_a read_transposed(const uint8_t* p) {
@@ -143,6 +155,70 @@ __device__ __forceinline__ v4s_a read_transposed(const uint8_t* p) {
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A row's m need not be its largest score so far: it follows only where that is more than 2^kLag times
+// larger, so that l and o, which have fp32's range, are rarely multiplied.
+constexpr float kLag = 8.0f;
+
+// What a workgroup works on: the rows of an item (a sequence's query tokens, or in the shared pass a group's, times the
+// query heads of one key/value head) and a piece of its keys.
+struct Work {
+  int head, seq, t0, rows;      // the item's first sequence and token, its rows
+  int c0, c1;                   // keys
+  int slot, slots;              // where the result goes: with one slot, to the output
+};
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int item, int head, int piece, Work& w) {
+  w.head = head;
+  int t1, first, end, chunk;
+  if (a.shared_pass) {
+    w.seq = clamp_to(a.group_starts[item], 0, a.seqs);
+    const int s1 = clamp_to(a.group_starts[item + 1], w.seq, a.seqs);
+    const int shared = shared_keys(a, item);
+    if (s1 == w.seq || piece >= shared_chunks(a, shared)) return false;
+    w.t0 = clamp_to(a.q_starts[w.seq], 0, a.tokens), t1 = clamp_to(a.q_starts[s1], w.t0, a.tokens);
+    first = 0, end = shared, chunk = a.shared_chunk, w.slot = piece, w.slots = 2;
+  } else {
+    w.seq = item;
+    w.t0 = clamp_to(a.q_starts[item], 0, a.tokens), t1 = clamp_to(a.q_starts[item + 1], w.t0, a.tokens);
+    const int kv = a.kv_lens[item], g = group_of(a, item), shared = g >= 0 ? shared_keys(a, g) : 0;
+    const Range own = own_range(a, kv, t1 - w.t0, shared);
+    const int pieces = own_chunks(a, own), before = shared_chunks(a, shared);
+    if (piece >= pieces) return false;
+    t1 = min(t1, w.t0 + a.max_q);
+    first = own.first, end = own.end, chunk = a.chunk, w.slot = before + piece, w.slots = before + pieces;
+  }
+  w.rows = (t1 - w.t0) * a.per_kv;
+  w.c0 = min(first + piece * chunk, end), w.c1 = min(w.c0 + chunk, end);
+  return true;
+}
+
+// The page ids of a workgroup's keys to LDS; an id that is none becomes -1.
+__device__ __forceinline__ int load_pages(const AttnArgs& a, const Work& w, int* pages) {
+  const int p0 = w.c0 >> a.page_shift, n = w.c1 > w.c0 ? ((w.c1 - 1) >> a.page_shift) - p0 + 1 : 0;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const int id = p0 + i < a.max_pages ? a.page_table[(int64_t)w.seq * a.max_pages + p0 + i] : -1;
+    pages[i] = id < 0 || id >= a.pages ? -1 : id;
+  }
+  return n;
+}
+
+// The keys that the row of a query token sees of the workgroup's: from first to end, first <= end.
+__device__ __forceinline__ Range row_keys(const AttnArgs& a, const Work& w, int t) {
+  Range r = visible(a, a.shared_pass ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : w.seq, t);
+  r.end = max(min(r.end, w.c1), r.first);
+  return r;
+}
+
+// 1 / l and lse of a row that is complete.  Nothing seen: zeros and -infinity; only scores of -infinity, or a length
+// out of bounds: NaN.
+__device__ __forceinline__ float finish(const AttnArgs& a, int seq, int t, float top, float sum, float& lse) {
+  lse = (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  if (sum != 0.0f) return 1.0f / sum;
+  const Range seen = visible(a, seq, t);
+  const bool none = seen.end <= seen.first && !broken(a, a.kv_lens[seq]);
+  lse = none ? -kInf : __builtin_nanf("");
+  return none ? 0.0f : __builtin_nanf("");
+}
 
 // -----------------------------------------------------------------------------------------
 // Few rows per key/value head: the keys' bytes are what counts.  A workgroup takes `chunk` keys of one
@@ -172,46 +248,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g4 = lane >> 4;
   int id = blockIdx.x;
-  const int chunk_at = id % a.chunks;
+  const int piece = id % a.chunks;
   id /= a.chunks;
   const int row_tile = id % a.row_tiles;
   id /= a.row_tiles;
-  const int head = id % a.kv_heads, item = id / a.kv_heads;
-
-  // The item's rows and keys.
-  int s0, t0, t1, slot = 0;   // first sequence, tokens
-  Range range;
-  bool direct = false, bad = false;
-  if (a.shared_pass) {
-    s0 = clamp_to(a.group_starts[item], 0, a.seqs);
-    const int s1 = clamp_to(a.group_starts[item + 1], s0, a.seqs);
-    t0 = clamp_to(a.q_starts[s0], 0, a.tokens), t1 = clamp_to(a.q_starts[s1], t0, a.tokens);
-    range = Range{0, shared_keys(a, item)};
-    if (s1 == s0) return;
-    slot = chunk_at;
-    if (chunk_at >= shared_chunks(a, range.end)) return;
-  } else {
-    s0 = item;
-    t0 = clamp_to(a.q_starts[s0], 0, a.tokens), t1 = clamp_to(a.q_starts[s0 + 1], t0, a.tokens);
-    const int g = group_of(a, s0), shared = g >= 0 ? shared_keys(a, g) : 0, kv = a.kv_lens[s0];
-    bad = broken(a, kv);
-    range = own_range(a, kv, t1 - t0, shared);
-    const int mine = own_chunks(a, range), before = shared_chunks(a, shared);
-    if (chunk_at >= mine) return;
-    direct = mine + before == 1;
-    slot = before + chunk_at;
-  }
-  const int rows = (a.shared_pass ? t1 - t0 : min(t1 - t0, a.max_q)) * a.per_kv, row0 = row_tile * 16 * R;
+  Work w;
+  if (!find_work(a, id / a.kv_heads, id % a.kv_heads, piece, w)) return;
+  const int head = w.head, rows = w.rows, row0 = row_tile * 16 * R, t0 = w.t0, c0 = w.c0, c1 = w.c1;
   if (row0 >= rows) return;
-  const int c0 = range.first + chunk_at * (a.shared_pass ? a.shared_chunk : a.chunk);
-  const int c1 = min(c0 + (a.shared_pass ? a.shared_chunk : a.chunk), range.end);
-
-  // Pages of the chunk; an id that is none counts as -1.
-  const int p0 = c0 >> a.page_shift, np = c1 > c0 ? ((c1 - 1) >> a.page_shift) - p0 + 1 : 0;
-  for (int i = threadIdx.x; i < np; i += 256) {
-    const int id_ = p0 + i < a.max_pages ? a.page_table[(int64_t)s0 * a.max_pages + p0 + i] : -1;
-    lds_page[i] = id_ < 0 || id_ >= a.pages ? -1 : id_;
-  }
+  const int np = load_pages(a, w, lds_page), p0 = c0 >> a.page_shift;
 
   // Queries, the MFMA's second operand: lane (n, g4) holds elements 64 i + 16 g4 .. + 15 of row n, as it does of the keys.
   v8b_a qf[R][W::LOADS][2];
@@ -220,8 +265,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
   for (int r = 0; r < R; ++r) {
     const int row = min(row0 + 16 * r + n, rows - 1);   // behind the last row: that one again, not stored
     const int t = t0 + row / a.per_kv, h = head * a.per_kv + row % a.per_kv;
-    const Range seen = visible(a, a.shared_pass ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : s0, t);
-    lo[r] = seen.first, hi[r] = min(seen.end, c1);
+    const Range seen = row_keys(a, w, t);
+    lo[r] = seen.first, hi[r] = seen.end;
     const uint16_t* x = a.q + t * a.q_token + h * a.q_head;
 #pragma unroll
     for (int i = 0; i < W::LOADS; ++i)
@@ -287,49 +332,41 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
   Fetch<D> f;
   if (begin < stop) fetch(begin, f);
   for (int key0 = begin; key0 < stop; key0 += kTile * kWaves) {
-    const Fetch<D> now = f;
+    Fetch<D> now = f;
     if (key0 + kTile * kWaves < stop) fetch(key0 + kTile * kWaves, f);
     if (key0 + kTile <= lo_min) continue;
     const bool edge = key0 < lo_max || key0 + kTile > hi_min;   // some row does not see some key
 
-    // Values to LDS as bf16.  Rows behind the chunk may hold anything: they become zeros.
-    u32x4_m vb[2][W::LOADS][2];
+    // Values to LDS as bf16.  Rows behind the chunk may hold anything: they become zeros.  So do values that are not finite
+    // in a tile that not every row sees whole, since 0 times them is NaN: rows that see them get theirs below.
     bool odd = false;
+    if (edge) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < W::LOADS; ++i) {
-        u32x4_m w = now.v[b][i];
-        uint32_t sc = now.vs[b][i];
-        if (edge) {
-          if (key0 + 16 * b + 64 / W::LINE * i + lane / W::LINE >= c1) w = u32x4_m{0u, 0u, 0u, 0u}, sc = 127u;
-          odd |= suspect(w, sc);
+        for (int i = 0; i < W::LOADS; ++i) {
+          if (key0 + 16 * b + 64 / W::LINE * i + lane / W::LINE >= c1) now.v[b][i] = u32x4_m{0u, 0u, 0u, 0u}, now.vs[b][i] = 127u;
+          odd |= suspect(now.v[b][i], now.vs[b][i]);
         }
-        to_bf16(w, sc, vb[b][i]);
-      }
-    odd = edge && __any(odd);
-    auto put = [&](bool zero_odd, bool marks) {
+      odd = __any(odd);
+    }
+    auto put = [&](bool finite) {
       wave_lds_fence();
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i = 0; i < W::LOADS; ++i)
+        for (int i = 0; i < W::LOADS; ++i) {
+          u32x4_m vb[2];
+          to_bf16(now.v[b][i], now.vs[b][i], vb);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            u32x4_m w = vb[b][i][j];
-            if (zero_odd || marks) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t o = odd_halves(w[e]);
-                w[e] = marks ? o & 0x3F803F80u : w[e] & ~o;
-              }
-            }
-            *reinterpret_cast<u32x4_m*>(mine + (16 * b + 64 / W::LINE * i + lane / W::LINE) * W::ROW +
-                                        32 * (lane % W::LINE) + 16 * j) = w;
-          }
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<u32x4_m*>(mine + (16 * b + 64 / W::LINE * i + lane / W::LINE) * W::ROW + 32 * (lane % W::LINE) + 16 * j) =
+                finite ? only_finite(vb[j]) : vb[j];
+        }
       wave_lds_fence();
     };
-    put(odd, false);
+    if (__builtin_expect(odd, 0)) put(true);
+    else put(false);
 
     // Scores: register j of half b is key key0 + 16 b + 4 g4 + j, row n.
     v4f_m s4[R][2];
@@ -362,14 +399,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int key = key0 + 16 * (i >> 2) + 4 * g4 + (i & 3);
-          if (key < lo[r] || key >= hi[r]) sc[i] = -kInf;
+          if ((uint32_t)(key - lo[r]) >= (uint32_t)(hi[r] - lo[r])) sc[i] = -kInf;
         }
       }
       float top = sc[0];
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, sc[i]);
       const float mt = __builtin_fmaxf(m[r], quad_max(top));
-      if (__any(mt > m[r])) {
+      if (__any(mt > m[r] + kLag)) {
         const float keep = mt == -kInf ? 1.0f : exp2_of(m[r] - mt);
         m[r] = mt, l[r] *= keep;
 #pragma unroll
@@ -386,36 +423,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
       p[r] = __builtin_bit_cast(v8b_a, u32x4_m{w[0], w[1], w[2], w[3]});
     }
     // O^T += V^T P^T, 16 elements of the head at a time.
-    auto product = [&](int i, const v8b_a& pr, v4f_m c) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
       const v4s_a x = read_transposed(tr + 32 * i), y = read_transposed(tr + 16 * W::ROW + 32 * i);
-      const v8b_a vf = __builtin_bit_cast(v8b_a, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
-      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pr, c, 0, 0, 0);
-    };
+      const v8b_a v = __builtin_bit_cast(v8b_a, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int r = 0; r < R; ++r) acc[r][i] = product(i, p[r], acc[r][i]);
+      for (int r = 0; r < R; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], acc[r][i], 0, 0, 0);
+    }
     if (__builtin_expect(odd, 0)) {
-      // Values that are no finite numbers, in a tile that not every row sees whole: 0 times them would be NaN, so
-      // the product above took zeros in their place, and the rows that see one get a NaN here.
-      put(false, true);
+      put(false);
+      for (int k = 0; k < kTile; ++k)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        uint32_t see[4];
+        for (int r = 0; r < R; ++r)
+          if ((uint32_t)(key0 + k - lo[r]) < (uint32_t)(hi[r] - lo[r]))
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = key0 + 16 * (i >> 1) + 4 * g4 + 2 * (i & 1);
-          see[i] = (key >= lo[r] && key < hi[r] ? 0x3F80u : 0u) | (key + 1 >= lo[r] && key + 1 < hi[r] ? 0x3F800000u : 0u);
-        }
-        const v8b_a pr = __builtin_bit_cast(v8b_a, u32x4_m{see[0], see[1], see[2], see[3]});
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const v4f_m hit = product(i, pr, v4f_m{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (hit[j] > 0.0f) acc[r][i][j] = __builtin_nanf("");
-        }
-      }
+            for (int i = 0; i < D / 16; ++i) {
+              v4f_m& c = acc[r][i];
+              float c0 = c[0], c1_ = c[1], c2 = c[2], c3 = c[3];
+              poison(*reinterpret_cast<const u32x2_m*>(mine + k * W::ROW + 32 * i + 8 * g4), c0, c1_, c2, c3);
+              c = v4f_m{c0, c1_, c2, c3};
+            }
+      wave_lds_fence();
     }
   }
 
@@ -438,34 +466,29 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
     if (at < rows) {
       float top = -kInf, sum = 0.0f, v[PER];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, lds_ml[w][16 * r + row][0]);
+      for (int u = 0; u < kWaves; ++u) top = __builtin_fmaxf(top, lds_ml[u][16 * r + row][0]);
 #pragma unroll
       for (int e = 0; e < PER; ++e) v[e] = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float mw = lds_ml[w][16 * r + row][0], f_ = mw == -kInf ? 0.0f : exp2_of(mw - top);
-        sum += f_ * lds_ml[w][16 * r + row][1];   // 0 times a NaN stays one
-        const float* src = reinterpret_cast<const float*>(lds_v[w]) + row * (D + 4) + e0;
+      for (int u = 0; u < kWaves; ++u) {
+        const float mu = lds_ml[u][16 * r + row][0], part = mu == -kInf ? 0.0f : exp2_of(mu - top);
+        sum += part * lds_ml[u][16 * r + row][1];   // 0 times a NaN stays one
+        const float* src = reinterpret_cast<const float*>(lds_v[u]) + row * (D + 4) + e0;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) v[e] = __builtin_fmaf(f_, src[e], v[e]);
+        for (int e = 0; e < PER; ++e) v[e] = __builtin_fmaf(part, src[e], v[e]);
       }
       const int t = t0 + at / a.per_kv, h = head * a.per_kv + at % a.per_kv;
       const int64_t place = (int64_t)t * a.kv_heads * a.per_kv + h;
-      if (direct) {
-        // nothing seen: zeros; only scores of -infinity, or a length out of bounds: NaN
-        const Range seen = visible(a, s0, t);
-        float inv = 1.0f / sum, out_lse = (top + __builtin_amdgcn_logf(sum)) * kLn2;
-        if (sum == 0.0f) {
-          const bool none = seen.end <= seen.first && !bad;
-          inv = none ? 0.0f : __builtin_nanf(""), out_lse = none ? -kInf : __builtin_nanf("");
-        }
+      if (w.slots == 1) {
+        float out_lse;
+        const float inv = finish(a, w.seq, t, top, sum, out_lse);
 #pragma unroll
         for (int e = 0; e < PER; e += 4)
           *reinterpret_cast<u32x2_m*>(a.out + place * D + e0 + e) =
               u32x2_m{bf16_pair(v[e] * inv, v[e + 1] * inv), bf16_pair(v[e + 2] * inv, v[e + 3] * inv)};
         if (a.lse && e0 == 0) a.lse[place] = out_lse;
       } else {
-        const int64_t p = (int64_t)slot * a.tokens * a.kv_heads * a.per_kv + place;
+        const int64_t p = (int64_t)w.slot * a.tokens * a.kv_heads * a.per_kv + place;
 #pragma unroll
         for (int e = 0; e < PER; e += 4) *reinterpret_cast<v4f_m*>(a.part_o + p * D + e0 + e) = v4f_m{v[e], v[e + 1], v[e + 2], v[e + 3]};
         if (e0 == 0) *reinterpret_cast<f32x2_m*>(a.part_ml + 2 * p) = f32x2_m{top, sum};
@@ -475,63 +498,352 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
   }
 }
 
-// Joins the slots of each row in their order: one wave per query row.  Slots: those of its group's shared keys, then
-// its sequence's own.
+// -----------------------------------------------------------------------------------------
+// Many rows per key/value head (prompts, a prefix shared by many sequences): the matrix products are what counts.
+// The four waves of a workgroup take 32 rows each and go through the same tiles of 64 keys, staged through
+// LDS as bf16 for all of them.  The next tile's loads are in flight during a tile, and its LDS buffer is the other of
+// two, so one barrier per tile.
+// -----------------------------------------------------------------------------------------
 template <int D>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), all = (int64_t)a.tokens * q_heads;
-  if (row >= all) return;
-  const int t = __builtin_amdgcn_readfirstlane((int)(row / q_heads));
-  const int s = wave_find(a.q_starts, a.seqs, t);
-  if (s < 0 || t >= a.q_starts[s + 1]) return;   // no sequence's token
-  const int t0 = clamp_to(a.q_starts[s], 0, a.tokens), t1 = clamp_to(a.q_starts[s + 1], t0, a.tokens);
-  if (t - t0 >= a.max_q) return;   // past the call's bound: not computed
-  const int g = group_of(a, s), shared = g >= 0 ? shared_keys(a, g) : 0, kv = a.kv_lens[s];
-  const int slots = shared_chunks(a, shared) + own_chunks(a, own_range(a, kv, t1 - t0, shared));
-  if (slots == 1) return;   // written already
-  constexpr int PER = D / 64;
-  float top = -kInf, sum = 0.0f, v[PER];
-  for (int i = 0; i < slots; ++i) top = __builtin_fmaxf(top, a.part_ml[2 * (i * all + row)]);
-#pragma unroll
-  for (int e = 0; e < PER; ++e) v[e] = 0.0f;
-  for (int i = 0; i < slots; ++i) {
-    const int64_t p = i * all + row;
-    const float m = a.part_ml[2 * p], f = m == -kInf ? 0.0f : exp2_of(m - top);
-    sum += f * a.part_ml[2 * p + 1];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) v[e] = __builtin_fmaf(f, a.part_o[p * D + PER * lane + e], v[e]);
-  }
-  float inv = 1.0f / sum, out_lse = (top + __builtin_amdgcn_logf(sum)) * kLn2;
-  if (sum == 0.0f) {
-    const Range seen = visible(a, s, t);
-    const bool none = seen.end <= seen.first && !broken(a, kv);
-    inv = none ? 0.0f : __builtin_nanf(""), out_lse = none ? -kInf : __builtin_nanf("");
-  }
-  uint16_t* o = a.out + row * D + PER * lane;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) o[e] = (uint16_t)bf16_pair(v[e] * inv, 0.0f);
-  if (a.lse && lane == 0) a.lse[row] = out_lse;
+struct Tile {
+  static constexpr int KEYS = 64;
+  static constexpr int K_ROW = 2 * D + 16;  // bytes of a row of K in LDS: the 16-byte pieces of 16 rows on different banks
+  static constexpr int V_ROW = 2 * D + 64;  // of V: the 64 bytes of four rows that half a transposed read covers, too
+  static constexpr int LOADS = D / 64;      // 16-byte loads per lane for the 16 rows that a wave stages
+  static constexpr int SB = D / 32;         // scale bytes of a row
+  static constexpr int LINE = D / 16;       // lanes to a row
+  static constexpr int BUFFER = KEYS * (K_ROW + V_ROW);
+};
+
+// Maximum and sum over lanes l and l ^ 32, the same bits in both.
+__device__ __forceinline__ float pair_max(float v) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+__device__ __forceinline__ v16f_m zeros16() {
+  return v16f_m{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 }
 
-// How a pass is cut: rows per workgroup, keys per workgroup.
+template <int D>
+__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a) {
+  using T = Tile<D>;
+  __shared__ __align__(16) uint8_t lds[2 * T::BUFFER];
+  __shared__ int lds_bounds[kWaves][4], lds_odd[2][kWaves];
+  extern __shared__ int lds_page[];   // the piece's pages
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, half = lane >> 5;
+  // Row tiles from the last on: under a causal mask it has the most keys.
+  const int per = a.chunks * a.kv_heads, items = a.items;
+  int id = blockIdx.x;
+  const int head = id % a.kv_heads, piece = id / a.kv_heads % a.chunks;
+  id /= per;
+  const int item = id % items, row_tile = a.row_tiles - 1 - id / items;
+  Work w;
+  if (!find_work(a, item, head, piece, w)) return;
+  const int rows = w.rows, row0 = row_tile * 128, c1 = w.c1;
+  if (row0 >= rows) return;
+  const int np = load_pages(a, w, lds_page), p0 = w.c0 >> a.page_shift;
+
+  // Queries: lane (n, half) holds elements 32 i + 16 half .. + 15 of row n, as it does of the keys.
+  v8b_a qf[D / 32][2];
+  int lo, hi;
+  {
+    const int row = min(row0 + 32 * wave + n, rows - 1);   // behind the last row: that one again, not stored
+    const int t = w.t0 + row / a.per_kv, h = head * a.per_kv + row % a.per_kv;
+    const Range seen = row_keys(a, w, t);
+    lo = seen.first, hi = seen.end;
+    const uint16_t* x = a.q + t * a.q_token + h * a.q_head;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) qf[i][j] = *reinterpret_cast<const v8b_a*>(x + 32 * i + 16 * half + 8 * j);
+  }
+  int lo_min = lo, lo_max = lo, hi_min = hi, hi_max = hi;
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) {
+    lo_min = min(lo_min, __shfl_xor(lo_min, x, 64)), lo_max = max(lo_max, __shfl_xor(lo_max, x, 64));
+    hi_min = min(hi_min, __shfl_xor(hi_min, x, 64)), hi_max = max(hi_max, __shfl_xor(hi_max, x, 64));
+  }
+  lo_min = __builtin_amdgcn_readfirstlane(lo_min), lo_max = __builtin_amdgcn_readfirstlane(lo_max);
+  hi_min = __builtin_amdgcn_readfirstlane(hi_min), hi_max = __builtin_amdgcn_readfirstlane(hi_max);
+  if (lane == 0) lds_bounds[wave][0] = lo_min, lds_bounds[wave][1] = lo_max, lds_bounds[wave][2] = hi_min, lds_bounds[wave][3] = hi_max;
+  __syncthreads();
+  int all_lo_min = lo_min, all_lo_max = lo_max, all_hi_min = hi_min, all_hi_max = hi_max;   // over the workgroup's rows
+#pragma unroll
+  for (int u = 0; u < kWaves; ++u) {
+    all_lo_min = min(all_lo_min, lds_bounds[u][0]), all_lo_max = max(all_lo_max, lds_bounds[u][1]);
+    all_hi_min = min(all_hi_min, lds_bounds[u][2]), all_hi_max = max(all_hi_max, lds_bounds[u][3]);
+  }
+  const int begin = __builtin_amdgcn_readfirstlane(w.c0 + max(all_lo_min - w.c0, 0) / T::KEYS * T::KEYS);
+  const int stop = __builtin_amdgcn_readfirstlane(min(c1, all_hi_max));
+
+  // A wave stages keys 16 wave .. + 15 of a tile, which are in one page.
+  const int64_t head_rows = (int64_t)1 << a.page_shift;
+  u32x4_m fk[T::LOADS], fv[T::LOADS];
+  uint32_t fks[T::LOADS], fvs[T::LOADS];
+  auto row_of = [&](int key, int& page) {
+    page = __builtin_amdgcn_readfirstlane(lds_page[min((key >> a.page_shift) - p0, np - 1)]);
+    return ((int64_t)max(page, 0) * a.kv_heads + head) * head_rows + (key & (int)(head_rows - 1));
+  };
+  auto fetch = [&](int key0) {
+    int page;
+    const int64_t r0 = row_of(key0 + 16 * wave, page);
+    const uint8_t *kc = a.k_codes + r0 * D, *vc = a.v_codes + r0 * D, *ks = a.k_scales + r0 * T::SB, *vs = a.v_scales + r0 * T::SB;
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) {
+      const uint32_t sb = (uint32_t)((64 / T::LINE * i + lane / T::LINE) * T::SB + lane % T::LINE / 2);
+      fk[i] = load16(kc, (uint32_t)(1024 * i + 16 * lane)), fks[i] = ks[sb];
+      fv[i] = load16(vc, (uint32_t)(1024 * i + 16 * lane)), fvs[i] = vs[sb];
+      if (page < 0) fks[i] = 255u;
+    }
+  };
+  auto store = [&](int key0, int buf) {
+    uint8_t* b = lds + buf * T::BUFFER;
+    bool odd = false;
+    const bool edge = key0 < all_lo_max || key0 + T::KEYS > all_hi_min;
+    if (edge) {   // see k_attn_stream
+#pragma unroll
+      for (int i = 0; i < T::LOADS; ++i) {
+        if (key0 + 16 * wave + 64 / T::LINE * i + lane / T::LINE >= c1) fv[i] = u32x4_m{0u, 0u, 0u, 0u}, fvs[i] = 127u;
+        odd |= suspect(fv[i], fvs[i]);
+      }
+      odd = __any(odd);
+    }
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) {
+      const int row = 16 * wave + 64 / T::LINE * i + lane / T::LINE, col = lane % T::LINE;
+      u32x4_m kb[2], vb[2];
+      to_bf16(fk[i], fks[i], kb);
+      to_bf16(fv[i], fvs[i], vb);
+      if (__builtin_expect(odd, 0)) vb[0] = only_finite(vb[0]), vb[1] = only_finite(vb[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<u32x4_m*>(b + row * T::K_ROW + 32 * col + 16 * j) = kb[j];
+        *reinterpret_cast<u32x4_m*>(b + T::KEYS * T::K_ROW + row * T::V_ROW + 32 * col + 16 * j) = vb[j];
+      }
+    }
+    if (lane == 0) lds_odd[buf][wave] = odd;
+  };
+
+  v16f_m acc[D / 32];
+  float m = -kInf, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[i] = zeros16();
+  const bool idle = row0 + 32 * wave >= rows;
+
+  auto compute = [&](int key0, int buf) {
+    const uint8_t* b = lds + buf * T::BUFFER;
+    const bool edge = key0 < lo_max || key0 + T::KEYS > hi_min;
+    // Scores: register t of tile kt is key key0 + 32 kt + 8 (t / 4) + 4 half + t % 4, row n.
+    v16f_m sc[2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      sc[kt] = zeros16();
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              *reinterpret_cast<const v8b_a*>(b + (32 * kt + n) * T::K_ROW + 64 * i + 32 * half + 16 * j), qf[i][j], sc[kt], 0, 0, 0);
+    }
+    if (edge) {
+      asm volatile("");   // a branch: the compiler would compare and select in every tile
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const int key = key0 + 8 * (i >> 2) + 4 * half + (i & 3);
+        if ((uint32_t)(key - lo) >= (uint32_t)(hi - lo)) sc[i >> 4][i & 15] = -kInf;
+      }
+    }
+    float top = sc[0][0];
+#pragma unroll
+    for (int i = 1; i < 32; ++i) top = __builtin_fmaxf(top, sc[i >> 4][i & 15]);
+    const float mt = __builtin_fmaxf(m, pair_max(top) * a.scale_log2);
+    if (__any(mt > m + kLag)) {
+      const float keep = mt == -kInf ? 1.0f : exp2_of(m - mt);
+      m = mt, l *= keep;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] *= keep;
+    }
+    const float base = m == -kInf ? 0.0f : m;
+    v8b_a p[4];   // 16 keys each
+#pragma unroll
+    for (int step = 0; step < 4; ++step) {
+      u32x4_m words;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = exp2_of(__builtin_fmaf(sc[step >> 1][8 * (step & 1) + 2 * i], a.scale_log2, -base));
+        const float y = exp2_of(__builtin_fmaf(sc[step >> 1][8 * (step & 1) + 2 * i + 1], a.scale_log2, -base));
+        l += x + y;
+        words[i] = bf16_pair(x, y);
+      }
+      p[step] = __builtin_bit_cast(v8b_a, words);
+    }
+    // O^T += V^T P^T: keys 16 step .. + 15, elements 32 i .. + 31
+    const uint8_t* tr = b + T::KEYS * T::K_ROW + (4 * half + ((lane & 15) >> 2)) * T::V_ROW + 32 * ((lane >> 4) & 1) + 8 * (lane & 3);
+#pragma unroll
+    for (int step = 0; step < 4; ++step)
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint8_t* at = tr + 16 * step * T::V_ROW + 64 * i;
+        const v4s_a x = read_transposed(at), y = read_transposed(at + 8 * T::V_ROW);
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_bit_cast(v8b_a, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), p[step], acc[i], 0, 0, 0);
+      }
+    if (__builtin_expect((lds_odd[buf][0] | lds_odd[buf][1] | lds_odd[buf][2] | lds_odd[buf][3]) != 0, 0)) {
+      for (int key = key0; key < min(key0 + T::KEYS, c1); ++key) {
+        int page;
+        const int64_t row = row_of(key, page);
+        if ((uint32_t)(key - lo) >= (uint32_t)(hi - lo)) continue;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const float s = __uint_as_float((uint32_t)a.v_scales[row * T::SB + i] << 23);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(a.v_codes + row * D + 32 * i + 2 * j + 4 * half);
+            float c0 = acc[i][j], c1_ = acc[i][j + 1], c2 = acc[i][j + 2], c3 = acc[i][j + 3];
+            poison(u32x2_m{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, s, false)),
+                           __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, s, true))}, c0, c1_, c2, c3);
+            acc[i][j] = c0, acc[i][j + 1] = c1_, acc[i][j + 2] = c2, acc[i][j + 3] = c3;
+          }
+        }
+      }
+    }
+  };
+
+  if (begin < stop) {
+    fetch(begin);
+    store(begin, 0);
+    lds_barrier();
+    int buf = 0;
+    for (int key0 = begin; key0 < stop; key0 += T::KEYS, buf ^= 1) {
+      const bool more = key0 + T::KEYS < stop;
+      if (more) fetch(key0 + T::KEYS);
+      if (!idle && key0 < hi_max && key0 + T::KEYS > lo_min) compute(key0, buf);
+      if (more) store(key0 + T::KEYS, buf ^ 1);
+      lds_barrier();
+    }
+  }
+
+  // Register t of tile i is element 32 i + 8 (t / 4) + 4 half + t % 4 of row n.
+  const float sum = pair_sum(l);
+  const int at = row0 + 32 * wave + n;
+  if (at >= rows) return;
+  const int t = w.t0 + at / a.per_kv, h = head * a.per_kv + at % a.per_kv;
+  const int64_t place = (int64_t)t * a.kv_heads * a.per_kv + h;
+  if (w.slots == 1) {
+    float out_lse;
+    const float inv = finish(a, w.seq, t, m, sum, out_lse);
+    uint16_t* o = a.out + place * D + 4 * half;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<u32x2_m*>(o + 32 * i + 2 * j) =
+            u32x2_m{bf16_pair(acc[i][j] * inv, acc[i][j + 1] * inv), bf16_pair(acc[i][j + 2] * inv, acc[i][j + 3] * inv)};
+    if (a.lse && half == 0) a.lse[place] = out_lse;
+  } else {
+    const int64_t p = (int64_t)w.slot * a.tokens * a.kv_heads * a.per_kv + place;
+    float* o = a.part_o + p * D + 4 * half;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) *reinterpret_cast<v4f_m*>(o + 32 * i + 2 * j) = v4f_m{acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]};
+    if (half == 0) *reinterpret_cast<f32x2_m*>(a.part_ml + 2 * p) = f32x2_m{m, sum};
+  }
+}
+
+// Joins the slots of each row: one workgroup per query row, wave w takes slots w, w + 4, ... in rounds of eight with
+// their loads in flight, then the waves are added in their order.  Slots: those of the row's group's shared keys, then its
+// sequence's own.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+  constexpr int PER = D / 64, AHEAD = 8;
+  __shared__ float lds_o[kWaves][D], lds_ml[kWaves][2];
+  const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = blockIdx.x, all = (int64_t)a.tokens * q_heads;
+  const int t = (int)(row / q_heads);
+  const int s = wave_sequence(a.q_starts, a.seqs, t);
+  if (s < 0) return;
+  const int t0 = clamp_to(a.q_starts[s], 0, a.tokens), t1 = clamp_to(a.q_starts[s + 1], t0, a.tokens);
+  if (t - t0 >= a.max_q) return;   // past the call's bound: not computed
+  const int g = group_of(a, s), shared = g >= 0 ? shared_keys(a, g) : 0;
+  const int slots = shared_chunks(a, shared) + own_chunks(a, own_range(a, a.kv_lens[s], t1 - t0, shared));
+  if (slots == 1) return;   // written already
+  float top = -kInf, sum = 0.0f, v[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) v[e] = 0.0f;
+  for (int i0 = wave; i0 < slots; i0 += kWaves * AHEAD) {
+    float o[AHEAD][PER], m[AHEAD], l[AHEAD], most = top;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int slot = i0 + kWaves * i;
+      const int64_t p = min(slot, slots - 1) * all + row;
+      const f32x2_m ml = *reinterpret_cast<const f32x2_m*>(a.part_ml + 2 * p);
+      m[i] = slot < slots ? ml.x : -kInf, l[i] = slot < slots ? ml.y : 0.0f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[i][e] = a.part_o[p * D + PER * lane + e];
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) most = __builtin_fmaxf(most, m[i]);
+    const float keep = top == -kInf ? 0.0f : exp2_of(top - most);
+    sum *= keep;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) v[e] *= keep;
+    top = most;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (i0 + kWaves * i >= slots) break;
+      const float part = m[i] == -kInf ? 0.0f : exp2_of(m[i] - top);
+      sum += part * l[i];   // 0 times a NaN stays one
+#pragma unroll
+      for (int e = 0; e < PER; ++e) v[e] = __builtin_fmaf(part, o[i][e], v[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) lds_o[wave][PER * lane + e] = v[e];
+  if (lane == 0) lds_ml[wave][0] = top, lds_ml[wave][1] = sum;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  top = -kInf, sum = 0.0f;
+  float r = 0.0f;
+#pragma unroll
+  for (int u = 0; u < kWaves; ++u) top = __builtin_fmaxf(top, lds_ml[u][0]);
+#pragma unroll
+  for (int u = 0; u < kWaves; ++u) {
+    const float part = lds_ml[u][0] == -kInf ? 0.0f : exp2_of(lds_ml[u][0] - top);
+    sum += part * lds_ml[u][1];
+    r = __builtin_fmaf(part, lds_o[u][threadIdx.x], r);
+  }
+  float out_lse;
+  const float inv = finish(a, s, t, top, sum, out_lse);
+  a.out[row * D + threadIdx.x] = (uint16_t)bf16_pair(r * inv, 0.0f);
+  if (a.lse && threadIdx.x == 0) a.lse[row] = out_lse;
+}
+
+// How a pass is cut: rows per workgroup (16 or 32 by k_attn_stream, 128 by k_attn_tile), keys per workgroup.
 struct Cut {
-  int r, row_tiles, chunk, chunks;
+  int rows, row_tiles, chunk, chunks;
   int64_t grid;
 };
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in one launch
 constexpr int kFill = 1024;                            // workgroups that fill the card twice over
+constexpr int kManyRows = 32;                          // more rows than this: k_attn_tile
 
 // `rows` and `keys`: the most that one of the `items` has.  Keys are split only until the card is full.
 Cut cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys) {
   Cut c;
-  c.r = rows <= 16 || cache.head_dim > 128 ? 1 : 2;   // (two 16-row tiles of 256 elements spill registers)
-  c.row_tiles = (int)std::min<int64_t>((rows + 16 * c.r - 1) / (16 * c.r), INT32_MAX);
+  const bool many = rows > kManyRows;
+  c.rows = many ? 128 : rows <= 16 || cache.head_dim > 128 ? 16 : 32;   // (two 16-row tiles of 256 elements spill registers)
+  c.row_tiles = (int)std::min<int64_t>((rows + c.rows - 1) / c.rows, INT32_MAX);
   const int64_t units = items * cache.heads * c.row_tiles, step = kTile * kWaves;
-  const int64_t want = std::max<int64_t>(1, kFill / units);
+  const int64_t want = std::max<int64_t>(1, (many ? kFill / 4 : kFill) / units);
   int64_t chunk = (keys + want - 1) / want;
   // lengths differ: pieces that are all alike keep the longest sequence from being the last
-  if (c.row_tiles == 1) chunk = std::min<int64_t>(chunk, std::max<int64_t>(2048, keys / 64));
+  if (!many && c.row_tiles == 1) chunk = std::min<int64_t>(chunk, std::max<int64_t>(2048, keys / 64));
   chunk = std::max<int64_t>(step, (chunk + step - 1) / step * step);
   c.chunk = (int)std::min<int64_t>(chunk, (int64_t)kMaxPages << cache.page_shift);
   c.chunks = (int)std::max<int64_t>(1, (keys + c.chunk - 1) / c.chunk);
@@ -550,7 +862,7 @@ Plan plan(const KvCache& c, const KvBatch& b, const Attention& a) {
   if (a.window > 0) keys = std::min(keys, a.window + max_q - 1);
   Plan p;
   p.own = cut(b.seqs, c, max_q * per_kv, keys + kHalf - 1);
-  p.shared = Cut{1, 1, kTile * kWaves, 0, 0};
+  p.shared = Cut{16, 1, kTile * kWaves, 0, 0};
   if (b.groups > 0 && b.max_shared_len > 0)
     p.shared = cut(b.groups, c, a.tokens * per_kv, b.max_shared_len);
   p.slots = p.own.chunks + p.shared.chunks;
@@ -576,22 +888,25 @@ void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t 
   a.part_o = static_cast<float*>(t.scratch), a.part_ml = a.part_o + p.slots * rows * D;
   a.most_chunks = p.own.chunks, a.shared_chunk = p.shared.chunk;
   auto pass = [&](const Cut& k, bool shared) {
-    a.shared_pass = shared, a.chunk = p.own.chunk, a.chunks = k.chunks, a.row_tiles = k.row_tiles;
-    const unsigned lds = (unsigned)((k.chunk >> c.page_shift) + 2) * 4u;
-    if (k.r == 1) k_attn_stream<D, 1><<<(unsigned)k.grid, 256, lds, st>>>(a);
+    a.shared_pass = shared, a.items = shared ? (int)b.groups : (int)b.seqs, a.chunk = p.own.chunk, a.chunks = k.chunks;
+    a.row_tiles = k.row_tiles;
+    const unsigned pages = (unsigned)((k.chunk >> c.page_shift) + 2) * 4u;
+    const unsigned grid = (unsigned)k.grid;
+    if (k.rows == 16) k_attn_stream<D, 1><<<grid, 256, pages, st>>>(a);
+    else if (k.rows == 128) k_attn_tile<D><<<grid, 256, pages, st>>>(a);
     if constexpr (D <= 128)
-      if (k.r == 2) k_attn_stream<D, 2><<<(unsigned)k.grid, 256, lds, st>>>(a);
+      if (k.rows == 32) k_attn_stream<D, 2><<<grid, 256, pages, st>>>(a);
   };
   if (a.groups > 0) pass(p.shared, true);
   pass(p.own, false);
-  if (p.slots > 1) k_attn_join<D><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+  if (p.slots > 1) k_attn_join<D><<<(unsigned)rows, 256, 0, st>>>(a);
 }
 
 }  // namespace
 
 bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) {
   const Plan p = plan(c, b, a);
-  return p.own.grid <= kMaxGrid && p.shared.grid <= kMaxGrid && (a.tokens * a.q_heads + 3) / 4 <= kMaxGrid;
+  return p.own.grid <= kMaxGrid && p.shared.grid <= kMaxGrid && (p.slots == 1 || a.tokens * a.q_heads <= kMaxGrid);
 }
 
 int64_t attention_scratch(const KvCache& c, const KvBatch& b, const Attention& a) {

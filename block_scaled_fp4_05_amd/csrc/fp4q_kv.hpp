@@ -41,5 +41,11 @@ __device__ __forceinline__ int lane_find(const int32_t* __restrict__ starts, int
   return lo;
 }
 
+// The sequence of token t (the same in the whole wave), or -1: t is behind the last or before the first.
+__device__ __forceinline__ int wave_sequence(const int32_t* __restrict__ q_starts, int seqs, int t) {
+  const int s = wave_find(q_starts, seqs + 1, t);
+  return s < seqs ? s : -1;
+}
+
 }  // namespace
 }  // namespace fp4q

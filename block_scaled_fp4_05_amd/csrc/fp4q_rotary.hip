@@ -224,10 +224,9 @@ template <typename T>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
   constexpr int N = Chunk<T>::N, LANES = Chunk<T>::LANES;
   const int t = blockIdx.x;
-  const int s = wave_find(a.q_starts, a.seqs, t);
+  const int s = wave_sequence(a.q_starts, a.seqs, t);
   if (s < 0) return;
   const int end = a.q_starts[s + 1];
-  if (t >= end) return;   // behind the last sequence
   const int64_t place = (int64_t)a.kv_lens[s] - ((int64_t)end - t);   // the token's in its sequence
   if (place < 0 || (place >> a.page_shift) >= a.max_pages) return;
   const int at = (int)place;
