@@ -1,3 +1,6 @@
+#ifndef FILL
+#define FILL 2
+#endif
 // Attention over a paged MXFP8 cache of keys and values.
 //
 // For a query row q with the keys lo <= j < hi of its sequence:
@@ -32,7 +35,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 32;       // keys that a wave takes at a time
 constexpr int kWaves = 4;
 constexpr int kHalf = 16;       // keys of one MFMA, from a multiple of 16 on: never in two pages, whose least size it is
-constexpr int kMaxPages = 4096; // page ids of a workgroup's keys
+constexpr int kMaxPages = 1024; // page ids of a workgroup of k_attn_tile
+constexpr int kFewRows = 32;    // rows of a sequence and key/value head up to which k_attn_stream takes it
 
 struct AttnArgs {
   const uint16_t* q;
@@ -41,12 +45,22 @@ struct AttnArgs {
   const int32_t *q_starts, *kv_lens, *page_table, *group_starts, *shared_lens;
   int64_t pages, max_kv, max_shared;
   int max_q, tokens, seqs, groups, kv_heads, per_kv, page_shift, max_pages, window;
-  bool causal, shared_pass;   // shared_pass: the items are groups and their shared keys
-  int items, chunk, chunks, row_tiles;      // keys per workgroup of the own pass, workgroups per row tile, row tiles per item
-  int most_chunks, shared_chunk;            // of the own pass; keys per workgroup of the shared pass
+  bool causal;
   float scale_log2;                         // scale log2(e)
   uint16_t* out;
-  float *lse, *part_o, *part_ml;            // partial results: [slot][token][head][head_dim], [..][2]
+  float* lse;
+  // k_attn_stream
+  int groups_of_work;                       // its workgroups
+  // k_attn_tile
+  bool shared_pass;                         // the items are groups and their shared keys, else sequences and their own
+  int items, row_tiles, chunks;             // a pass's items, their row tiles, pieces of a row tile's keys
+  int own_chunk, own_chunks, shared_chunk;  // keys of a piece, most pieces
+  // Partial results, each with its m and l: of the shared pass [piece][token][head][head_dim], behind them k_attn_tile's
+  // own pieces or k_attn_stream's whole results of sequences that share keys; of pairs that several workgroups of
+  // k_attn_stream took, two pieces of piece_rows to a workgroup.
+  int shared_slots, piece_rows, few_rows;   // few_rows: the most that a pair has
+  float *part_o, *part_ml, *piece_o, *piece_ml;
+  int* taken;                               // [sequence][kv head][2 row tiles]: first workgroup and number of them
 };
 
 // The keys that an item's workgroups go through, from a multiple of 16 on.
@@ -78,21 +92,27 @@ __device__ __forceinline__ Range own_range(const AttnArgs& a, int kv, int q_len,
   first = min(first, kv) & ~(kHalf - 1);
   return Range{first, kv};
 }
-__device__ __forceinline__ int own_chunks(const AttnArgs& a, Range r) {
-  return clamp_to((r.end - r.first + a.chunk - 1) / a.chunk, 1, a.most_chunks);
+__device__ __forceinline__ int own_pieces(const AttnArgs& a, Range r) {
+  return clamp_to((r.end - r.first + a.own_chunk - 1) / a.own_chunk, 1, a.own_chunks);
 }
-__device__ __forceinline__ int shared_chunks(const AttnArgs& a, int shared) {
+__device__ __forceinline__ int shared_pieces(const AttnArgs& a, int shared) {
   return (shared + a.shared_chunk - 1) / a.shared_chunk;
 }
 
-// The keys lo .. hi-1 that the query token t of sequence s sees.
-__device__ __forceinline__ Range visible(const AttnArgs& a, int s, int t) {
-  const int kv = a.kv_lens[s];
+// The keys lo .. hi-1 that the query token t of a sequence sees, which has kv positions and whose tokens end
+// before q_end.
+__device__ __forceinline__ Range visible(const AttnArgs& a, int kv, int q_end, int t) {
   if (broken(a, kv)) return Range{0, 0};
-  const int64_t pos = (int64_t)kv - ((int64_t)a.q_starts[s + 1] - t);
+  const int64_t pos = (int64_t)kv - ((int64_t)q_end - t);
   Range r{0, kv};
   if (a.causal) r.end = (int)max((int64_t)0, min(pos + 1, (int64_t)kv));
   if (a.window > 0) r.first = (int)max((int64_t)0, min(pos + 1 - a.window, (int64_t)kv));
+  return r;
+}
+// Those of them before c1: from first to end, first <= end.
+__device__ __forceinline__ Range visible_to(const AttnArgs& a, int kv, int q_end, int t, int c1) {
+  Range r = visible(a, kv, q_end, t);
+  r.end = max(min(r.end, c1), r.first);
   return r;
 }
 
@@ -165,29 +185,36 @@ constexpr float kLag = 8.0f;
 struct Work {
   int head, seq, t0, rows;      // the item's first sequence and token, its rows
   int c0, c1;                   // keys
-  int slot, slots;              // where the result goes: with one slot, to the output
+  int slot;                     // of the partial result; -1: the result is whole and goes to the output
 };
+
+// Tokens of sequence s that the call computes, from t0 on.
+__device__ __forceinline__ int own_tokens(const AttnArgs& a, int s, int& t0) {
+  t0 = clamp_to(a.q_starts[s], 0, a.tokens);
+  return min(clamp_to(a.q_starts[s + 1], t0, a.tokens) - t0, a.max_q);
+}
+
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, int head, int piece, Work& w) {
   w.head = head;
-  int t1, first, end, chunk;
+  int n, first, end, chunk;
   if (a.shared_pass) {
     w.seq = clamp_to(a.group_starts[item], 0, a.seqs);
-    const int s1 = clamp_to(a.group_starts[item + 1], w.seq, a.seqs);
-    const int shared = shared_keys(a, item);
-    if (s1 == w.seq || piece >= shared_chunks(a, shared)) return false;
-    w.t0 = clamp_to(a.q_starts[w.seq], 0, a.tokens), t1 = clamp_to(a.q_starts[s1], w.t0, a.tokens);
-    first = 0, end = shared, chunk = a.shared_chunk, w.slot = piece, w.slots = 2;
+    const int s1 = clamp_to(a.group_starts[item + 1], w.seq, a.seqs), shared = shared_keys(a, item);
+    if (s1 == w.seq || piece >= shared_pieces(a, shared)) return false;
+    w.t0 = clamp_to(a.q_starts[w.seq], 0, a.tokens), n = clamp_to(a.q_starts[s1], w.t0, a.tokens) - w.t0;
+    first = 0, end = shared, chunk = a.shared_chunk, w.slot = piece;
   } else {
     w.seq = item;
-    w.t0 = clamp_to(a.q_starts[item], 0, a.tokens), t1 = clamp_to(a.q_starts[item + 1], w.t0, a.tokens);
-    const int kv = a.kv_lens[item], g = group_of(a, item), shared = g >= 0 ? shared_keys(a, g) : 0;
-    const Range own = own_range(a, kv, t1 - w.t0, shared);
-    const int pieces = own_chunks(a, own), before = shared_chunks(a, shared);
+    n = own_tokens(a, item, w.t0);
+    if (n * a.per_kv <= kFewRows) return false;   // k_attn_stream's
+    const int g = group_of(a, item), shared = g >= 0 ? shared_keys(a, g) : 0;
+    const Range own = own_range(a, a.kv_lens[item], n, shared);
+    const int pieces = own_pieces(a, own);
     if (piece >= pieces) return false;
-    t1 = min(t1, w.t0 + a.max_q);
-    first = own.first, end = own.end, chunk = a.chunk, w.slot = before + piece, w.slots = before + pieces;
+    first = own.first, end = own.end, chunk = a.own_chunk;
+    w.slot = pieces + shared_pieces(a, shared) == 1 ? -1 : a.shared_slots + piece;
   }
-  w.rows = (t1 - w.t0) * a.per_kv;
+  w.rows = n * a.per_kv;
   w.c0 = min(first + piece * chunk, end), w.c1 = min(w.c0 + chunk, end);
   return true;
 }
@@ -202,29 +229,69 @@ __device__ __forceinline__ int load_pages(const AttnArgs& a, const Work& w, int*
   return n;
 }
 
-// The keys that the row of a query token sees of the workgroup's: from first to end, first <= end.
-__device__ __forceinline__ Range row_keys(const AttnArgs& a, const Work& w, int t) {
-  Range r = visible(a, a.shared_pass ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : w.seq, t);
-  r.end = max(min(r.end, w.c1), r.first);
-  return r;
-}
-
 // 1 / l and lse of a row that is complete.  Nothing seen: zeros and -infinity; only scores of -infinity, or a length
 // out of bounds: NaN.
 __device__ __forceinline__ float finish(const AttnArgs& a, int seq, int t, float top, float sum, float& lse) {
   lse = (top + __builtin_amdgcn_logf(sum)) * kLn2;
   if (sum != 0.0f) return 1.0f / sum;
-  const Range seen = visible(a, seq, t);
+  const Range seen = visible(a, a.kv_lens[seq], a.q_starts[seq + 1], t);
   const bool none = seen.end <= seen.first && !broken(a, a.kv_lens[seq]);
   lse = none ? -kInf : __builtin_nanf("");
   return none ? 0.0f : __builtin_nanf("");
 }
 
 // -----------------------------------------------------------------------------------------
-// Few rows per key/value head: the keys' bytes are what counts.  A workgroup takes `chunk` keys of one
-// head; each of its four waves takes every fourth tile of 32 keys for all 16 R rows, with the next tile's loads in
-// flight, and no barrier until the waves' results are joined at the end.
+// Few rows per key/value head: the keys' bytes are what counts.  The work is a line of units, 128 keys of a pair
+// (sequence and key/value head) with all of its 16 R rows, sequence by sequence, and every workgroup takes the same
+// number of units in a row, so that lengths, which the host does not know, balance.  It finds its place by a
+// prefix sum over the sequences, takes pair after pair, and writes what it has of each: the output where it took a pair
+// whole, else a piece for k_attn_join.  Within a pair each of its four waves takes every fourth tile of 32 keys, with the
+// next tile's loads in flight, and no barrier until the waves' results are joined at the pair's end.
 // -----------------------------------------------------------------------------------------
+constexpr int kUnit = kTile * kWaves;
+
+// Units and row tiles of a sequence's pairs.
+struct Pairs {
+  int kv, q_end, t0, rows;
+  int tiles, units;             // units of one pair; the sequence has kv_heads * tiles pairs
+  Range keys;
+  bool shares;                  // keys of its group come from elsewhere
+};
+template <int R>
+__device__ __forceinline__ Pairs pairs_of(const AttnArgs& a, int s) {
+  Pairs p;
+  const int q_start = a.q_starts[s];
+  p.kv = a.kv_lens[s], p.q_end = a.q_starts[s + 1];
+  p.t0 = clamp_to(q_start, 0, a.tokens);
+  const int n = min(clamp_to(p.q_end, p.t0, a.tokens) - p.t0, a.max_q);
+  p.rows = n * a.per_kv;
+  p.tiles = p.rows <= kFewRows ? (p.rows + 16 * R - 1) / (16 * R) : 0;
+  int shared = 0;
+  if (a.groups > 0) {
+    const int g = lane_find(a.group_starts, a.groups + 1, s);
+    if (g >= 0 && g < a.groups) shared = shared_keys(a, g);
+  }
+  p.shares = shared > 0;
+  p.keys = own_range(a, p.kv, n, shared);
+  p.units = max(1, (p.keys.end - p.keys.first + kUnit - 1) / kUnit);
+  return p;
+}
+
+// The same value, held once for the wave: it is the same in all lanes.
+__device__ __forceinline__ Pairs uniform(const Pairs& p) {
+  auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  return Pairs{one(p.kv), one(p.q_end), one(p.t0), one(p.rows), one(p.tiles), one(p.units), Range{one(p.keys.first), one(p.keys.end)}, one(p.shares) != 0};
+}
+
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive sum over the lanes up to this one
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) {
+    const int o = __shfl_up(v, x, 64);
+    if ((int)(threadIdx.x & 63) >= x) v += o;
+  }
+  return v;
+}
+
 template <int D>
 struct Wave {
   static constexpr int ROW = 2 * D + 32;           // bytes of a row of V in LDS: 16 rows' 32-byte pieces on different banks
@@ -237,26 +304,76 @@ template <int D>
 struct Fetch {   // one tile
   u32x4_m k[2][Wave<D>::LOADS], v[2][Wave<D>::LOADS];
   uint32_t ks[2][D == 256 ? 2 : 1], vs[2][Wave<D>::LOADS];   // ks: the scale bytes of a lane's row
+  uint32_t none[2];                                          // all ones where the page is none: NaN scales
 };
 
+// Workgroups on a CU, by registers.
 template <int D, int R>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs a) {
+constexpr int kStreamPerCu = D == 64 ? 5 - R : D == 128 ? 2 : 1;
+
+template <int D, int R>
+__global__ __launch_bounds__(256, (kStreamPerCu<D, R>)) void k_attn_stream(AttnArgs a) {
   using W = Wave<D>;
   __shared__ __align__(16) uint8_t lds_v[kWaves][kTile * W::ROW];
   __shared__ float lds_ml[kWaves][16 * R][2];
-  extern __shared__ int lds_page[];   // the chunk's pages
+  __shared__ int lds_before[257];   // units per key/value head before each block of sequences
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g4 = lane >> 4;
-  int id = blockIdx.x;
-  const int piece = id % a.chunks;
-  id /= a.chunks;
-  const int row_tile = id % a.row_tiles;
-  id /= a.row_tiles;
-  Work w;
-  if (!find_work(a, id / a.kv_heads, id % a.kv_heads, piece, w)) return;
-  const int head = w.head, rows = w.rows, row0 = row_tile * 16 * R, t0 = w.t0, c0 = w.c0, c1 = w.c1;
-  if (row0 >= rows) return;
-  const int np = load_pages(a, w, lds_page), p0 = c0 >> a.page_shift;
+  const int block = (a.seqs + 255) >> 8;   // sequences to a block: one up to 256
+  {
+    int mine = 0;
+    for (int s = threadIdx.x * block; s < min((int)(threadIdx.x + 1) * block, a.seqs); ++s) {
+      const Pairs p = pairs_of<R>(a, s);
+      mine += p.tiles * p.units;
+    }
+    const int upto = wave_scan(mine);
+    if (lane == 63) lds_ml[0][wave][0] = __int_as_float(upto);
+    __syncthreads();
+    int before = 0;
+    for (int u = 0; u < wave; ++u) before += __float_as_int(lds_ml[0][u][0]);
+    lds_before[threadIdx.x + 1] = before + upto;
+    if (threadIdx.x == 0) lds_before[0] = 0;
+    __syncthreads();
+  }
+  const int all = lds_before[256] * a.kv_heads, each = (all + a.groups_of_work - 1) / a.groups_of_work;
+  const int me = blockIdx.x;
+  int unit = __builtin_amdgcn_readfirstlane((int)min((int64_t)me * each, (int64_t)all));
+  const int unit_end = __builtin_amdgcn_readfirstlane(min(unit + each, all));
+
+  while (unit < unit_end) {
+  // The sequence that has the unit, and its first one.
+  int seq, seq_unit;
+  {
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count += __popcll(__ballot(lds_before[64 * i + lane + 1] * a.kv_heads <= unit));
+    seq = count * block, seq_unit = lds_before[count];
+    if (block > 1) {
+      for (;;) {   // 64 sequences at a time; the block has the unit, so this ends in it
+        const Pairs p = pairs_of<R>(a, min(seq + lane, a.seqs - 1));
+        const int mine = seq + lane < a.seqs ? p.tiles * p.units : 0, upto = seq_unit + wave_scan(mine);
+        const uint64_t past = __ballot(upto * a.kv_heads > unit);
+        if (past) {
+          const int at = __builtin_ctzll(past);
+          seq_unit = __shfl(upto - mine, at, 64), seq += at;
+          break;
+        }
+        seq_unit = __shfl(upto, 63, 64), seq += 64;
+      }
+    }
+    seq = __builtin_amdgcn_readfirstlane(seq), seq_unit = __builtin_amdgcn_readfirstlane(seq_unit) * a.kv_heads;
+  }
+  const Pairs pairs = uniform(pairs_of<R>(a, seq));
+  const int pair = (unit - seq_unit) / pairs.units, pair_unit = seq_unit + pair * pairs.units, k0 = unit - pair_unit;
+  const int units = min(pairs.units - k0, unit_end - unit);
+  const int head = pair % a.kv_heads, row_tile = pair / a.kv_heads, rows = pairs.rows, row0 = row_tile * 16 * R, t0 = pairs.t0;
+  const int c0 = pairs.keys.first + k0 * kUnit, c1 = min(c0 + units * kUnit, pairs.keys.end);
+  const bool whole = units == pairs.units;
+  if (k0 == 0 && threadIdx.x == 0) {   // who has the pair: for k_attn_join
+    int* at = a.taken + 2 * (((int64_t)seq * a.kv_heads + head) * 2 + row_tile);
+    at[0] = me, at[1] = (pair_unit + pairs.units - 1) / each - me + 1;
+  }
+  unit += units;
 
   // Queries, the MFMA's second operand: lane (n, g4) holds elements 64 i + 16 g4 .. + 15 of row n, as it does of the keys.
   v8b_a qf[R][W::LOADS][2];
@@ -265,7 +382,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
   for (int r = 0; r < R; ++r) {
     const int row = min(row0 + 16 * r + n, rows - 1);   // behind the last row: that one again, not stored
     const int t = t0 + row / a.per_kv, h = head * a.per_kv + row % a.per_kv;
-    const Range seen = row_keys(a, w, t);
+    const Range seen = visible_to(a, pairs.kv, pairs.q_end, t, c1);
     lo[r] = seen.first, hi[r] = seen.end;
     const uint16_t* x = a.q + t * a.q_token + h * a.q_head;
 #pragma unroll
@@ -286,15 +403,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
   }
   lo_min = __builtin_amdgcn_readfirstlane(lo_min), lo_max = __builtin_amdgcn_readfirstlane(lo_max);
   hi_min = __builtin_amdgcn_readfirstlane(hi_min), hi_max = __builtin_amdgcn_readfirstlane(hi_max);
-  __syncthreads();
 
+  // Pages of the two halves of a tile, by scalar loads (a vector load's wait would be one for the rows asked for
+  // before it, too).  Past the keys: those of the last.
   const int64_t head_rows = (int64_t)1 << a.page_shift;
-  auto fetch = [&](int key0, Fetch<D>& f) {   // keys key0 .. key0 + 31; past the chunk's pages: those of its last
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)(a.page_table + (int64_t)seq * a.max_pages);
+  auto fetch = [&](int key0, Fetch<D>& f) {   // keys key0 .. key0 + 31
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int key = key0 + 16 * b, at = min((key >> a.page_shift) - p0, np - 1);
-      const int page = __builtin_amdgcn_readfirstlane(lds_page[at]);
-      const int64_t r0 = ((int64_t)max(page, 0) * a.kv_heads + head) * head_rows + (key & (int)(head_rows - 1));
+      const int key = key0 + 16 * b, page = table[min(min(key, c1 - 1) >> a.page_shift, a.max_pages - 1)];
+      const bool none = page < 0 || page >= a.pages;
+      const int64_t r0 = ((int64_t)(none ? 0 : page) * a.kv_heads + head) * head_rows + (key & (int)(head_rows - 1));
       const uint8_t *kc = a.k_codes + r0 * D, *vc = a.v_codes + r0 * D, *ks = a.k_scales + r0 * W::SB,
                     *vs = a.v_scales + r0 * W::SB;
 #pragma unroll
@@ -309,10 +428,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
 #pragma unroll
         for (int i = 0; i < D / 128; ++i) f.ks[b][i] = *reinterpret_cast<const uint32_t*>(ks + n * W::SB + 4 * i);
       }
-      if (page < 0) {
-#pragma unroll
-        for (uint32_t& w : f.ks[b]) w = 0xFFFFFFFFu;
-      }
+      f.none[b] = none ? 0xFFFFFFFFu : 0u;   // (applied where the scales are used: here it would wait for them)
     }
   };
 
@@ -329,12 +445,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
   const uint8_t* tr = mine + (4 * g4 + (n >> 2)) * W::ROW + 8 * (n & 3);
 
   const int begin = c0 + kTile * wave, stop = min(c1, hi_max);
-  Fetch<D> f;
-  if (begin < stop) fetch(begin, f);
-  for (int key0 = begin; key0 < stop; key0 += kTile * kWaves) {
-    Fetch<D> now = f;
-    if (key0 + kTile * kWaves < stop) fetch(key0 + kTile * kWaves, f);
-    if (key0 + kTile <= lo_min) continue;
+  // One tile of keys, in f, and the loads of the one after the next into f as soon as that is free.
+  auto step = [&](int key0, Fetch<D>& f) {
     const bool edge = key0 < lo_max || key0 + kTile > hi_min;   // some row does not see some key
 
     // Values to LDS as bf16.  Rows behind the chunk may hold anything: they become zeros.  So do values that are not finite
@@ -345,8 +457,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < W::LOADS; ++i) {
-          if (key0 + 16 * b + 64 / W::LINE * i + lane / W::LINE >= c1) now.v[b][i] = u32x4_m{0u, 0u, 0u, 0u}, now.vs[b][i] = 127u;
-          odd |= suspect(now.v[b][i], now.vs[b][i]);
+          if (key0 + 16 * b + 64 / W::LINE * i + lane / W::LINE >= c1) f.v[b][i] = u32x4_m{0u, 0u, 0u, 0u}, f.vs[b][i] = 127u;
+          odd |= suspect(f.v[b][i], f.vs[b][i]);
         }
       odd = __any(odd);
     }
@@ -357,7 +469,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
 #pragma unroll
         for (int i = 0; i < W::LOADS; ++i) {
           u32x4_m vb[2];
-          to_bf16(now.v[b][i], now.vs[b][i], vb);
+          to_bf16(f.v[b][i], f.vs[b][i], vb);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             *reinterpret_cast<u32x4_m*>(mine + (16 * b + 64 / W::LINE * i + lane / W::LINE) * W::ROW + 32 * (lane % W::LINE) + 16 * j) =
@@ -365,8 +477,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
         }
       wave_lds_fence();
     };
-    if (__builtin_expect(odd, 0)) put(true);
-    else put(false);
+    put(false);
+    if (__builtin_expect(odd, 0)) {
+      for (int k = 0; k < kTile; ++k)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if ((uint32_t)(key0 + k - lo[r]) < (uint32_t)(hi[r] - lo[r]))
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              v4f_m& c = acc[r][i];
+              float c0 = c[0], c1_ = c[1], c2 = c[2], c3 = c[3];
+              poison(*reinterpret_cast<const u32x2_m*>(mine + k * W::ROW + 32 * i + 8 * g4), c0, c1_, c2, c3);
+              c = v4f_m{c0, c1_, c2, c3};
+            }
+      put(true);
+    }
 
     // Scores: register j of half b is key key0 + 16 b + 4 g4 + j, row n.
     v4f_m s4[R][2];
@@ -377,7 +502,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
 #pragma unroll
       for (int i = 0; i < W::LOADS; ++i) {   // elements 64 i + 16 g4 ..: the row's scale byte 2 i + g4 / 2
         u32x4_m kb[2];
-        to_bf16(now.k[b][i], now.ks[b][i / 2] >> (16 * (i & 1) + 8 * (g4 >> 1)) & 0xFFu, kb);
+        to_bf16(f.k[b][i], (f.ks[b][i / 2] | f.none[b]) >> (16 * (i & 1) + 8 * (g4 >> 1)) & 0xFFu, kb);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -385,6 +510,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
             s4[r][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8b_a, kb[j]), qf[r][i][j], s4[r][b], 0, 0, 0);
       }
     }
+    if (key0 + kUnit < stop) fetch(key0 + kUnit, f);
     v8b_a p[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -430,21 +556,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
 #pragma unroll
       for (int r = 0; r < R; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], acc[r][i], 0, 0, 0);
     }
-    if (__builtin_expect(odd, 0)) {
-      put(false);
-      for (int k = 0; k < kTile; ++k)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if ((uint32_t)(key0 + k - lo[r]) < (uint32_t)(hi[r] - lo[r]))
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              v4f_m& c = acc[r][i];
-              float c0 = c[0], c1_ = c[1], c2 = c[2], c3 = c[3];
-              poison(*reinterpret_cast<const u32x2_m*>(mine + k * W::ROW + 32 * i + 8 * g4), c0, c1_, c2, c3);
-              c = v4f_m{c0, c1_, c2, c3};
-            }
-      wave_lds_fence();
-    }
+  };
+  {
+    const int from = begin + max(lo_min - begin, 0) / kUnit * kUnit;   // the first tile that some row sees
+    Fetch<D> f;
+    if (from < stop) fetch(from, f);
+    for (int key0 = from; key0 < stop; key0 += kUnit) step(key0, f);
   }
 
   // Join the waves in their order.
@@ -479,22 +596,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_stream(AttnArgs 
       }
       const int t = t0 + at / a.per_kv, h = head * a.per_kv + at % a.per_kv;
       const int64_t place = (int64_t)t * a.kv_heads * a.per_kv + h;
-      if (w.slots == 1) {
+      if (whole && !pairs.shares) {
         float out_lse;
-        const float inv = finish(a, w.seq, t, top, sum, out_lse);
+        const float inv = finish(a, seq, t, top, sum, out_lse);
 #pragma unroll
         for (int e = 0; e < PER; e += 4)
           *reinterpret_cast<u32x2_m*>(a.out + place * D + e0 + e) =
               u32x2_m{bf16_pair(v[e] * inv, v[e + 1] * inv), bf16_pair(v[e + 2] * inv, v[e + 3] * inv)};
         if (a.lse && e0 == 0) a.lse[place] = out_lse;
       } else {
-        const int64_t p = (int64_t)w.slot * a.tokens * a.kv_heads * a.per_kv + place;
+        // a whole result, or the workgroup's piece of the pair that it begins with (0) or ends with (1)
+        const int64_t p = whole ? (int64_t)a.shared_slots * a.tokens * a.kv_heads * a.per_kv + place
+                                : (int64_t)(2 * me + (k0 == 0)) * a.piece_rows + 16 * r + row;
+        float *po = whole ? a.part_o : a.piece_o, *pm = whole ? a.part_ml : a.piece_ml;
 #pragma unroll
-        for (int e = 0; e < PER; e += 4) *reinterpret_cast<v4f_m*>(a.part_o + p * D + e0 + e) = v4f_m{v[e], v[e + 1], v[e + 2], v[e + 3]};
-        if (e0 == 0) *reinterpret_cast<f32x2_m*>(a.part_ml + 2 * p) = f32x2_m{top, sum};
+        for (int e = 0; e < PER; e += 4) *reinterpret_cast<v4f_m*>(po + p * D + e0 + e) = v4f_m{v[e], v[e + 1], v[e + 2], v[e + 3]};
+        if (e0 == 0) *reinterpret_cast<f32x2_m*>(pm + 2 * p) = f32x2_m{top, sum};
       }
     }
     __syncthreads();
+  }
   }
 }
 
@@ -554,7 +675,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   {
     const int row = min(row0 + 32 * wave + n, rows - 1);   // behind the last row: that one again, not stored
     const int t = w.t0 + row / a.per_kv, h = head * a.per_kv + row % a.per_kv;
-    const Range seen = row_keys(a, w, t);
+    const int s = a.shared_pass ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : w.seq;
+    const Range seen = visible_to(a, a.kv_lens[s], a.q_starts[s + 1], t, c1);
     lo = seen.first, hi = seen.end;
     const uint16_t* x = a.q + t * a.q_token + h * a.q_head;
 #pragma unroll
@@ -584,7 +706,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   // A wave stages keys 16 wave .. + 15 of a tile, which are in one page.
   const int64_t head_rows = (int64_t)1 << a.page_shift;
   u32x4_m fk[T::LOADS], fv[T::LOADS];
-  uint32_t fks[T::LOADS], fvs[T::LOADS];
+  uint32_t fks[T::LOADS], fvs[T::LOADS], none = 0;
   auto row_of = [&](int key, int& page) {
     page = __builtin_amdgcn_readfirstlane(lds_page[min((key >> a.page_shift) - p0, np - 1)]);
     return ((int64_t)max(page, 0) * a.kv_heads + head) * head_rows + (key & (int)(head_rows - 1));
@@ -598,8 +720,8 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
       const uint32_t sb = (uint32_t)((64 / T::LINE * i + lane / T::LINE) * T::SB + lane % T::LINE / 2);
       fk[i] = load16(kc, (uint32_t)(1024 * i + 16 * lane)), fks[i] = ks[sb];
       fv[i] = load16(vc, (uint32_t)(1024 * i + 16 * lane)), fvs[i] = vs[sb];
-      if (page < 0) fks[i] = 255u;
     }
+    none = (uint32_t)(page >> 31) & 255u;   // (applied where the scales are used: here it would wait for them)
   };
   auto store = [&](int key0, int buf) {
     uint8_t* b = lds + buf * T::BUFFER;
@@ -617,7 +739,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
     for (int i = 0; i < T::LOADS; ++i) {
       const int row = 16 * wave + 64 / T::LINE * i + lane / T::LINE, col = lane % T::LINE;
       u32x4_m kb[2], vb[2];
-      to_bf16(fk[i], fks[i], kb);
+      to_bf16(fk[i], fks[i] | none, kb);
       to_bf16(fv[i], fvs[i], vb);
       if (__builtin_expect(odd, 0)) vb[0] = only_finite(vb[0]), vb[1] = only_finite(vb[1]);
 #pragma unroll
@@ -638,18 +760,25 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   auto compute = [&](int key0, int buf) {
     const uint8_t* b = lds + buf * T::BUFFER;
     const bool edge = key0 < lo_max || key0 + T::KEYS > hi_min;
+    const int odd = lds_odd[buf][0] | lds_odd[buf][1] | lds_odd[buf][2] | lds_odd[buf][3];
     // Scores: register t of tile kt is key key0 + 32 kt + 8 (t / 4) + 4 half + t % 4, row n.
-    v16f_m sc[2];
+    v16f_m sc[2] = {zeros16(), zeros16()};
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-      sc[kt] = zeros16();
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int kt = 0; kt < 2; ++kt)
           sc[kt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               *reinterpret_cast<const v8b_a*>(b + (32 * kt + n) * T::K_ROW + 64 * i + 32 * half + 16 * j), qf[i][j], sc[kt], 0, 0, 0);
+    // fragments are read six ahead of their products
+    __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);
+#pragma unroll
+    for (int i = 0; i < D / 8 - 6; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
     if (edge) {
       asm volatile("");   // a branch: the compiler would compare and select in every tile
 #pragma unroll
@@ -693,7 +822,14 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
         acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             __builtin_bit_cast(v8b_a, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7)), p[step], acc[i], 0, 0, 0);
       }
-    if (__builtin_expect((lds_odd[buf][0] | lds_odd[buf][1] | lds_odd[buf][2] | lds_odd[buf][3]) != 0, 0)) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 1);
+#pragma unroll
+    for (int i = 0; i < D / 8 - 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 1);
+    if (__builtin_expect(odd != 0, 0)) {
       for (int key = key0; key < min(key0 + T::KEYS, c1); ++key) {
         int page;
         const int64_t row = row_of(key, page);
@@ -734,7 +870,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   if (at >= rows) return;
   const int t = w.t0 + at / a.per_kv, h = head * a.per_kv + at % a.per_kv;
   const int64_t place = (int64_t)t * a.kv_heads * a.per_kv + h;
-  if (w.slots == 1) {
+  if (w.slot < 0) {
     float out_lse;
     const float inv = finish(a, w.seq, t, m, sum, out_lse);
     uint16_t* o = a.out + place * D + 4 * half;
@@ -756,36 +892,66 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   }
 }
 
-// Joins the slots of each row: one workgroup per query row, wave w takes slots w, w + 4, ... in rounds of eight with
-// their loads in flight, then the waves are added in their order.  Slots: those of the row's group's shared keys, then its
-// sequence's own.
-template <int D>
+// Joins the partial results of each row: one workgroup per query row, wave w takes every fourth in rounds of eight
+// with their loads in flight, then the waves are added in their order.  MANY: the rows of all tokens, and of them those of
+// sequences that k_attn_tile took; else the most rows of every pair that k_attn_stream took.
+template <int D, int R, bool MANY>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int PER = D / 64, AHEAD = 8;
   __shared__ float lds_o[kWaves][D], lds_ml[kWaves][2];
   const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = blockIdx.x, all = (int64_t)a.tokens * q_heads;
-  const int t = (int)(row / q_heads);
-  const int s = wave_sequence(a.q_starts, a.seqs, t);
-  if (s < 0) return;
-  const int t0 = clamp_to(a.q_starts[s], 0, a.tokens), t1 = clamp_to(a.q_starts[s + 1], t0, a.tokens);
-  if (t - t0 >= a.max_q) return;   // past the call's bound: not computed
-  const int g = group_of(a, s), shared = g >= 0 ? shared_keys(a, g) : 0;
-  const int slots = shared_chunks(a, shared) + own_chunks(a, own_range(a, a.kv_lens[s], t1 - t0, shared));
-  if (slots == 1) return;   // written already
+  const int64_t all = (int64_t)a.tokens * q_heads;
+  int s, t, h, t0;
+  if constexpr (MANY) {
+    t = blockIdx.x / q_heads, h = blockIdx.x % q_heads;
+    s = wave_sequence(a.q_starts, a.seqs, t);
+    if (s < 0) return;
+  } else {
+    const int in_pair = blockIdx.x % a.few_rows, pair = blockIdx.x / a.few_rows;
+    s = pair / a.kv_heads, t = in_pair / a.per_kv, h = pair % a.kv_heads * a.per_kv + in_pair % a.per_kv;
+  }
+  const int n = own_tokens(a, s, t0);
+  if constexpr (!MANY) t += t0;
+  if (t - t0 >= n || n * a.per_kv > kFewRows != MANY) return;
+  const int64_t row = (int64_t)t * q_heads + h;
+  // Where they are: `before` of the shared keys, then the own ones.
+  int before = 0, shared = 0, own, at = 0;
+  if (a.groups > 0) {
+    const int g = group_of(a, s);
+    shared = g >= 0 ? shared_keys(a, g) : 0, before = shared_pieces(a, shared);
+  }
+  bool pieces = false;
+  if constexpr (MANY) {
+    own = own_pieces(a, own_range(a, a.kv_lens[s], n, shared));
+  } else {
+    const int in_pair = (t - t0) * a.per_kv + h % a.per_kv, tile = in_pair / (16 * R);
+    const int* taken = a.taken + 2 * (((int64_t)s * a.kv_heads + h / a.per_kv) * 2 + tile);
+    at = (2 * taken[0] + 1) * a.piece_rows + in_pair % (16 * R), own = taken[1], pieces = own > 1;
+  }
+  const int count = before + own;
+  if (count == 1) return;   // written already
+  // number i, as an index of rows
+  auto place = [&](int i) -> int64_t {
+    if (i < before) return i * all + row;
+    i -= before;
+    if (!pieces) return (a.shared_slots + i) * all + row;
+    return at + (i == 0 ? 0 : (2 * i - 1) * a.piece_rows);   // the first ends with the pair, the others begin with it
+  };
   float top = -kInf, sum = 0.0f, v[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) v[e] = 0.0f;
-  for (int i0 = wave; i0 < slots; i0 += kWaves * AHEAD) {
+  for (int i0 = wave; i0 < count; i0 += kWaves * AHEAD) {
     float o[AHEAD][PER], m[AHEAD], l[AHEAD], most = top;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const int slot = i0 + kWaves * i;
-      const int64_t p = min(slot, slots - 1) * all + row;
-      const f32x2_m ml = *reinterpret_cast<const f32x2_m*>(a.part_ml + 2 * p);
-      m[i] = slot < slots ? ml.x : -kInf, l[i] = slot < slots ? ml.y : 0.0f;
+      const int slot = i0 + kWaves * i, in = min(slot, count - 1);
+      const int64_t p = place(in);
+      const bool piece = pieces && in >= before;
+      const float *po = (piece ? a.piece_o : a.part_o) + p * D + PER * lane, *pm = (piece ? a.piece_ml : a.part_ml) + 2 * p;
+      const f32x2_m ml = *reinterpret_cast<const f32x2_m*>(pm);
+      m[i] = slot < count ? ml.x : -kInf, l[i] = slot < count ? ml.y : 0.0f;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) o[i][e] = a.part_o[p * D + PER * lane + e];
+      for (int e = 0; e < PER; ++e) o[i][e] = po[e];
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) most = __builtin_fmaxf(most, m[i]);
@@ -796,7 +962,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     top = most;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      if (i0 + kWaves * i >= slots) break;
+      if (i0 + kWaves * i >= count) break;
       const float part = m[i] == -kInf ? 0.0f : exp2_of(m[i] - top);
       sum += part * l[i];   // 0 times a NaN stays one
 #pragma unroll
@@ -824,95 +990,114 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   if (a.lse && threadIdx.x == 0) a.lse[row] = out_lse;
 }
 
-// How a pass is cut: rows per workgroup (16 or 32 by k_attn_stream, 128 by k_attn_tile), keys per workgroup.
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in one launch
+constexpr int kCus = 256;
+
+// A pass of k_attn_tile: its row tiles and pieces of keys.
 struct Cut {
-  int rows, row_tiles, chunk, chunks;
+  int row_tiles, chunk, chunks;   // chunks 0: no such pass
   int64_t grid;
 };
-constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in one launch
-constexpr int kFill = 1024;                            // workgroups that fill the card twice over
-constexpr int kManyRows = 32;                          // more rows than this: k_attn_tile
-
 // `rows` and `keys`: the most that one of the `items` has.  Keys are split only until the card is full.
 Cut cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys) {
   Cut c;
-  const bool many = rows > kManyRows;
-  c.rows = many ? 128 : rows <= 16 || cache.head_dim > 128 ? 16 : 32;   // (two 16-row tiles of 256 elements spill registers)
-  c.row_tiles = (int)std::min<int64_t>((rows + c.rows - 1) / c.rows, INT32_MAX);
-  const int64_t units = items * cache.heads * c.row_tiles, step = kTile * kWaves;
-  const int64_t want = std::max<int64_t>(1, (many ? kFill / 4 : kFill) / units);
+  c.row_tiles = (int)((rows + 127) / 128);
+  const int64_t units = items * cache.heads * c.row_tiles, want = std::max<int64_t>(1, FILL * kCus / units);
   int64_t chunk = (keys + want - 1) / want;
-  // lengths differ: pieces that are all alike keep the longest sequence from being the last
-  if (!many && c.row_tiles == 1) chunk = std::min<int64_t>(chunk, std::max<int64_t>(2048, keys / 64));
-  chunk = std::max<int64_t>(step, (chunk + step - 1) / step * step);
+  chunk = std::max<int64_t>(kUnit, (chunk + kUnit - 1) / kUnit * kUnit);
   c.chunk = (int)std::min<int64_t>(chunk, (int64_t)kMaxPages << cache.page_shift);
-  c.chunks = (int)std::max<int64_t>(1, (keys + c.chunk - 1) / c.chunk);
+  c.chunks = (int)((keys + c.chunk - 1) / c.chunk);
   c.grid = units * c.chunks;
   return c;
 }
 
 struct Plan {
-  Cut own, shared;
-  int64_t slots;
+  int r;                    // row tiles of k_attn_stream's workgroups
+  int64_t stream, units;    // its workgroups; most units of all pairs
+  int64_t few, piece_rows;  // most rows of a pair, and in one of its row tiles
+  Cut own, shared;          // k_attn_tile's passes
+  bool join_few, join_many;
+  int64_t slots;            // partial results per row; the other parts of the scratch, in bytes from its start
+  int64_t part_ml, piece_o, piece_ml, taken, scratch;
 };
 Plan plan(const KvCache& c, const KvBatch& b, const Attention& a) {
-  const int64_t per_kv = a.q_heads / c.heads;
-  const int64_t max_q = std::min(a.tokens, b.max_q_len);
+  const int64_t per_kv = a.q_heads / c.heads, max_q = std::min(a.tokens, b.max_q_len), rows = a.tokens * a.q_heads;
   int64_t keys = b.max_kv_len;
   if (a.window > 0) keys = std::min(keys, a.window + max_q - 1);
-  Plan p;
-  p.own = cut(b.seqs, c, max_q * per_kv, keys + kHalf - 1);
-  p.shared = Cut{16, 1, kTile * kWaves, 0, 0};
-  if (b.groups > 0 && b.max_shared_len > 0)
-    p.shared = cut(b.groups, c, a.tokens * per_kv, b.max_shared_len);
-  p.slots = p.own.chunks + p.shared.chunks;
+  keys += kHalf - 1;
+  Plan p{};
+  const int64_t few = p.few = std::min<int64_t>(max_q * per_kv, kFewRows);
+  p.r = few <= 16 || c.head_dim > 128 ? 1 : 2;   // (two 16-row tiles of 256 elements spill registers)
+  p.piece_rows = std::min<int64_t>(few, 16 * p.r);
+  const int per_cu = c.head_dim == 64 ? 5 - p.r : c.head_dim == 128 ? 2 : 1;
+  const int64_t pair_units = (keys + kUnit - 1) / kUnit;
+  p.units = b.seqs * c.heads * ((few + 16 * p.r - 1) / (16 * p.r)) * pair_units;
+  p.stream = std::min<int64_t>(kCus * per_cu, p.units);
+  const bool many = max_q * per_kv > kFewRows, shares = b.groups > 0 && b.max_shared_len > 0;
+  p.own = many ? cut(b.seqs, c, max_q * per_kv, keys) : Cut{0, kUnit, 0, 0};
+  p.shared = shares ? cut(b.groups, c, a.tokens * per_kv, b.max_shared_len) : Cut{0, kUnit, 0, 0};
+  p.join_few = pair_units > 1 || shares, p.join_many = many && (p.own.chunks > 1 || shares);
+  p.slots = p.shared.chunks + std::max(p.own.chunks > 1 || shares ? p.own.chunks : 0, shares ? 1 : 0);
+  auto put = [&](int64_t& at, int64_t bytes) { at = p.scratch, p.scratch += (bytes + 15) / 16 * 16; };
+  int64_t part_o;
+  put(part_o, p.slots * rows * c.head_dim * 4);
+  put(p.part_ml, p.slots * rows * 8);
+  put(p.piece_o, p.stream * 2 * p.piece_rows * c.head_dim * 4);
+  put(p.piece_ml, p.stream * 2 * p.piece_rows * 8);
+  put(p.taken, b.seqs * c.heads * 16);
   return p;
+}
+
+template <int D, int R>
+void launch_few(const AttnArgs& a, const Plan& p, int64_t rows, hipStream_t st) {
+  k_attn_stream<D, R><<<(unsigned)p.stream, 256, 0, st>>>(a);
+  if (p.join_few) k_attn_join<D, R, false><<<(unsigned)(a.seqs * a.kv_heads * a.few_rows), 256, 0, st>>>(a);
+  if (p.join_many) k_attn_join<D, 1, true><<<(unsigned)rows, 256, 0, st>>>(a);
 }
 
 template <int D>
 void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t st) {
   const Plan p = plan(c, b, t);
-  const int64_t rows = t.tokens * t.q_heads;
   AttnArgs a{};
   a.q = static_cast<const uint16_t*>(t.q), a.q_token = t.q_token, a.q_head = t.q_head;
   a.k_codes = c.k_codes, a.k_scales = c.k_scales, a.v_codes = c.v_codes, a.v_scales = c.v_scales;
   a.q_starts = b.q_starts, a.kv_lens = b.kv_lens, a.page_table = b.page_table, a.group_starts = b.group_starts;
   a.shared_lens = b.shared_lens;
-  a.pages = c.pages, a.max_kv = b.max_kv_len, a.max_q = (int)std::min(t.tokens, b.max_q_len), a.tokens = (int)t.tokens, a.seqs = (int)b.seqs;
+  a.pages = c.pages, a.max_kv = b.max_kv_len, a.max_shared = b.max_shared_len;
+  a.max_q = (int)std::min(t.tokens, b.max_q_len), a.tokens = (int)t.tokens, a.seqs = (int)b.seqs;
   a.groups = p.shared.chunks > 0 ? (int)b.groups : 0;
   a.kv_heads = (int)c.heads, a.per_kv = (int)(t.q_heads / c.heads), a.page_shift = c.page_shift;
   a.max_pages = (int)b.max_pages, a.window = (int)std::min<int64_t>(t.window, 1 << 30), a.causal = t.causal;
-  a.max_shared = b.max_shared_len;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(t.out), a.lse = t.lse;
-  a.part_o = static_cast<float*>(t.scratch), a.part_ml = a.part_o + p.slots * rows * D;
-  a.most_chunks = p.own.chunks, a.shared_chunk = p.shared.chunk;
-  auto pass = [&](const Cut& k, bool shared) {
-    a.shared_pass = shared, a.items = shared ? (int)b.groups : (int)b.seqs, a.chunk = p.own.chunk, a.chunks = k.chunks;
-    a.row_tiles = k.row_tiles;
-    const unsigned pages = (unsigned)((k.chunk >> c.page_shift) + 2) * 4u;
-    const unsigned grid = (unsigned)k.grid;
-    if (k.rows == 16) k_attn_stream<D, 1><<<grid, 256, pages, st>>>(a);
-    else if (k.rows == 128) k_attn_tile<D><<<grid, 256, pages, st>>>(a);
-    if constexpr (D <= 128)
-      if (k.rows == 32) k_attn_stream<D, 2><<<grid, 256, pages, st>>>(a);
+  a.groups_of_work = (int)p.stream;
+  a.own_chunk = p.own.chunk, a.own_chunks = std::max(p.own.chunks, 1), a.shared_chunk = p.shared.chunk;
+  a.shared_slots = p.shared.chunks, a.piece_rows = (int)p.piece_rows, a.few_rows = (int)p.few;
+  char* s = static_cast<char*>(t.scratch);
+  a.part_o = reinterpret_cast<float*>(s), a.part_ml = reinterpret_cast<float*>(s + p.part_ml);
+  a.piece_o = reinterpret_cast<float*>(s + p.piece_o), a.piece_ml = reinterpret_cast<float*>(s + p.piece_ml);
+  a.taken = reinterpret_cast<int*>(s + p.taken);
+  auto tiles = [&](const Cut& k, int64_t items, bool shared) {
+    a.shared_pass = shared, a.items = (int)items, a.row_tiles = k.row_tiles, a.chunks = k.chunks;
+    k_attn_tile<D><<<(unsigned)k.grid, 256, (unsigned)((k.chunk >> c.page_shift) + 2) * 4u, st>>>(a);
   };
-  if (a.groups > 0) pass(p.shared, true);
-  pass(p.own, false);
-  if (p.slots > 1) k_attn_join<D><<<(unsigned)rows, 256, 0, st>>>(a);
+  if (p.shared.chunks > 0) tiles(p.shared, b.groups, true);
+  if (p.own.chunks > 0) tiles(p.own, b.seqs, false);
+  const int64_t rows = t.tokens * t.q_heads;
+  if constexpr (D <= 128)
+    if (p.r == 2) return launch_few<D, 2>(a, p, rows, st);
+  launch_few<D, 1>(a, p, rows, st);
 }
 
 }  // namespace
 
 bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) {
   const Plan p = plan(c, b, a);
-  return p.own.grid <= kMaxGrid && p.shared.grid <= kMaxGrid && (p.slots == 1 || a.tokens * a.q_heads <= kMaxGrid);
+  return p.own.grid <= kMaxGrid && p.shared.grid <= kMaxGrid && p.units <= INT32_MAX - kCus * 8 &&
+         (!p.join_many || a.tokens * a.q_heads <= kMaxGrid) && (!p.join_few || b.seqs * c.heads * p.few <= kMaxGrid);
 }
 
-int64_t attention_scratch(const KvCache& c, const KvBatch& b, const Attention& a) {
-  const int64_t slots = plan(c, b, a).slots;
-  return slots > 1 ? slots * a.tokens * a.q_heads * (c.head_dim + 2) * 4 : 16;
-}
+int64_t attention_scratch(const KvCache& c, const KvBatch& b, const Attention& a) { return plan(c, b, a).scratch; }
 
 void launch_attention(const KvCache& c, const KvBatch& b, const Attention& a, hipStream_t st) {
   if (c.head_dim == 64) launch<64>(c, b, a, st);
