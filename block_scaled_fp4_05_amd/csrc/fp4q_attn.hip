@@ -1,6 +1,3 @@
-#ifndef FILL
-#define FILL 2
-#endif
 // Attention over a paged MXFP8 cache of keys and values.
 //
 // For a query row q with the keys lo <= j < hi of its sequence:
@@ -35,8 +32,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kTile = 32;       // keys that a wave takes at a time
 constexpr int kWaves = 4;
 constexpr int kHalf = 16;       // keys of one MFMA, from a multiple of 16 on: never in two pages, whose least size it is
-constexpr int kMaxPages = 1024; // page ids of a workgroup of k_attn_tile
-constexpr int kFewRows = 32;    // rows of a sequence and key/value head up to which k_attn_stream takes it
+constexpr int kMaxPages = 1024; // page ids of a workgroup of many_rows
+constexpr int kFewRows = 32;    // rows of a sequence and key/value head up to which few_rows takes it
+
+// A pass of many_rows over its items' row tiles: pieces of `chunk` keys.
+struct Pass {
+  int items, row_tiles, chunk, chunks;   // chunks: the most pieces of a row tile; 0: no such pass
+  int grid;                              // workgroups
+};
 
 struct AttnArgs {
   const uint16_t* q;
@@ -49,16 +52,13 @@ struct AttnArgs {
   float scale_log2;                         // scale log2(e)
   uint16_t* out;
   float* lse;
-  // k_attn_stream
-  int groups_of_work;                       // its workgroups
-  // k_attn_tile
-  bool shared_pass;                         // the items are groups and their shared keys, else sequences and their own
-  int items, row_tiles, chunks;             // a pass's items, their row tiles, pieces of a row tile's keys
-  int own_chunk, own_chunks, shared_chunk;  // keys of a piece, most pieces
-  // Partial results, each with its m and l: of the shared pass [piece][token][head][head_dim], behind them k_attn_tile's
-  // own pieces or k_attn_stream's whole results of sequences that share keys; of pairs that several workgroups of
-  // k_attn_stream took, two pieces of piece_rows to a workgroup.
-  int shared_slots, piece_rows, few_rows;   // few_rows: the most that a pair has
+  int shares;                               // workgroups of few_rows
+  // many_rows, two passes: groups with the keys that they share, sequences with their own
+  Pass shared, own;
+  // Partial results, each with its m and l: of the shared pass [piece][token][head][head_dim], behind them many_rows'
+  // own pieces or few_rows' whole results of sequences that share keys; of pairs that several workgroups of
+  // few_rows took, two pieces of piece_rows to a workgroup.
+  int piece_rows, most_rows;                // most_rows: that a pair has
   float *part_o, *part_ml, *piece_o, *piece_ml;
   int* taken;                               // [sequence][kv head][2 row tiles]: first workgroup and number of them
 };
@@ -93,10 +93,10 @@ __device__ __forceinline__ Range own_range(const AttnArgs& a, int kv, int q_len,
   return Range{first, kv};
 }
 __device__ __forceinline__ int own_pieces(const AttnArgs& a, Range r) {
-  return clamp_to((r.end - r.first + a.own_chunk - 1) / a.own_chunk, 1, a.own_chunks);
+  return clamp_to((r.end - r.first + a.own.chunk - 1) / a.own.chunk, 1, max(a.own.chunks, 1));
 }
 __device__ __forceinline__ int shared_pieces(const AttnArgs& a, int shared) {
-  return (shared + a.shared_chunk - 1) / a.shared_chunk;
+  return (shared + a.shared.chunk - 1) / a.shared.chunk;
 }
 
 // The keys lo .. hi-1 that the query token t of a sequence sees, which has kv positions and whose tokens end
@@ -194,25 +194,27 @@ __device__ __forceinline__ int own_tokens(const AttnArgs& a, int s, int& t0) {
   return min(clamp_to(a.q_starts[s + 1], t0, a.tokens) - t0, a.max_q);
 }
 
+template <bool SHARED>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, int head, int piece, Work& w) {
+  const int chunk = SHARED ? a.shared.chunk : a.own.chunk;
   w.head = head;
-  int n, first, end, chunk;
-  if (a.shared_pass) {
+  int n, first, end;
+  if constexpr (SHARED) {
     w.seq = clamp_to(a.group_starts[item], 0, a.seqs);
     const int s1 = clamp_to(a.group_starts[item + 1], w.seq, a.seqs), shared = shared_keys(a, item);
     if (s1 == w.seq || piece >= shared_pieces(a, shared)) return false;
     w.t0 = clamp_to(a.q_starts[w.seq], 0, a.tokens), n = clamp_to(a.q_starts[s1], w.t0, a.tokens) - w.t0;
-    first = 0, end = shared, chunk = a.shared_chunk, w.slot = piece;
+    first = 0, end = shared, w.slot = piece;
   } else {
     w.seq = item;
     n = own_tokens(a, item, w.t0);
-    if (n * a.per_kv <= kFewRows) return false;   // k_attn_stream's
+    if (n * a.per_kv <= kFewRows) return false;   // few_rows'
     const int g = group_of(a, item), shared = g >= 0 ? shared_keys(a, g) : 0;
     const Range own = own_range(a, a.kv_lens[item], n, shared);
     const int pieces = own_pieces(a, own);
     if (piece >= pieces) return false;
-    first = own.first, end = own.end, chunk = a.own_chunk;
-    w.slot = pieces + shared_pieces(a, shared) == 1 ? -1 : a.shared_slots + piece;
+    first = own.first, end = own.end;
+    w.slot = pieces + shared_pieces(a, shared) == 1 ? -1 : a.shared.chunks + piece;
   }
   w.rows = n * a.per_kv;
   w.c0 = min(first + piece * chunk, end), w.c1 = min(w.c0 + chunk, end);
@@ -307,16 +309,19 @@ struct Fetch {   // one tile
   uint32_t none[2];                                          // all ones where the page is none: NaN scales
 };
 
-// Workgroups on a CU, by registers.
 template <int D, int R>
-constexpr int kStreamPerCu = D == 64 ? 5 - R : D == 128 ? 2 : 1;
+struct FewLds {
+  __align__(16) uint8_t v[kWaves][kTile * Wave<D>::ROW];
+  float ml[kWaves][16 * R][2];
+  int before[257];   // units per key/value head before each block of sequences
+};
 
 template <int D, int R>
-__global__ __launch_bounds__(256, (kStreamPerCu<D, R>)) void k_attn_stream(AttnArgs a) {
+__device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>& lds) {
   using W = Wave<D>;
-  __shared__ __align__(16) uint8_t lds_v[kWaves][kTile * W::ROW];
-  __shared__ float lds_ml[kWaves][16 * R][2];
-  __shared__ int lds_before[257];   // units per key/value head before each block of sequences
+  auto& lds_v = lds.v;
+  auto& lds_ml = lds.ml;
+  auto& lds_before = lds.before;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 15, g4 = lane >> 4;
   const int block = (a.seqs + 255) >> 8;   // sequences to a block: one up to 256
@@ -335,8 +340,7 @@ __global__ __launch_bounds__(256, (kStreamPerCu<D, R>)) void k_attn_stream(AttnA
     if (threadIdx.x == 0) lds_before[0] = 0;
     __syncthreads();
   }
-  const int all = lds_before[256] * a.kv_heads, each = (all + a.groups_of_work - 1) / a.groups_of_work;
-  const int me = blockIdx.x;
+  const int all = lds_before[256] * a.kv_heads, each = (all + a.shares - 1) / a.shares;
   int unit = __builtin_amdgcn_readfirstlane((int)min((int64_t)me * each, (int64_t)all));
   const int unit_end = __builtin_amdgcn_readfirstlane(min(unit + each, all));
 
@@ -606,7 +610,7 @@ __global__ __launch_bounds__(256, (kStreamPerCu<D, R>)) void k_attn_stream(AttnA
         if (a.lse && e0 == 0) a.lse[place] = out_lse;
       } else {
         // a whole result, or the workgroup's piece of the pair that it begins with (0) or ends with (1)
-        const int64_t p = whole ? (int64_t)a.shared_slots * a.tokens * a.kv_heads * a.per_kv + place
+        const int64_t p = whole ? (int64_t)a.shared.chunks * a.tokens * a.kv_heads * a.per_kv + place
                                 : (int64_t)(2 * me + (k0 == 0)) * a.piece_rows + 16 * r + row;
         float *po = whole ? a.part_o : a.piece_o, *pm = whole ? a.part_ml : a.piece_ml;
 #pragma unroll
@@ -650,21 +654,28 @@ __device__ __forceinline__ v16f_m zeros16() {
 }
 
 template <int D>
-__global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a) {
+struct ManyLds {
+  __align__(16) uint8_t tile[2 * Tile<D>::BUFFER];
+  int bounds[kWaves][4], odd[2][kWaves], page[kMaxPages + 2];
+};
+
+template <int D, bool SHARED>
+__device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D>& shared_lds) {
   using T = Tile<D>;
-  __shared__ __align__(16) uint8_t lds[2 * T::BUFFER];
-  __shared__ int lds_bounds[kWaves][4], lds_odd[2][kWaves];
-  extern __shared__ int lds_page[];   // the piece's pages
+  uint8_t* lds = shared_lds.tile;
+  auto& lds_bounds = shared_lds.bounds;
+  auto& lds_odd = shared_lds.odd;
+  int* lds_page = shared_lds.page;
+  const Pass& pass = SHARED ? a.shared : a.own;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, half = lane >> 5;
-  // Row tiles from the last on: under a causal mask it has the most keys.
-  const int per = a.chunks * a.kv_heads, items = a.items;
-  int id = blockIdx.x;
-  const int head = id % a.kv_heads, piece = id / a.kv_heads % a.chunks;
-  id /= per;
-  const int item = id % items, row_tile = a.row_tiles - 1 - id / items;
+  // Heads first, since workgroups go to the eight XCDs in turn and those of one head read the same keys; row tiles from the
+  // last on, which under a causal mask has the most keys.
+  const int head = id % a.kv_heads, piece = id / a.kv_heads % pass.chunks;
+  id /= pass.chunks * a.kv_heads;
+  const int item = id % pass.items, row_tile = pass.row_tiles - 1 - id / pass.items;
   Work w;
-  if (!find_work(a, item, head, piece, w)) return;
+  if (!find_work<SHARED>(a, item, head, piece, w)) return;
   const int rows = w.rows, row0 = row_tile * 128, c1 = w.c1;
   if (row0 >= rows) return;
   const int np = load_pages(a, w, lds_page), p0 = w.c0 >> a.page_shift;
@@ -675,7 +686,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   {
     const int row = min(row0 + 32 * wave + n, rows - 1);   // behind the last row: that one again, not stored
     const int t = w.t0 + row / a.per_kv, h = head * a.per_kv + row % a.per_kv;
-    const int s = a.shared_pass ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : w.seq;
+    const int s = SHARED ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : w.seq;
     const Range seen = visible_to(a, a.kv_lens[s], a.q_starts[s + 1], t, c1);
     lo = seen.first, hi = seen.end;
     const uint16_t* x = a.q + t * a.q_token + h * a.q_head;
@@ -727,7 +738,7 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
     uint8_t* b = lds + buf * T::BUFFER;
     bool odd = false;
     const bool edge = key0 < all_lo_max || key0 + T::KEYS > all_hi_min;
-    if (edge) {   // see k_attn_stream
+    if (edge) {   // see few_rows
 #pragma unroll
       for (int i = 0; i < T::LOADS; ++i) {
         if (key0 + 16 * wave + 64 / T::LINE * i + lane / T::LINE >= c1) fv[i] = u32x4_m{0u, 0u, 0u, 0u}, fvs[i] = 127u;
@@ -892,9 +903,35 @@ __global__ __launch_bounds__(256, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a)
   }
 }
 
+// Workgroups on a CU, by registers and LDS.
+template <int D, int R>
+constexpr int kFewPerCu = D == 64 ? 5 - R : D == 128 ? 2 : 1;
+template <int D>
+constexpr int kManyPerCu = D <= 128 ? 2 : 1;
+
+template <int D, int R>
+__global__ __launch_bounds__(256, (kFewPerCu<D, R>)) void k_attn_few(AttnArgs a) {
+  __shared__ FewLds<D, R> lds;
+  few_rows<D, R>(a, blockIdx.x, lds);
+}
+
+// One launch for all: the shared pass, the sequences with many rows, and those with few, which wait for memory while
+// the others multiply.
+template <int D, int R>
+__global__ __launch_bounds__(256, kManyPerCu<D>) void k_attn_all(AttnArgs a) {
+  __shared__ union {
+    FewLds<D, R> few;
+    ManyLds<D> many;
+  } lds;
+  const int id = blockIdx.x;
+  if (id < a.shared.grid) many_rows<D, true>(a, id, lds.many);
+  else if (id < a.shared.grid + a.own.grid) many_rows<D, false>(a, id - a.shared.grid, lds.many);
+  else few_rows<D, R>(a, id - a.shared.grid - a.own.grid, lds.few);
+}
+
 // Joins the partial results of each row: one workgroup per query row, wave w takes every fourth in rounds of eight
 // with their loads in flight, then the waves are added in their order.  MANY: the rows of all tokens, and of them those of
-// sequences that k_attn_tile took; else the most rows of every pair that k_attn_stream took.
+// sequences that many_rows took; else the most rows of every pair that few_rows took.
 template <int D, int R, bool MANY>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int PER = D / 64, AHEAD = 8;
@@ -907,7 +944,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     s = wave_sequence(a.q_starts, a.seqs, t);
     if (s < 0) return;
   } else {
-    const int in_pair = blockIdx.x % a.few_rows, pair = blockIdx.x / a.few_rows;
+    const int in_pair = blockIdx.x % a.most_rows, pair = blockIdx.x / a.most_rows;
     s = pair / a.kv_heads, t = in_pair / a.per_kv, h = pair % a.kv_heads * a.per_kv + in_pair % a.per_kv;
   }
   const int n = own_tokens(a, s, t0);
@@ -934,7 +971,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   auto place = [&](int i) -> int64_t {
     if (i < before) return i * all + row;
     i -= before;
-    if (!pieces) return (a.shared_slots + i) * all + row;
+    if (!pieces) return (a.shared.chunks + i) * all + row;
     return at + (i == 0 ? 0 : (2 * i - 1) * a.piece_rows);   // the first ends with the pair, the others begin with it
   };
   float top = -kInf, sum = 0.0f, v[PER];
@@ -993,29 +1030,24 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in one launch
 constexpr int kCus = 256;
 
-// A pass of k_attn_tile: its row tiles and pieces of keys.
-struct Cut {
-  int row_tiles, chunk, chunks;   // chunks 0: no such pass
-  int64_t grid;
-};
-// `rows` and `keys`: the most that one of the `items` has.  Keys are split only until the card is full.
-Cut cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys) {
-  Cut c;
-  c.row_tiles = (int)((rows + 127) / 128);
-  const int64_t units = items * cache.heads * c.row_tiles, want = std::max<int64_t>(1, FILL * kCus / units);
+// `rows` and `keys`: the most that one of the `items` has.  Keys are split only until every CU has a workgroup: more and
+// smaller pieces cost more in joining them (64 queries of 32 heads on a prefix of 16384: 256 workgroups 59 us, 512 61, 1024 76).
+Pass cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys, int64_t& grid) {
+  const int64_t row_tiles = (rows + 127) / 128, units = items * cache.heads * row_tiles;
+  const int64_t want = std::max<int64_t>(1, kCus / units);
   int64_t chunk = (keys + want - 1) / want;
   chunk = std::max<int64_t>(kUnit, (chunk + kUnit - 1) / kUnit * kUnit);
-  c.chunk = (int)std::min<int64_t>(chunk, (int64_t)kMaxPages << cache.page_shift);
-  c.chunks = (int)((keys + c.chunk - 1) / c.chunk);
-  c.grid = units * c.chunks;
-  return c;
+  chunk = std::min<int64_t>(chunk, (int64_t)kMaxPages << cache.page_shift);
+  const int64_t chunks = (keys + chunk - 1) / chunk;
+  grid += units * chunks;
+  return Pass{(int)items, (int)row_tiles, (int)chunk, (int)chunks, (int)std::min<int64_t>(units * chunks, kMaxGrid)};
 }
 
 struct Plan {
-  int r;                    // row tiles of k_attn_stream's workgroups
-  int64_t stream, units;    // its workgroups; most units of all pairs
-  int64_t few, piece_rows;  // most rows of a pair, and in one of its row tiles
-  Cut own, shared;          // k_attn_tile's passes
+  int r;                    // row tiles of few_rows' workgroups
+  int64_t few, grid, units; // its workgroups; all; most units of all pairs
+  int64_t most_rows, piece_rows;   // of a pair, and in one of its row tiles
+  Pass own, shared;
   bool join_few, join_many;
   int64_t slots;            // partial results per row; the other parts of the scratch, in bytes from its start
   int64_t part_ml, piece_o, piece_ml, taken, scratch;
@@ -1026,32 +1058,33 @@ Plan plan(const KvCache& c, const KvBatch& b, const Attention& a) {
   if (a.window > 0) keys = std::min(keys, a.window + max_q - 1);
   keys += kHalf - 1;
   Plan p{};
-  const int64_t few = p.few = std::min<int64_t>(max_q * per_kv, kFewRows);
-  p.r = few <= 16 || c.head_dim > 128 ? 1 : 2;   // (two 16-row tiles of 256 elements spill registers)
-  p.piece_rows = std::min<int64_t>(few, 16 * p.r);
-  const int per_cu = c.head_dim == 64 ? 5 - p.r : c.head_dim == 128 ? 2 : 1;
+  p.most_rows = std::min<int64_t>(max_q * per_kv, kFewRows);
+  p.r = p.most_rows <= 16 || c.head_dim > 128 ? 1 : 2;   // (two 16-row tiles of 256 elements spill registers)
+  p.piece_rows = std::min<int64_t>(p.most_rows, 16 * p.r);
+  const int per_cu = c.head_dim == 64 ? (p.r == 1 ? kFewPerCu<64, 1> : kFewPerCu<64, 2>) : c.head_dim == 128 ? kFewPerCu<128, 1> : kFewPerCu<256, 1>;
   const int64_t pair_units = (keys + kUnit - 1) / kUnit;
-  p.units = b.seqs * c.heads * ((few + 16 * p.r - 1) / (16 * p.r)) * pair_units;
-  p.stream = std::min<int64_t>(kCus * per_cu, p.units);
+  p.units = b.seqs * c.heads * ((p.most_rows + 16 * p.r - 1) / (16 * p.r)) * pair_units;
+  p.few = p.grid = std::min<int64_t>(kCus * per_cu, p.units);
   const bool many = max_q * per_kv > kFewRows, shares = b.groups > 0 && b.max_shared_len > 0;
-  p.own = many ? cut(b.seqs, c, max_q * per_kv, keys) : Cut{0, kUnit, 0, 0};
-  p.shared = shares ? cut(b.groups, c, a.tokens * per_kv, b.max_shared_len) : Cut{0, kUnit, 0, 0};
+  p.own = many ? cut(b.seqs, c, max_q * per_kv, keys, p.grid) : Pass{0, 0, kUnit, 0, 0};
+  p.shared = shares ? cut(b.groups, c, a.tokens * per_kv, b.max_shared_len, p.grid) : Pass{0, 0, kUnit, 0, 0};
   p.join_few = pair_units > 1 || shares, p.join_many = many && (p.own.chunks > 1 || shares);
   p.slots = p.shared.chunks + std::max(p.own.chunks > 1 || shares ? p.own.chunks : 0, shares ? 1 : 0);
   auto put = [&](int64_t& at, int64_t bytes) { at = p.scratch, p.scratch += (bytes + 15) / 16 * 16; };
   int64_t part_o;
   put(part_o, p.slots * rows * c.head_dim * 4);
   put(p.part_ml, p.slots * rows * 8);
-  put(p.piece_o, p.stream * 2 * p.piece_rows * c.head_dim * 4);
-  put(p.piece_ml, p.stream * 2 * p.piece_rows * 8);
+  put(p.piece_o, p.few * 2 * p.piece_rows * c.head_dim * 4);
+  put(p.piece_ml, p.few * 2 * p.piece_rows * 8);
   put(p.taken, b.seqs * c.heads * 16);
   return p;
 }
 
 template <int D, int R>
-void launch_few(const AttnArgs& a, const Plan& p, int64_t rows, hipStream_t st) {
-  k_attn_stream<D, R><<<(unsigned)p.stream, 256, 0, st>>>(a);
-  if (p.join_few) k_attn_join<D, R, false><<<(unsigned)(a.seqs * a.kv_heads * a.few_rows), 256, 0, st>>>(a);
+void launch_all(const AttnArgs& a, const Plan& p, int64_t rows, hipStream_t st) {
+  if (p.grid > p.few) k_attn_all<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
+  else k_attn_few<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
+  if (p.join_few) k_attn_join<D, R, false><<<(unsigned)(a.seqs * a.kv_heads * a.most_rows), 256, 0, st>>>(a);
   if (p.join_many) k_attn_join<D, 1, true><<<(unsigned)rows, 256, 0, st>>>(a);
 }
 
@@ -1070,31 +1103,24 @@ void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t 
   a.max_pages = (int)b.max_pages, a.window = (int)std::min<int64_t>(t.window, 1 << 30), a.causal = t.causal;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(t.out), a.lse = t.lse;
-  a.groups_of_work = (int)p.stream;
-  a.own_chunk = p.own.chunk, a.own_chunks = std::max(p.own.chunks, 1), a.shared_chunk = p.shared.chunk;
-  a.shared_slots = p.shared.chunks, a.piece_rows = (int)p.piece_rows, a.few_rows = (int)p.few;
+  a.shares = (int)p.few, a.shared = p.shared, a.own = p.own;
+  a.piece_rows = (int)p.piece_rows, a.most_rows = (int)p.most_rows;
   char* s = static_cast<char*>(t.scratch);
   a.part_o = reinterpret_cast<float*>(s), a.part_ml = reinterpret_cast<float*>(s + p.part_ml);
   a.piece_o = reinterpret_cast<float*>(s + p.piece_o), a.piece_ml = reinterpret_cast<float*>(s + p.piece_ml);
   a.taken = reinterpret_cast<int*>(s + p.taken);
-  auto tiles = [&](const Cut& k, int64_t items, bool shared) {
-    a.shared_pass = shared, a.items = (int)items, a.row_tiles = k.row_tiles, a.chunks = k.chunks;
-    k_attn_tile<D><<<(unsigned)k.grid, 256, (unsigned)((k.chunk >> c.page_shift) + 2) * 4u, st>>>(a);
-  };
-  if (p.shared.chunks > 0) tiles(p.shared, b.groups, true);
-  if (p.own.chunks > 0) tiles(p.own, b.seqs, false);
   const int64_t rows = t.tokens * t.q_heads;
   if constexpr (D <= 128)
-    if (p.r == 2) return launch_few<D, 2>(a, p, rows, st);
-  launch_few<D, 1>(a, p, rows, st);
+    if (p.r == 2) return launch_all<D, 2>(a, p, rows, st);
+  launch_all<D, 1>(a, p, rows, st);
 }
 
 }  // namespace
 
 bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) {
   const Plan p = plan(c, b, a);
-  return p.own.grid <= kMaxGrid && p.shared.grid <= kMaxGrid && p.units <= INT32_MAX - kCus * 8 &&
-         (!p.join_many || a.tokens * a.q_heads <= kMaxGrid) && (!p.join_few || b.seqs * c.heads * p.few <= kMaxGrid);
+  return p.grid <= kMaxGrid && p.units <= INT32_MAX - kCus * 8 && (!p.join_many || a.tokens * a.q_heads <= kMaxGrid) &&
+         (!p.join_few || b.seqs * c.heads * p.most_rows <= kMaxGrid);
 }
 
 int64_t attention_scratch(const KvCache& c, const KvBatch& b, const Attention& a) { return plan(c, b, a).scratch; }
