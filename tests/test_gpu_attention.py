@@ -157,7 +157,7 @@ def test_pages_outside_the_cache_and_lengths_outside_the_bounds():
 
 
 def _raw(q, cache, batch, out, lse, scratch=None, **kw):
-    c, b = B._kv_cache(cache, 0), B._kv_batch(batch, 0)
+    c, b = B._kv_cache(cache, 0)[0], B._kv_batch(batch, 0)
     n, h, d = q.shape
     need = B.fp4q_attention_paged_scratch(c, b, n, h, 0)
     scratch = torch.empty(need, dtype=torch.uint8, device=DEV) if scratch is None else scratch
