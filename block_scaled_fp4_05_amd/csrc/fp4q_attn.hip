@@ -60,7 +60,7 @@ struct AttnArgs {
   // few_rows took, two pieces of piece_rows to a workgroup.
   int piece_rows, most_rows;                // most_rows: that a pair has
   float *part_o, *part_ml, *piece_o, *piece_ml;
-  int* taken;                               // [sequence][kv head][2 row tiles]: first workgroup and number of them
+  int* taken;                               // [sequence][kv head][2 row tiles][4]: first workgroup, number of them, shared pieces
 };
 
 // The keys that an item's workgroups go through, from a multiple of 16 on.
@@ -257,7 +257,7 @@ struct Pairs {
   int kv, q_end, t0, rows;
   int tiles, units;             // units of one pair; the sequence has kv_heads * tiles pairs
   Range keys;
-  bool shares;                  // keys of its group come from elsewhere
+  int shared;                   // keys before them, of its group, that come from elsewhere
 };
 template <int R>
 __device__ __forceinline__ Pairs pairs_of(const AttnArgs& a, int s) {
@@ -268,13 +268,12 @@ __device__ __forceinline__ Pairs pairs_of(const AttnArgs& a, int s) {
   const int n = min(clamp_to(p.q_end, p.t0, a.tokens) - p.t0, a.max_q);
   p.rows = n * a.per_kv;
   p.tiles = p.rows <= kFewRows ? (p.rows + 16 * R - 1) / (16 * R) : 0;
-  int shared = 0;
+  p.shared = 0;
   if (a.groups > 0) {
     const int g = lane_find(a.group_starts, a.groups + 1, s);
-    if (g >= 0 && g < a.groups) shared = shared_keys(a, g);
+    if (g >= 0 && g < a.groups) p.shared = shared_keys(a, g);
   }
-  p.shares = shared > 0;
-  p.keys = own_range(a, p.kv, n, shared);
+  p.keys = own_range(a, p.kv, n, p.shared);
   p.units = max(1, (p.keys.end - p.keys.first + kUnit - 1) / kUnit);
   return p;
 }
@@ -282,7 +281,7 @@ __device__ __forceinline__ Pairs pairs_of(const AttnArgs& a, int s) {
 // The same value, held once for the wave: it is the same in all lanes.
 __device__ __forceinline__ Pairs uniform(const Pairs& p) {
   auto one = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-  return Pairs{one(p.kv), one(p.q_end), one(p.t0), one(p.rows), one(p.tiles), one(p.units), Range{one(p.keys.first), one(p.keys.end)}, one(p.shares) != 0};
+  return Pairs{one(p.kv), one(p.q_end), one(p.t0), one(p.rows), one(p.tiles), one(p.units), Range{one(p.keys.first), one(p.keys.end)}, one(p.shared)};
 }
 
 __device__ __forceinline__ int wave_scan(int v) {   // inclusive sum over the lanes up to this one
@@ -374,8 +373,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
   const int c0 = pairs.keys.first + k0 * kUnit, c1 = min(c0 + units * kUnit, pairs.keys.end);
   const bool whole = units == pairs.units;
   if (k0 == 0 && threadIdx.x == 0) {   // who has the pair: for k_attn_join
-    int* at = a.taken + 2 * (((int64_t)seq * a.kv_heads + head) * 2 + row_tile);
-    at[0] = me, at[1] = (pair_unit + pairs.units - 1) / each - me + 1;
+    int* at = a.taken + 4 * (((int64_t)seq * a.kv_heads + head) * 2 + row_tile);
+    at[0] = me, at[1] = (pair_unit + pairs.units - 1) / each - me + 1, at[2] = shared_pieces(a, pairs.shared);
   }
   unit += units;
 
@@ -600,7 +599,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
       }
       const int t = t0 + at / a.per_kv, h = head * a.per_kv + at % a.per_kv;
       const int64_t place = (int64_t)t * a.kv_heads * a.per_kv + h;
-      if (whole && !pairs.shares) {
+      if (whole && pairs.shared == 0) {
         float out_lse;
         const float inv = finish(a, seq, t, top, sum, out_lse);
 #pragma unroll
@@ -939,6 +938,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t all = (int64_t)a.tokens * q_heads;
   int s, t, h, t0;
+  int4 taken = {0, 0, 0, 0};
   if constexpr (MANY) {
     t = blockIdx.x / q_heads, h = blockIdx.x % q_heads;
     s = wave_sequence(a.q_starts, a.seqs, t);
@@ -946,24 +946,26 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   } else {
     const int in_pair = blockIdx.x % a.most_rows, pair = blockIdx.x / a.most_rows;
     s = pair / a.kv_heads, t = in_pair / a.per_kv, h = pair % a.kv_heads * a.per_kv + in_pair % a.per_kv;
+    // asked for along with the sequence's tokens; without any it means nothing
+    taken = *reinterpret_cast<const int4*>(a.taken + 4 * ((int64_t)pair * 2 + in_pair / (16 * R)));
   }
   const int n = own_tokens(a, s, t0);
   if constexpr (!MANY) t += t0;
   if (t - t0 >= n || n * a.per_kv > kFewRows != MANY) return;
   const int64_t row = (int64_t)t * q_heads + h;
   // Where they are: `before` of the shared keys, then the own ones.
-  int before = 0, shared = 0, own, at = 0;
-  if (a.groups > 0) {
-    const int g = group_of(a, s);
-    shared = g >= 0 ? shared_keys(a, g) : 0, before = shared_pieces(a, shared);
-  }
+  int before = 0, own, at = 0;
   bool pieces = false;
   if constexpr (MANY) {
+    int shared = 0;
+    if (a.groups > 0) {
+      const int g = group_of(a, s);
+      shared = g >= 0 ? shared_keys(a, g) : 0, before = shared_pieces(a, shared);
+    }
     own = own_pieces(a, own_range(a, a.kv_lens[s], n, shared));
   } else {
-    const int in_pair = (t - t0) * a.per_kv + h % a.per_kv, tile = in_pair / (16 * R);
-    const int* taken = a.taken + 2 * (((int64_t)s * a.kv_heads + h / a.per_kv) * 2 + tile);
-    at = (2 * taken[0] + 1) * a.piece_rows + in_pair % (16 * R), own = taken[1], pieces = own > 1;
+    before = taken.z, own = taken.y, pieces = own > 1;
+    at = (2 * taken.x + 1) * a.piece_rows + ((t - t0) * a.per_kv + h % a.per_kv) % (16 * R);
   }
   const int count = before + own;
   if (count == 1) return;   // written already
@@ -1076,7 +1078,7 @@ Plan plan(const KvCache& c, const KvBatch& b, const Attention& a) {
   put(p.part_ml, p.slots * rows * 8);
   put(p.piece_o, p.few * 2 * p.piece_rows * c.head_dim * 4);
   put(p.piece_ml, p.few * 2 * p.piece_rows * 8);
-  put(p.taken, b.seqs * c.heads * 16);
+  put(p.taken, b.seqs * c.heads * 32);
   return p;
 }
 

@@ -6,6 +6,7 @@
 // The pairs of a head of `rot` rotated elements are (i, i + rot/2) in the half layout and
 // (2i, 2i+1) in the interleaved one.  The map is m times a rotation, so its gradient is the same with -sin.
 #include "fp4q_kv.hpp"
+#include "fp4q_mx8.hpp"
 #include "fp4q_mxfp8.hpp"
 
 #include <type_traits>
@@ -79,58 +80,75 @@ __device__ __forceinline__ T narrow(float v) {
   else return v;
 }
 
-// Items of 16 bytes: rot/2 a multiple of the chunk in the half layout.  256 threads take one token: thread t
-// has item t % items of heads t / items, + 256 / items, ...
+// Items of 16 bytes: rot/2 a multiple of the chunk in the half layout.  A wave takes a token: lane l has item l % items of
+// heads l / items, + 64 / items, ..., with kAhead heads' loads in flight; the token's row of the table comes by way of
+// the wave's own LDS (see k_kv_append).
+constexpr int kAhead = 2;
+
 template <typename T, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a) {
-  constexpr int N = Chunk<T>::N;
-  const int64_t t = blockIdx.x;
+  constexpr int N = Chunk<T>::N, P = INTERLEAVED ? N / 2 : N;   // P: pairs per item
+  extern __shared__ __align__(16) f32x2 rows[];                 // [4][half]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t >= a.tokens) return;
   const int pos = a.positions[t];
   if (pos < 0 || pos >= a.table_rows) return;   // padding
+  f32x2* row = rows + wave * a.half;
+  for (int i = lane; i < a.half; i += 64) row[i] = a.table[(int64_t)pos * a.half + i];
+  wave_lds_fence();
   const int rot = 2 * a.half;
   const int turned = INTERLEAVED ? a.head_dim / N : a.half / N;              // items with a rotation (interleaved: or a part of one)
   const int items = INTERLEAVED ? turned : turned + (a.head_dim - rot) / N;
   const T* x = static_cast<const T*>(a.x) + t * a.x_token;
   T* y = static_cast<T*>(a.y) + t * a.y_token;
-  for (int first = 0; first < items; first += 256) {   // one round unless a head has over 256 items
-    const int now = min(items - first, 256), per = 256 / now;
-    const int item = first + (int)threadIdx.x % now, h0 = (int)threadIdx.x / now;
+  for (int first = 0; first < items; first += 64) {   // one round unless a head has over 64 items
+    const int now = min(items - first, 64), per = 64 / now;
+    const int item = first + lane % now, h0 = lane / now;
     if (h0 >= per) continue;
-    constexpr int P = INTERLEAVED ? N / 2 : N;   // pairs per item
+    const bool turns = INTERLEAVED || item < turned;
+    const int e = turns ? item * N : rot + (item - turned) * N;
     f32x2 cs[P];
-    const f32x2* row = a.table + (int64_t)pos * a.half;
+    if (turns) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int p = item * P + i;
-      const f32x2 v = row[min(p, a.half - 1)];
-      cs[i] = p < a.half ? f32x2{v.x, a.sign * v.y} : f32x2{1.0f, 0.0f};
+      for (int i = 0; i < P; ++i) {
+        const f32x2 v = row[min(item * P + i, a.half - 1)];
+        cs[i] = f32x2{v.x, a.sign * v.y};
+      }
     }
-    if (INTERLEAVED || item < turned) {
-      for (int h = h0; h < a.heads; h += per) {
-        const int64_t xa = h * a.x_head + item * N, ya = h * a.y_head + item * N;
+    for (int h = h0; h < a.heads; h += per * kAhead) {
+      u32x4_t one[kAhead], two[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const T* p = x + (int64_t)min(h + j * per, a.heads - 1) * a.x_head + e;
+        one[j] = load_chunk(p);
+        if (!INTERLEAVED && turns) two[j] = load_chunk(p + a.half);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (h + j * per >= a.heads) break;
+        T* p = y + (int64_t)(h + j * per) * a.y_head + e;
         float u[N], o[N];
+        if (!turns) {
+          *reinterpret_cast<u32x4_t*>(p) = one[j];
+          continue;
+        }
+        unpack(one[j], u);
         if constexpr (INTERLEAVED) {
-          unpack(load_chunk(x + xa), u);
 #pragma unroll
           for (int i = 0; i < P; ++i) {
             turn(u[2 * i], u[2 * i + 1], cs[i], o[2 * i], o[2 * i + 1]);
             if (item * P + i >= a.half) o[2 * i] = u[2 * i], o[2 * i + 1] = u[2 * i + 1];   // past the rotated part
           }
-          *reinterpret_cast<u32x4_t*>(y + ya) = pack(o);
         } else {
           float v[N], q[N];
-          unpack(load_chunk(x + xa), u);
-          unpack(load_chunk(x + xa + a.half), v);
+          unpack(two[j], v);
 #pragma unroll
           for (int i = 0; i < N; ++i) turn(u[i], v[i], cs[i], o[i], q[i]);
-          *reinterpret_cast<u32x4_t*>(y + ya) = pack(o);
-          *reinterpret_cast<u32x4_t*>(y + ya + a.half) = pack(q);
+          *reinterpret_cast<u32x4_t*>(p + a.half) = pack(q);
         }
+        *reinterpret_cast<u32x4_t*>(p) = pack(o);
       }
-    } else {
-      const int e = rot + (item - turned) * N;
-      for (int h = h0; h < a.heads; h += per)
-        *reinterpret_cast<u32x4_t*>(y + h * a.y_head + e) = load_chunk(x + h * a.x_head + e);
     }
   }
 }
@@ -160,21 +178,25 @@ __global__ __launch_bounds__(256) void k_rotary_pairs(RotaryArgs a) {
 }
 
 // -----------------------------------------------------------------------------------------
-// Append.  One workgroup per token; a lane takes one chunk (8 bf16 or 4 fp32) of the token's keys
+// Append.  A workgroup takes kAppendTokens tokens; a lane one chunk (8 bf16 or 4 fp32) of each one's keys
 // or values, so that neighbouring lanes hold the 32-element blocks as in the quantizer.
 //
-// A rotated key is rounded once, from the value of x1 cos - x2 sin: the products are exact in binary64, their
-// difference is rounded to 53 bits and then to odd in fp32, which E4M3's rounding does not see.
+// A rotated key is rounded once, from the value of x1 cos - x2 sin.  In fp32 that value is off by some 2^-23 of it, which
+// changes a code only next to a point halfway between two codes, or a scale next to its boundaries (1.75 2^k).  These have
+// at most five significant bits, so a result whose last 19 are within kNear of zero (one in 2^15) is computed again:
+// the products are exact in binary64, their difference is rounded to 53 bits and then to odd in fp32, which rounds to a
+// code as the difference does.  (All in binary64: 13460 tokens of 8 heads of 128 in 32 us, against 26.)
 // -----------------------------------------------------------------------------------------
+constexpr int kAppendTokens = 2;
+
 struct AppendArgs {
   const void *k, *v;
   int64_t k_token, k_head, v_token, v_head;
   const f32x2* table;
   int64_t table_rows;
   int half;
-  bool interleaved, aligned;   // aligned: a chunk's partners are a chunk
   const int32_t *positions, *q_starts, *kv_lens, *page_table;
-  int seqs, max_pages, page_shift, heads, head_dim;
+  int tokens, seqs, max_pages, page_shift, heads, head_dim;
   int64_t pages;
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
 };
@@ -188,81 +210,173 @@ __device__ __forceinline__ float to_odd(double r) {
   return __uint_as_float(b | 1u);
 }
 
-template <typename T>
-__device__ __forceinline__ void turned_key(const T* __restrict__ x, int e0, const f32x2* __restrict__ row, int half,
-                                           bool interleaved, bool aligned, float (&v)[Chunk<T>::N]) {
-  constexpr int N = Chunk<T>::N;
-  unpack(load_chunk(x + e0), v);
-  if (e0 >= 2 * half) return;
-  float w[N];
-  if (interleaved) {
+// x cos - other sin, rounded once in the sense of to_odd; other: an element's partner, its sign turned for the second
+// element of a pair.
+__device__ __forceinline__ float turned_exactly(float x, float other, f32x2 cs) {
+  return to_odd(__builtin_fma((double)x, (double)cs.x, -((double)other * (double)cs.y)));
+}
+// In fp32, within three roundings of the result; `near` falls to kNearLimit or below where that may not do.
+constexpr uint32_t kNear = 16;
+constexpr uint32_t kNearLimit = (2 * kNear) << 13;   // of the last 19 bits in the upper ones' place
+constexpr uint32_t kTiny = 30;   // and so it may in blocks with a scale code below this, whose results lose bits
+__device__ __forceinline__ float turned(float x, float other, f32x2 cs, uint32_t& near) {
+  const float far = other * cs.y;
+  const float y = __builtin_fmaf(x, cs.x, -far) - __builtin_fmaf(other, cs.y, -far);
+  near = min(near, (__float_as_uint(y) << 13) + (kNear << 13));
+  return y;
+}
+
+// Where a token's keys and values go and its row of the table.
+struct Place {
+  int64_t row;     // (page heads << page_shift) + row in the page: head h is (h << page_shift) further; -1: nowhere
+  int pos;         // -1: no such row
+};
+
+// Of token t in sequence s (-1: none) with kv positions, whose tokens end before q_end.
+__device__ __forceinline__ Place place_of(const AppendArgs& a, int t, int s, int q_end, int kv) {
+  Place p{-1, -1};
+  const int64_t at = (int64_t)kv - ((int64_t)q_end - t);   // its place in the sequence
+  if (s < 0 || at < 0 || (at >> a.page_shift) >= a.max_pages) return p;
+  const auto* table = (const __attribute__((address_space(4))) int32_t*)a.page_table;   // scalar loads
+  const int page = table[(int64_t)s * a.max_pages + (at >> a.page_shift)];
+  const int64_t pos = a.positions ? a.positions[t] : at;
+  if (pos >= 0 && pos < a.table_rows) p.pos = (int)pos;
+  if (page >= 0 && page < a.pages) p.row = (((int64_t)page * a.heads) << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+  return p;
+}
+
+// Of the tokens t0, t0 + 1, ...: up to 63 sequences are held by the wave's lanes, in one trip to memory.
+template <int TOKENS>
+__device__ __forceinline__ void find_places(const AppendArgs& a, int t0, Place (&p)[TOKENS]) {
+  const int lane = threadIdx.x & 63;
+  if (a.seqs < 64) {
+    const int start = a.q_starts[min(lane, a.seqs)], kv = a.kv_lens[min(lane, a.seqs - 1)];
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = v[i ^ 1];
-  } else if (aligned) {
-    unpack(load_chunk(x + (e0 < half ? e0 + half : e0 - half)), w);
+    for (int j = 0; j < TOKENS; ++j) {
+      const int t = t0 + j, s = __popcll(__ballot(lane <= a.seqs && start <= t)) - 1;
+      const bool some = s >= 0 && s < a.seqs && t < a.tokens;
+      const int at = some ? s : 0;
+      p[j] = place_of(a, t, some ? s : -1, __builtin_amdgcn_readlane(start, at + 1), __builtin_amdgcn_readlane(kv, at));
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = e0 + i;
-      w[i] = e < 2 * half ? widen(x[e < half ? e + half : e - half]) : 0.0f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = e0 + i;
-    const bool second = interleaved ? (i & 1) != 0 : e >= half;
-    const int p = interleaved ? e >> 1 : second ? e - half : e;
-    if (e < 2 * half) {
-      const f32x2 cs = row[p];
-      const double far = (double)w[i] * (double)cs.y;
-      v[i] = to_odd(__builtin_fma((double)v[i], (double)cs.x, second ? far : -far));
+    for (int j = 0; j < TOKENS; ++j) {
+      const int t = t0 + j, s = t < a.tokens ? __builtin_amdgcn_readfirstlane(wave_sequence(a.q_starts, a.seqs, t)) : -1;
+      p[j] = place_of(a, t, s, s < 0 ? 0 : __builtin_amdgcn_readfirstlane(a.q_starts[s + 1]),
+                      s < 0 ? 0 : __builtin_amdgcn_readfirstlane(a.kv_lens[s]));
     }
   }
 }
 
-template <typename T>
+template <int N>
+__device__ __forceinline__ void put_codes(uint8_t* p, const uint32_t (&w)[N / 4]) {
+  if constexpr (N == 8) *reinterpret_cast<u32x2_t*>(p) = u32x2_t{w[0], w[1]};
+  else *reinterpret_cast<uint32_t*>(p) = w[0];
+}
+
+// How keys are turned: not; in interleaved pairs; in halves, whose chunks meet chunks or not.
+enum Layout { kPlain, kPairs, kHalfChunks, kHalfAny };
+
+template <typename T, Layout L>
 __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
-  constexpr int N = Chunk<T>::N, LANES = Chunk<T>::LANES;
-  const int t = blockIdx.x;
-  const int s = wave_sequence(a.q_starts, a.seqs, t);
-  if (s < 0) return;
-  const int end = a.q_starts[s + 1];
-  const int64_t place = (int64_t)a.kv_lens[s] - ((int64_t)end - t);   // the token's in its sequence
-  if (place < 0 || (place >> a.page_shift) >= a.max_pages) return;
-  const int at = (int)place;
-  const int page = a.page_table[(int64_t)s * a.max_pages + (at >> a.page_shift)];
-  if (page < 0 || page >= a.pages) return;
-  const int pos = a.positions ? a.positions[t] : at;
-  const bool known = pos >= 0 && pos < a.table_rows;
-  const f32x2* row = a.table + (known ? (int64_t)pos * a.half : 0);
-  const int per = a.head_dim / N, chunks = a.heads * per;
-  const int in_page = at & ((1 << a.page_shift) - 1);
-  // whole blocks per wave: 2 * chunks is a multiple of LANES, and so is 256
-  for (int i = threadIdx.x; i < 2 * chunks; i += 256) {
+  constexpr int N = Chunk<T>::N, LANES = Chunk<T>::LANES, TOKENS = kAppendTokens;
+  extern __shared__ __align__(16) f32x2 rows[];   // [tokens][half]
+  const int t0 = blockIdx.x * TOKENS, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int per = a.head_dim / N, chunks = a.heads * per, rot = 2 * a.half;
+  // A lane's chunk is the same in every token: its loads go out before the tokens' places are known.
+  Place place[TOKENS];
+  for (int first = 0; first < 2 * chunks; first += 256) {
+    const bool live = first + (int)threadIdx.x < 2 * chunks;
+    const int i = min(first + (int)threadIdx.x, 2 * chunks - 1);
     const bool key = i < chunks;
     const int c = key ? i : i - chunks, h = c / per, e0 = (c - h * per) * N;
-    float v[N];
-    uint32_t w[N / 4];
-    if (key) {
-      const T* x = static_cast<const T*>(a.k) + t * a.k_token + h * a.k_head;
-      if (a.table && known) {
-        turned_key(x, e0, row, a.half, a.interleaved, a.aligned, v);
-      } else {
-        unpack(load_chunk(x + e0), v);
-        if (a.table) {   // no such row of the table: a key that no one takes for one
+    const bool turns = L != kPlain && key && e0 < rot;
+    const T* x = key ? static_cast<const T*>(a.k) + h * a.k_head + e0 : static_cast<const T*>(a.v) + h * a.v_head + e0;
+    const int64_t step = key ? a.k_token : a.v_token;
+    const int to_partner = e0 < a.half ? a.half : -a.half;
+    u32x4_t own[TOKENS], partner[TOKENS];
 #pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = __builtin_nanf("");
+    for (int j = 0; j < TOKENS; ++j) {
+      const T* p = x + min(t0 + j, a.tokens - 1) * step;
+      own[j] = load_chunk(p);
+      if constexpr (L == kHalfChunks) partner[j] = turns ? load_chunk(p + to_partner) : own[j];
+    }
+    if (first == 0) find_places<TOKENS>(a, t0, place);
+    if (L != kPlain && first == 0) {
+      // The tokens' rows of the table by way of LDS: a lane's pairs lie 64 bytes from its neighbour's, which costs the
+      // address unit as much as 64 lines for one load (13460 tokens of 8 heads of 128 in 32 us).
+      for (int j = wave; j < TOKENS; j += 4) {
+        int pos = place[0].pos;
+#pragma unroll
+        for (int k = 1; k < TOKENS; ++k) pos = j == k ? place[k].pos : pos;
+        const f32x2* row = a.table + (int64_t)max(pos, 0) * a.half;
+        for (int n = lane; n < a.half; n += 64) rows[j * a.half + n] = row[n];
+      }
+      __syncthreads();
+    }
+    const int pair = e0 >= a.half ? e0 - a.half : e0;
+    const uint32_t signs = e0 < a.half ? 0u : sizeof(T) == 2 ? 0x80008000u : 0x80000000u;
+    const uint32_t in_page = (uint32_t)(h << a.page_shift) * (uint32_t)a.head_dim + (uint32_t)e0;
+    uint8_t* codes = (key ? a.k_codes : a.v_codes) + in_page;
+    uint8_t* scales = (key ? a.k_scales : a.v_scales) + in_page / 32;
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) {
+      const int64_t at = place[j].row;
+      const int pos = place[j].pos;
+      if (at < 0) continue;
+      float v[N];
+      uint32_t w[N / 4];
+      unpack(own[j], v);
+      if (L != kPlain && key && pos < 0) {   // no such row of the table: a key that no one takes for one
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = __builtin_nanf("");
+      }
+      uint32_t near = ~0u;
+      // the chunk's elements through f(element, other, cosine and sine)
+      auto turn_all = [&](auto f) {
+        if constexpr (L == kPairs) {
+          const f32x2* row = rows + j * a.half;
+#pragma unroll
+          for (int n = 0; n < N; n += 2) {
+            if (e0 + n >= rot) continue;
+            const f32x2 c_ = row[(e0 + n) >> 1];
+            const float y0 = f(v[n], v[n + 1], c_), y1 = f(v[n + 1], -v[n], c_);
+            v[n] = y0, v[n + 1] = y1;
+          }
+        } else if constexpr (L == kHalfChunks) {
+          float u[N];
+          unpack(partner[j] ^ signs, u);
+#pragma unroll
+          for (int n = 0; n < N; ++n) v[n] = f(v[n], u[n], rows[j * a.half + pair + n]);
+        } else if constexpr (L == kHalfAny) {
+          const T* p = x + (int64_t)(t0 + j) * step;
+          const f32x2* row = rows + j * a.half;
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const int e = e0 + n;
+            const bool second = e >= a.half;
+            if (e >= rot) continue;
+            const float u = widen(p[n + (second ? -a.half : a.half)]);
+            v[n] = f(v[n], second ? -u : u, row[second ? e - a.half : e]);
+          }
+        }
+      };
+      const bool turn_it = turns && pos >= 0;
+      if (turn_it) turn_all([&](float x_, float w_, f32x2 c_) { return turned(x_, w_, c_, near); });
+      uint32_t code = mx8_encode<T>(v, w);
+      if constexpr (L != kPlain) {
+        if (__builtin_expect(__any(turn_it && (near <= kNearLimit || code < kTiny)), 0)) {
+          if (turn_it) {
+            unpack(own[j], v);
+            turn_all([&](float x_, float w_, f32x2 c_) { return turned_exactly(x_, w_, c_); });
+          }
+          code = mx8_encode<T>(v, w);
         }
       }
-    } else {
-      unpack(load_chunk(static_cast<const T*>(a.v) + t * a.v_token + h * a.v_head + e0), v);
+      const int64_t token = at * a.head_dim;
+      if (live) put_codes<N>(codes + token, w);
+      if (live && (threadIdx.x & (LANES - 1)) == 0) scales[token / 32] = (uint8_t)code;
     }
-    const uint32_t code = mx8_encode<T>(v, w);
-    const int64_t r = (((int64_t)page * a.heads + h) << a.page_shift) + in_page;
-    uint8_t* codes = (key ? a.k_codes : a.v_codes) + r * a.head_dim + e0;
-    if constexpr (N == 8) *reinterpret_cast<u32x2_t*>(codes) = u32x2_t{w[0], w[1]};
-    else *reinterpret_cast<uint32_t*>(codes) = w[0];
-    if ((threadIdx.x & (LANES - 1)) == 0) (key ? a.k_scales : a.v_scales)[r * (a.head_dim / 32) + e0 / 32] = (uint8_t)code;
   }
 }
 
@@ -280,29 +394,39 @@ void launch_rotary(const Rotary& r, hipStream_t st) {
   const RotaryArgs a{r.x, r.y, r.positions, reinterpret_cast<const f32x2*>(r.table), r.table_rows, r.x_token, r.x_head,
                      r.y_token, r.y_head, r.tokens, r.heads, r.head_dim, r.rot / 2, r.backward ? -1.0f : 1.0f,
                      r.interleaved};
-  const unsigned grid = (unsigned)r.tokens;
+  const unsigned grid = (unsigned)r.tokens, grid4 = (unsigned)((r.tokens + 3) / 4), lds = 4 * (unsigned)a.half * 8u;
   const int n = r.dtype ? 8 : 4;
   if (r.interleaved) {
-    if (r.dtype) k_rotary<uint16_t, true><<<grid, 256, 0, st>>>(a);
-    else k_rotary<float, true><<<grid, 256, 0, st>>>(a);
+    if (r.dtype) k_rotary<uint16_t, true><<<grid4, 256, lds, st>>>(a);
+    else k_rotary<float, true><<<grid4, 256, lds, st>>>(a);
   } else if (a.half % n == 0) {
-    if (r.dtype) k_rotary<uint16_t, false><<<grid, 256, 0, st>>>(a);
-    else k_rotary<float, false><<<grid, 256, 0, st>>>(a);
+    if (r.dtype) k_rotary<uint16_t, false><<<grid4, 256, lds, st>>>(a);
+    else k_rotary<float, false><<<grid4, 256, lds, st>>>(a);
   } else {
     if (r.dtype) k_rotary_pairs<uint16_t><<<grid, 256, 0, st>>>(a);
     else k_rotary_pairs<float><<<grid, 256, 0, st>>>(a);
   }
 }
 
+template <typename T>
+void append(const AppendArgs& a, Layout l, hipStream_t st) {
+  const unsigned grid = (unsigned)((a.tokens + kAppendTokens - 1) / kAppendTokens);
+  const unsigned lds = kAppendTokens * (unsigned)a.half * 8u;
+  if (l == kPlain) k_kv_append<T, kPlain><<<grid, 256, 0, st>>>(a);
+  else if (l == kPairs) k_kv_append<T, kPairs><<<grid, 256, lds, st>>>(a);
+  else if (l == kHalfChunks) k_kv_append<T, kHalfChunks><<<grid, 256, lds, st>>>(a);
+  else k_kv_append<T, kHalfAny><<<grid, 256, lds, st>>>(a);
+}
+
 void launch_kv_append(const KvCache& c, const KvBatch& b, const KvAppend& p, hipStream_t st) {
   const int n = p.dtype ? 8 : 4, half = p.table ? p.rot / 2 : 0;
   const AppendArgs a{p.k, p.v, p.k_token, p.k_head, p.v_token, p.v_head, reinterpret_cast<const f32x2*>(p.table),
-                     p.table_rows, half, p.interleaved, half % n == 0, p.positions, b.q_starts, b.kv_lens,
-                     b.page_table, (int)b.seqs, (int)b.max_pages, c.page_shift, (int)c.heads, (int)c.head_dim, c.pages,
-                     c.k_codes, c.k_scales, c.v_codes, c.v_scales};
-  const unsigned grid = (unsigned)p.tokens;
-  if (p.dtype) k_kv_append<uint16_t><<<grid, 256, 0, st>>>(a);
-  else k_kv_append<float><<<grid, 256, 0, st>>>(a);
+                     p.table_rows, half, p.positions, b.q_starts, b.kv_lens, b.page_table, (int)p.tokens, (int)b.seqs,
+                     (int)b.max_pages, c.page_shift, (int)c.heads, (int)c.head_dim, c.pages, c.k_codes, c.k_scales,
+                     c.v_codes, c.v_scales};
+  const Layout l = !p.table ? kPlain : p.interleaved ? kPairs : half % n == 0 ? kHalfChunks : kHalfAny;
+  if (p.dtype) append<uint16_t>(a, l, st);
+  else append<float>(a, l, st);
 }
 
 }  // namespace fp4q
