@@ -539,7 +539,8 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t* x_codes, const uint8_t* x_scales, cons
 
 fp4q_status fp4q_rotary_table(int64_t positions, int64_t rot_dim, double base, double factor, double original,
                               double low, double high, double amplitude, float* table, hipStream_t stream) {
-  if (positions < 1 || positions > INT32_MAX || rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0)
+  if (positions < 1 || positions > INT32_MAX || rot_dim < 2 || rot_dim > 1024 || rot_dim % 2 != 0 ||
+      positions > ((int64_t)1 << 36) / rot_dim)   // half a TiB: also keeps a launch's threads within 32 bits
     return FP4Q_E_SHAPE;
   if (!table) return FP4Q_E_NULL;
   if (!(base > 0.0 && base <= DBL_MAX) || !(factor > 0.0 && factor <= DBL_MAX) || !(amplitude >= -DBL_MAX && amplitude <= DBL_MAX))

@@ -176,8 +176,10 @@ __device__ __forceinline__ v4s_a read_transposed(const uint8_t* p) {
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// A row's m need not be its largest score so far: it follows only where that is more than 2^kLag times
-// larger, so that l and o, which have fp32's range, are rarely multiplied.
+// Where the products count (many_rows) a row's m need not be its largest score so far: it follows only where that
+// is more than 2^kLag times larger, so that l and o, which have fp32's range, are rarely multiplied (prompts of 1021 to 4096
+// tokens 215 -> 205 us).  Where they do not, m is the largest, whose p = 1 is exact in bf16 (on few keys out is
+// 1.9e-3 of its norm off instead of 2.3e-3).
 constexpr float kLag = 8.0f;
 
 // What a workgroup works on: the rows of an item (a sequence's query tokens, or in the shared pass a group's, times the
@@ -352,7 +354,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
     for (int i = 0; i < 4; ++i) count += __popcll(__ballot(lds_before[64 * i + lane + 1] * a.kv_heads <= unit));
     seq = count * block, seq_unit = lds_before[count];
     if (block > 1) {
-      for (;;) {   // 64 sequences at a time; the block has the unit, so this ends in it
+      while (seq < a.seqs) {   // 64 sequences at a time
         const Pairs p = pairs_of<R>(a, min(seq + lane, a.seqs - 1));
         const int mine = seq + lane < a.seqs ? p.tiles * p.units : 0, upto = seq_unit + wave_scan(mine);
         const uint64_t past = __ballot(upto * a.kv_heads > unit);
@@ -366,7 +368,10 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
     }
     seq = __builtin_amdgcn_readfirstlane(seq), seq_unit = __builtin_amdgcn_readfirstlane(seq_unit) * a.kv_heads;
   }
+  if (seq >= a.seqs) break;
   const Pairs pairs = uniform(pairs_of<R>(a, seq));
+  // Lengths that change under the call (a mistake of its caller's) could name a pair that is none.
+  if (unit < seq_unit || unit - seq_unit >= (int64_t)pairs.units * pairs.tiles * a.kv_heads) break;
   const int pair = (unit - seq_unit) / pairs.units, pair_unit = seq_unit + pair * pairs.units, k0 = unit - pair_unit;
   const int units = min(pairs.units - k0, unit_end - unit);
   const int head = pair % a.kv_heads, row_tile = pair / a.kv_heads, rows = pairs.rows, row0 = row_tile * 16 * R, t0 = pairs.t0;
@@ -535,7 +540,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
 #pragma unroll
       for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, sc[i]);
       const float mt = __builtin_fmaxf(m[r], quad_max(top));
-      if (__any(mt > m[r] + kLag)) {
+      if (__any(mt > m[r])) {
         const float keep = mt == -kInf ? 1.0f : exp2_of(m[r] - mt);
         m[r] = mt, l[r] *= keep;
 #pragma unroll
@@ -1121,7 +1126,7 @@ void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t 
 
 bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) {
   const Plan p = plan(c, b, a);
-  return p.grid <= kMaxGrid && p.units <= INT32_MAX - kCus * 8 && (!p.join_many || a.tokens * a.q_heads <= kMaxGrid) &&
+  return p.grid <= kMaxGrid && p.units <= ((int64_t)1 << 30) && (!p.join_many || a.tokens * a.q_heads <= kMaxGrid) &&
          (!p.join_few || b.seqs * c.heads * p.most_rows <= kMaxGrid);
 }
 

@@ -534,7 +534,7 @@ fp4q_status fp4q_rotary(const void* x, fp4q_dtype dt, int64_t tokens, int64_t he
  * the turns.  factor 1: no scaling, the other three are not read; to divide every frequency pass
  * original 0, low 0, high 1.
  * base > 0, factor > 0, original >= 0, low < high, amplitude: finite (FP4Q_E_ARG).
- * Shapes: 1 <= positions < 2^31, rot_dim even, 2 .. 1024.  Alignment: 16 bytes.
+ * Shapes: 1 <= positions < 2^31, rot_dim even, 2 .. 1024, positions * rot_dim <= 2^36.  Alignment: 16 bytes.
  */
 fp4q_status fp4q_rotary_table(int64_t positions, int64_t rot_dim, double base, double factor, double original,
                               double low, double high, double amplitude, float* table, hipStream_t stream);

@@ -55,7 +55,7 @@ def _need(window=0, **kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(positions=0), 2), (dict(positions=1 << 31), 2), (dict(rot=0), 2), (dict(rot=3), 2), (dict(rot=1026), 2), (dict(table=None), 1),
+    (dict(positions=0), 2), (dict(positions=1 << 31), 2), (dict(positions=(1 << 31) - 1, rot=128), 2), (dict(rot=0), 2), (dict(rot=3), 2), (dict(rot=1026), 2), (dict(table=None), 1),
     (dict(table=MIS), 3), (dict(base=0.0), 4), (dict(base=-1.0), 4), (dict(base=float("nan")), 4), (dict(base=float("inf")), 4),
     (dict(factor=0.0), 4), (dict(factor=float("nan")), 4), (dict(amplitude=float("inf")), 4), (dict(factor=2.0), 4),
     (dict(factor=2.0, low=1.0, high=0.5), 4), (dict(factor=2.0, high=1.0, original=-1.0), 4), (dict(factor=2.0, high=float("nan")), 4)])
