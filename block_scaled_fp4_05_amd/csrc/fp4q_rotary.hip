@@ -136,26 +136,41 @@ __global__ __launch_bounds__(256) void k_rotary(RotaryArgs a) {
   }
 }
 
-// Half layout where rot/2 is no multiple of the chunk: one pair, or one copied element, per item.
+// Half layout where rot/2 is no multiple of the chunk: a lane has one pair, or one copied element, of the heads that its
+// wave takes, wave w those of w, w + 4, ..., four of them in flight.
 template <typename T>
 __global__ __launch_bounds__(256) void k_rotary_pairs(RotaryArgs a) {
+  constexpr int AHEAD = 4;
   const int64_t t = blockIdx.x;
-  const int pos = a.positions[t];
+  const int pos = a.positions[t], wave = threadIdx.x >> 6;
   if (pos < 0 || pos >= a.table_rows) return;
   const T* x = static_cast<const T*>(a.x) + t * a.x_token;
   T* y = static_cast<T*>(a.y) + t * a.y_token;
   const int items = a.head_dim - a.half;   // pairs, then the elements past the rotated part
-  for (int i = threadIdx.x; i < items * a.heads; i += 256) {
-    const int h = i / items, e = i - h * items;
-    const T* xh = x + h * a.x_head;
-    T* yh = y + h * a.y_head;
-    if (e < a.half) {
-      const f32x2 v = a.table[(int64_t)pos * a.half + e];
-      float o, q;
-      turn(widen(xh[e]), widen(xh[e + a.half]), f32x2{v.x, a.sign * v.y}, o, q);
-      yh[e] = narrow<T>(o), yh[e + a.half] = narrow<T>(q);
-    } else {
-      yh[e + a.half] = xh[e + a.half];
+  for (int e = threadIdx.x & 63; e < items; e += 64) {
+    const bool pair = e < a.half;
+    f32x2 cs = a.table[(int64_t)pos * a.half + (pair ? e : 0)];
+    cs.y *= a.sign;
+    for (int h0 = wave; h0 < a.heads; h0 += 4 * AHEAD) {
+      T one[AHEAD], two[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const T* p = x + min(h0 + 4 * j, a.heads - 1) * a.x_head + e;
+        two[j] = p[a.half];
+        if (pair) one[j] = p[0];
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (h0 + 4 * j >= a.heads) break;
+        T* p = y + (h0 + 4 * j) * a.y_head + e;
+        if (pair) {
+          float o, q;
+          turn(widen(one[j]), widen(two[j]), cs, o, q);
+          p[0] = narrow<T>(o), p[a.half] = narrow<T>(q);
+        } else {
+          p[a.half] = two[j];
+        }
+      }
     }
   }
 }
@@ -168,7 +183,7 @@ __global__ __launch_bounds__(256) void k_rotary_pairs(RotaryArgs a) {
 // changes a code only next to a point halfway between two codes, or a scale next to its boundaries (1.75 2^k).  These have
 // at most five significant bits, so a result whose last 19 are within kNear of zero (one in 2^15) is computed again:
 // the products are exact in binary64, their difference is rounded to 53 bits and then to odd in fp32, which rounds to a
-// code as the difference does.  (All in binary64: 13460 tokens of 8 heads of 128 in 32 us, against 26.)
+// code as the difference does.  (All in binary64: 13460 tokens of 8 heads of 128 in 32 us, against 25.)
 // -----------------------------------------------------------------------------------------
 constexpr int kAppendTokens = 2;
 
