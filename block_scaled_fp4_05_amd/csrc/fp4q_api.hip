@@ -45,6 +45,11 @@ bool table_shape(int64_t rows, int64_t rot, int64_t head_dim) {
   return rows >= 1 && rows <= INT32_MAX && rot >= 2 && rot % 2 == 0 && rot <= head_dim;
 }
 bool stride16(int64_t stride, int dt) { return stride % (dt == FP4Q_BF16 ? 8 : 4) == 0; }
+// Whether the heads that a call writes may lie apart: no stride of an axis longer than one below head_dim.
+bool apart(int64_t tokens, int64_t heads, int64_t head_dim, int64_t token_stride, int64_t head_stride) {
+  const auto ok = [&](int64_t n, int64_t stride) { return n == 1 || stride >= head_dim || stride <= -head_dim; };
+  return ok(tokens, token_stride) && ok(heads, head_stride);
+}
 bool cache_shape(const fp4q_kv_cache& c) {
   return c.pages >= 1 && c.pages <= INT32_MAX && c.page_size >= 16 && c.page_size <= 1024 &&
          (c.page_size & (c.page_size - 1)) == 0 && c.kv_heads >= 1 && c.kv_heads <= 1024 && c.head_dim >= 32 &&
@@ -564,6 +569,9 @@ fp4q_status fp4q_rotary(const void* x, fp4q_dtype dt, int64_t tokens, int64_t he
   if (!aligned16(x) || !aligned16(y) || !aligned16(table) || !aligned4(positions) || !stride16(x_token_stride, dt) ||
       !stride16(x_head_stride, dt) || !stride16(y_token_stride, dt) || !stride16(y_head_stride, dt))
     return FP4Q_E_ALIGN;
+  if (!apart(tokens, heads, head_dim, y_token_stride, y_head_stride) ||
+      (x == y && ((tokens > 1 && x_token_stride != y_token_stride) || (heads > 1 && x_head_stride != y_head_stride))))
+    return FP4Q_E_ARG;
   fp4q::launch_rotary(fp4q::Rotary{x, dt, tokens, (int)heads, (int)head_dim, (int)rot_dim, x_token_stride,
                                    x_head_stride, y_token_stride, y_head_stride, positions, table, table_rows,
                                    (mode & FP4Q_ROTARY_INTERLEAVED) != 0, (mode & FP4Q_ROTARY_BACKWARD) != 0, y},
@@ -605,7 +613,7 @@ fp4q_status fp4q_attention_paged(const void* q, int64_t tokens, int64_t q_heads,
   if (!cache || !batch) return FP4Q_E_NULL;
   if (!attn_shape(*cache, *batch, tokens, q_heads, window)) return FP4Q_E_SHAPE;
   if (!q || !out || !scratch || !cache_present(*cache) || !batch_present(*batch)) return FP4Q_E_NULL;
-  if (!(scale > 0.0f) || scale > FLT_MAX || mask > FP4Q_ATTN_ALL || (mask == FP4Q_ATTN_ALL && window != 0))
+  if (!(scale >= 0x1p-126f && scale <= 0x1p127f) || mask > FP4Q_ATTN_ALL || (mask == FP4Q_ATTN_ALL && window != 0))
     return FP4Q_E_ARG;
   fp4q::Attention a = attn_call(tokens, q_heads, window);
   const fp4q::KvCache c = kv_cache(*cache);

@@ -509,7 +509,8 @@ int64_t fp4q_moe_scratch(int64_t tokens, int64_t d, int64_t hidden, int64_t expe
  * With FP4Q_ROTARY_BACKWARD or-ed to either, the transpose (-sin): x is the gradient of y and y that of x.
  *   x, y       [tokens][heads][head_dim] of type dt, elements of a head dense, tokens and heads at the
  *              given strides (in elements), e.g. the query and key heads inside the rows of a fused
- *              projection.  y may be x with the same strides (in place); no other overlap.
+ *              projection.  y may be x with the same strides (in place); no other overlap.  FP4Q_E_ARG: y == x with others,
+ *              or strides of y (of an axis longer than one) below head_dim.
  *   positions  device int32 [tokens].  A token whose position is outside 0 .. table_rows-1 is padding: its rows
  *              of y are not written.
  *   table      device float [table_rows][rot_dim/2][2], cosine and sine, e.g. from fp4q_rotary_table.
@@ -602,7 +603,7 @@ fp4q_status fp4q_kv_append(const void* k, const void* v, fp4q_dtype dt, int64_t 
  * FP4Q_ATTN_ALL (window 0 only).
  *   q      bf16 [tokens][q_heads][head_dim] at the given strides (elements), rotated already; query head h reads
  *          key/value head h / (q_heads / kv_heads).
- *   scale  > 0, finite.
+ *   scale  2^-126 .. 2^127.  Scores of 2^127 and more in magnitude count as infinite, and so does q . k past fp32's range.
  *   out    bf16 [tokens][q_heads][head_dim];  lse  float [tokens][q_heads] or NULL.
  *   scratch  device memory of at least fp4q_attention_paged_scratch bytes, 16-byte aligned; its contents before
  *            and after the call mean nothing.  Calls that may run at the same time need their own.

@@ -131,3 +131,15 @@ def test_helpers_refuse_what_the_library_cannot_see():
             B.kv_append({}, {}, t, t)
     with pytest.raises(TypeError):
         B.attention_paged(torch.zeros(4, 2, 64), {}, {})
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=2 * A, yh=0), dict(y=2 * A, yt=0), dict(y=2 * A, yh=120), dict(y=2 * A, yt=-120), dict(xt=512), dict(xh=512), dict(yt=512),
+    dict(xh=0, yh=0), dict(xt=0, yt=0)])
+def test_rotary_refuses_heads_that_are_written_over_each_other(kw):
+    assert _call("fp4q_rotary", ROTARY, kw) == 4
+
+
+@pytest.mark.parametrize("scale,status", [(2.0 ** -127, 4), (1e-45, 4), (2.0 ** 127.5, 4), (3.4e38, 4)])
+def test_scales_whose_scores_are_no_fp32_numbers(scale, status):
+    assert _attend(scale=scale) == status

@@ -244,3 +244,14 @@ def test_refusals():
         with pytest.raises(B.Fp4qError) as e:
             bad()
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -126, 2.0 ** 127])
+def test_smallest_and_largest_scale(scale):
+    """Queries that make up for the scale; few rows and many."""
+    for lens in ([(2, 40)], [(70, 130)]):
+        case = ref.Case(lens, 1, 64, 16)
+        cache, batch = case.tensors(DEV)
+        q = (_queries(case, 2).float() * (2.0 ** 120 if scale < 1 else 2.0 ** -124)).to(torch.bfloat16)
+        want = ref.attention(case, q.double().cpu().numpy(), scale)
+        _compare(B.attention_paged(q, cache, batch, scale=scale, with_lse=True), want)
