@@ -251,6 +251,13 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int seq, int t, float
 // prefix sum over the sequences, takes pair after pair, and writes what it has of each: the output where it took a pair
 // whole, else a piece for k_attn_join.  Within a pair each of its four waves takes every fourth tile of 32 keys, with the
 // next tile's loads in flight, and no barrier until the waves' results are joined at the pair's end.
+//
+// 64 single tokens of 32 query and 8 key/value heads of 128 on 301 to 16384 keys (554 MB): 108 us and 7 in the join.
+// The same loads alone, in the same order, take 95 us, 5.8 TB/s: bound by memory, and by some 12 us in which the
+// workgroups find their places and end.  Alternatives: two tiles of loads in flight per wave 121 together, three
+// workgroups on a CU (spills) 136, a workgroup per pair and fixed piece of its keys 127.  On few keys it is the chain of
+// trips to memory (lengths, page ids, codes; then the join) that bounds: one token on 4000 keys 7 + 4 us, 3 to 5
+// tokens of 7 sequences with windows of 1000 keys as many.
 // -----------------------------------------------------------------------------------------
 constexpr int kUnit = kTile * kWaves;
 
@@ -632,6 +639,14 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
 // The four waves of a workgroup take 32 rows each and go through the same tiles of 64 keys, staged through
 // LDS as bf16 for all of them.  The next tile's loads are in flight during a tile, and its LDS buffer is the other of
 // two, so one barrier per tile.
+//
+// Prompts of 1021 to 4096 tokens, 32 query and 8 key/value heads of 128, causal (180 GFLOP): 204 us, 880 TFLOP/s.
+// The MFMA pipe is busy for 40 % of it, and the vector instructions (exponentials, conversions of codes, P to
+// bf16) take about as long, so no one part bounds it: without the exponentials 196, without any of the softmax 186, without
+// the loads 196.  Alternatives: 64 rows to a wave (spills) 482; the next tile's scores during this one's exponentials,
+// with two sets of scores (spills), 224; two tiles of loads in flight 225.
+// 64 queries of 32 heads on a shared prefix of 16384 keys: 39 us and 8 in the join; one workgroup on a CU goes through 16
+// tiles of some 2 us each, bound by their latencies.
 // -----------------------------------------------------------------------------------------
 template <int D>
 struct Tile {
@@ -935,7 +950,8 @@ __global__ __launch_bounds__(256, kManyPerCu<D>) void k_attn_all(AttnArgs a) {
 
 // Joins the partial results of each row: one workgroup per query row, wave w takes every fourth in rounds of eight
 // with their loads in flight, then the waves are added in their order.  MANY: the rows of all tokens, and of them those of
-// sequences that many_rows took; else the most rows of every pair that few_rows took.
+// sequences that many_rows took; else the most rows of every pair that few_rows took.  2048 rows 6 to 8 us (11 MB), 32 rows
+// 3.5 to 4.5: two trips to memory, one after the other, what each row has and then its pieces.
 template <int D, int R, bool MANY>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int PER = D / 64, AHEAD = 8;
