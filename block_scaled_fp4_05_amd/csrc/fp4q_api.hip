@@ -86,7 +86,8 @@ fp4q::Attention attn_call(int64_t tokens, int64_t q_heads, int64_t window) {
   return a;
 }
 bool attn_shape(const fp4q_kv_cache& c, const fp4q_kv_batch& b, int64_t tokens, int64_t q_heads, int64_t window) {
-  if (!cache_shape(c) || !batch_shape(b, c) || !token_shape(tokens) || q_heads < 1 || q_heads > 4096 ||
+  // keys up to 2^30: places of keys, a tile past the last included, are 32-bit in the kernels
+  if (!cache_shape(c) || !batch_shape(b, c) || b.max_kv_len > (1 << 30) || !token_shape(tokens) || q_heads < 1 || q_heads > 4096 ||
       q_heads % c.kv_heads != 0 || tokens * q_heads >= ((int64_t)1 << 26) || window < 0 || window > INT32_MAX ||
       (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256))
     return false;

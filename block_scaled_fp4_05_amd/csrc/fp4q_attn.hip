@@ -70,9 +70,13 @@ struct Range {
 
 __device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// Shared keys of a group: whole pages, no more than the call's bound covers.
+__device__ __forceinline__ bool broken(const AttnArgs& a, int kv) { return kv < 0 || kv > a.max_kv; }
+
+// Shared keys of a group: whole pages, no more than the call's bound covers, and none past the end of its first
+// sequence, whose page table they are read by.
 __device__ __forceinline__ int shared_keys(const AttnArgs& a, int group) {
-  const int n = clamp_to(a.shared_lens[group], 0, (int)a.max_shared);
+  const int kv = a.kv_lens[clamp_to(a.group_starts[group], 0, a.seqs - 1)];
+  const int n = broken(a, kv) ? 0 : clamp_to(a.shared_lens[group], 0, min(kv, (int)a.max_shared));
   return n >> a.page_shift << a.page_shift;
 }
 
@@ -83,14 +87,13 @@ __device__ __forceinline__ int group_of(const AttnArgs& a, int s) {
 }
 
 // Own keys of a sequence: what its group does not share, from the first that its window's first query sees.
-// A length out of bounds gives no keys (and NaN, see `broken`).
-__device__ __forceinline__ bool broken(const AttnArgs& a, int kv) { return kv < 0 || kv > a.max_kv; }
+// None where it ends within the shared ones.  A length out of bounds gives no keys (and NaN, see `broken`).
 __device__ __forceinline__ Range own_range(const AttnArgs& a, int kv, int q_len, int shared) {
   if (broken(a, kv)) return Range{0, 0};
   int first = shared;
   if (a.window > 0) first = max(first, kv - min(q_len, a.max_q) + 1 - a.window);
-  first = min(first, kv) & ~(kHalf - 1);
-  return Range{first, kv};
+  first &= ~(kHalf - 1);   // whole pages are shared: none of their keys
+  return first < kv ? Range{first, kv} : Range{0, 0};
 }
 __device__ __forceinline__ int own_pieces(const AttnArgs& a, Range r) {
   return clamp_to((r.end - r.first + a.own.chunk - 1) / a.own.chunk, 1, max(a.own.chunks, 1));
@@ -969,6 +972,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     s = pair / a.kv_heads, t = in_pair / a.per_kv, h = pair % a.kv_heads * a.per_kv + in_pair % a.per_kv;
     // asked for along with the sequence's tokens; without any it means nothing
     taken = *reinterpret_cast<const int4*>(a.taken + 4 * ((int64_t)pair * 2 + in_pair / (16 * R)));
+    // (and so where lengths change under the call, but then it is used)
+    taken.x = clamp_to(taken.x, 0, a.shares - 1), taken.y = clamp_to(taken.y, 1, a.shares - taken.x);
+    taken.z = clamp_to(taken.z, 0, a.shared.chunks);
   }
   const int n = own_tokens(a, s, t0);
   if constexpr (!MANY) t += t0;

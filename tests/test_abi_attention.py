@@ -143,3 +143,10 @@ def test_rotary_refuses_heads_that_are_written_over_each_other(kw):
 @pytest.mark.parametrize("scale,status", [(2.0 ** -127, 4), (1e-45, 4), (2.0 ** 127.5, 4), (3.4e38, 4)])
 def test_scales_whose_scores_are_no_fp32_numbers(scale, status):
     assert _attend(scale=scale) == status
+
+
+def test_longest_keys():
+    """Places of keys are 32-bit in the kernels, a tile past the last included."""
+    kw = dict(seqs=1, tokens=1, max_q_len=1, page_size=1024, max_pages=1 << 21, kv_heads=2)
+    assert _need(**kw, max_kv_len=1 << 30) > 0
+    assert _need(**kw, max_kv_len=(1 << 30) + 1) == 0 and _attend(**kw, max_kv_len=(1 << 31) - 1) == 2

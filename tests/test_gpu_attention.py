@@ -255,3 +255,15 @@ def test_smallest_and_largest_scale(scale):
         q = (_queries(case, 2).float() * (2.0 ** 120 if scale < 1 else 2.0 ** -124)).to(torch.bfloat16)
         want = ref.attention(case, q.double().cpu().numpy(), scale)
         _compare(B.attention_paged(q, cache, batch, scale=scale, with_lse=True), want)
+
+
+@pytest.mark.parametrize("window", [0, 20], ids=["all", "window"])
+@pytest.mark.parametrize("lens", [[(1, 50), (1, 128), (2, 127), (1, 200), (1, 1), (0, 0)], [(50, 50), (40, 127), (1, 300), (33, 140)]],
+                         ids=["tokens", "prompts"])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64), (256, 32)])
+def test_sequences_that_end_within_the_shared_pages(dim, page, lens, window):
+    case = ref.Case(lens, 2, dim, page, groups=[(len(lens), 128)])
+    cache, batch = case.tensors(DEV)
+    q = _queries(case, 3)
+    want = ref.attention(case, q.float().cpu().numpy(), _scale(case), window)
+    _compare(B.attention_paged(q, cache, batch, scale=_scale(case), window=window, with_lse=True), want)
