@@ -648,7 +648,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
 // bf16) take about as long, so no one part bounds it: without the exponentials 196, without any of the softmax 186, without
 // the loads 196.  Alternatives: 64 rows to a wave (spills) 482; the next tile's scores during this one's exponentials,
 // with two sets of scores (spills), 224; two tiles of loads in flight 225.
-// 64 queries of 32 heads on a shared prefix of 16384 keys: 39 us and 8 in the join; one workgroup on a CU goes through 16
+// 64 queries of 32 heads on a shared prefix of 16384 keys: 40 us and 8 in the join; one workgroup on a CU goes through 16
 // tiles of some 2 us each, bound by their latencies.
 // -----------------------------------------------------------------------------------------
 template <int D>
