@@ -951,20 +951,24 @@ __global__ __launch_bounds__(256, kManyPerCu<D>) void k_attn_all(AttnArgs a) {
   else few_rows<D, R>(a, id - a.shared.grid - a.own.grid, lds.few);
 }
 
-// Joins the partial results of each row: one workgroup per query row, wave w takes every fourth in rounds of eight
-// with their loads in flight, then the waves are added in their order.  MANY: the rows of all tokens, and of them those of
-// sequences that many_rows took; else the most rows of every pair that few_rows took.  2048 rows 6 to 8 us (11 MB), 32 rows
+// Joins the partial results of each row.  MANY: the rows of all tokens, and of them those of sequences that many_rows
+// took, a wave for each, since they are many and have few pieces (the last 512 tokens of 2048, 32
+// heads, 69 us together with a workgroup for each row and 45 so).  Else the most
+// rows of every pair that few_rows took, a workgroup for each: wave w takes every fourth piece in rounds of eight
+// with their loads in flight, then the waves are added in their order.  2048 rows 6 to 8 us (11 MB), 32 rows
 // 3.5 to 4.5: two trips to memory, one after the other, what each row has and then its pieces.
 template <int D, int R, bool MANY>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int PER = D / 64, AHEAD = 8;
+  constexpr int PER = D / 64, AHEAD = MANY ? 4 : 8, WAVES = MANY ? 1 : kWaves;   // WAVES: that share a row
   __shared__ float lds_o[kWaves][D], lds_ml[kWaves][2];
   const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t all = (int64_t)a.tokens * q_heads;
   int s, t, h, t0;
   int4 taken = {0, 0, 0, 0};
   if constexpr (MANY) {
-    t = blockIdx.x / q_heads, h = blockIdx.x % q_heads;
+    const int64_t mine = (int64_t)blockIdx.x * kWaves + wave;
+    if (mine >= all) return;
+    t = (int)mine / q_heads, h = (int)mine % q_heads;
     s = wave_sequence(a.q_starts, a.seqs, t);
     if (s < 0) return;
   } else {
@@ -1006,11 +1010,11 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   float top = -kInf, sum = 0.0f, v[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) v[e] = 0.0f;
-  for (int i0 = wave; i0 < count; i0 += kWaves * AHEAD) {
+  for (int i0 = MANY ? 0 : wave; i0 < count; i0 += WAVES * AHEAD) {
     float o[AHEAD][PER], m[AHEAD], l[AHEAD], most = top;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      const int slot = i0 + kWaves * i, in = min(slot, count - 1);
+      const int slot = i0 + WAVES * i, in = min(slot, count - 1);
       const int64_t p = place(in);
       const bool piece = pieces && in >= before;
       const float *po = (piece ? a.piece_o : a.part_o) + p * D + PER * lane, *pm = (piece ? a.piece_ml : a.part_ml) + 2 * p;
@@ -1028,12 +1032,25 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     top = most;
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      if (i0 + kWaves * i >= count) break;
+      if (i0 + WAVES * i >= count) break;
       const float part = m[i] == -kInf ? 0.0f : exp2_of(m[i] - top);
       sum += part * l[i];   // 0 times a NaN stays one
 #pragma unroll
       for (int e = 0; e < PER; ++e) v[e] = __builtin_fmaf(part, o[i][e], v[e]);
     }
+  }
+  float out_lse;
+  if constexpr (MANY) {
+    const float inv = finish(a, s, t, top, sum, out_lse);
+    uint16_t* o = a.out + row * D + PER * lane;
+    if constexpr (PER == 1) {
+      o[0] = (uint16_t)bf16_pair(v[0] * inv, 0.0f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t*>(o + e) = bf16_pair(v[e] * inv, v[e + 1] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[row] = out_lse;
+    return;
   }
 #pragma unroll
   for (int e = 0; e < PER; ++e) lds_o[wave][PER * lane + e] = v[e];
@@ -1050,7 +1067,6 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     sum += part * lds_ml[u][1];
     r = __builtin_fmaf(part, lds_o[u][threadIdx.x], r);
   }
-  float out_lse;
   const float inv = finish(a, s, t, top, sum, out_lse);
   a.out[row * D + threadIdx.x] = (uint16_t)bf16_pair(r * inv, 0.0f);
   if (a.lse && threadIdx.x == 0) a.lse[row] = out_lse;
@@ -1059,12 +1075,17 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in one launch
 constexpr int kCus = 256;
 
-// `rows` and `keys`: the most that one of the `items` has.  Keys are split only until every CU has a workgroup: more and
-// smaller pieces cost more in joining them (64 queries of 32 heads on a prefix of 16384: 256 workgroups 59 us, 512 61, 1024 76).
+// `rows` and `keys`: the most that one of the `items` has.  Keys are split until every CU has a workgroup, and where the
+// pieces stay long, until it has the two that it holds and that hide each other's waits; more and smaller pieces cost
+// more in joining them.  One against two workgroups on a CU, 64 queries of 32 heads on a prefix of 16384 keys 42 and 50 us,
+// of 32768 64 and 67, of 65536 109 and 100 (pieces of 2048), of 131072 194 and 171; the last 512 tokens of 8192 112 and 97;
+// 1024 of 4096, of which the one has no pieces to join, 99 and 102, of 8192 187 and 173.
+constexpr int kLongPiece = 2048;
 Pass cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys, int64_t& grid) {
   const int64_t row_tiles = (rows + 127) / 128, units = items * cache.heads * row_tiles;
   const int64_t want = std::max<int64_t>(1, kCus / units);
   int64_t chunk = (keys + want - 1) / want;
+  if (const int64_t two = 2 * kCus / units; cache.head_dim <= 128 && two > want && keys >= two * kLongPiece) chunk = (keys + two - 1) / two;
   chunk = std::max<int64_t>(kUnit, (chunk + kUnit - 1) / kUnit * kUnit);
   chunk = std::min<int64_t>(chunk, (int64_t)kMaxPages << cache.page_shift);
   const int64_t chunks = (keys + chunk - 1) / chunk;
@@ -1114,7 +1135,7 @@ void launch_all(const AttnArgs& a, const Plan& p, int64_t rows, hipStream_t st) 
   if (p.grid > p.few) k_attn_all<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
   else k_attn_few<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
   if (p.join_few) k_attn_join<D, R, false><<<(unsigned)(a.seqs * a.kv_heads * a.most_rows), 256, 0, st>>>(a);
-  if (p.join_many) k_attn_join<D, 1, true><<<(unsigned)rows, 256, 0, st>>>(a);
+  if (p.join_many) k_attn_join<D, 1, true><<<(unsigned)((rows + kWaves - 1) / kWaves), 256, 0, st>>>(a);
 }
 
 template <int D>
@@ -1148,7 +1169,7 @@ void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t 
 
 bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) {
   const Plan p = plan(c, b, a);
-  return p.grid <= kMaxGrid && p.units <= ((int64_t)1 << 30) && (!p.join_many || a.tokens * a.q_heads <= kMaxGrid) &&
+  return p.grid <= kMaxGrid && p.units <= ((int64_t)1 << 30) &&
          (!p.join_few || b.seqs * c.heads * p.most_rows <= kMaxGrid);
 }
 

@@ -227,3 +227,17 @@ def test_before_the_projection():
     v = mxfp8_ref.fp4(w["codes"].cpu().numpy(), w["scales"].cpu().numpy())
     # the product's documented cut: 13 bits below the largest of a few neighbours, and fp32 sums of 512 terms
     assert np.all(np.abs(y.cpu().numpy() - x @ v.T) <= (2.0 ** -12 + 2.0 ** -15) * (np.abs(x) @ np.abs(v).T))
+
+
+@pytest.mark.parametrize("lens,groups", [([(40, 8300)], ()), ([(20, 8250), (20, 8300)], [(2, 8192)]), ([(40, 8300), (33, 8250)], [(2, 8192)])],
+                         ids=["own", "shared", "both"])
+def test_long_pieces(lens, groups):
+    """So many heads and keys that a CU has two workgroups, with long pieces of them; two heads are compared."""
+    case = ref.Case(lens, 128, 64, 64, groups=groups)
+    cache, batch = case.tensors(DEV)
+    q, some = _queries(case, 1), [3, 126]
+    o, lse = B.attention_paged(q, cache, batch, scale=_scale(case), with_lse=True)
+    for n in cache:
+        setattr(case, n, getattr(case, n)[:, some])
+    case.heads = len(some)
+    _compare((o[:, some], lse[:, some]), ref.attention(case, q[:, some].float().cpu().numpy(), _scale(case)))
