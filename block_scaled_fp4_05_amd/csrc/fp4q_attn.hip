@@ -86,14 +86,20 @@ __device__ __forceinline__ int group_of(const AttnArgs& a, int s) {
   return wave_sequence(a.group_starts, a.groups, s);
 }
 
-// Own keys of a sequence: what its group does not share, from the first that its window's first query sees.
-// None where it ends within the shared ones.  A length out of bounds gives no keys (and NaN, see `broken`).
-__device__ __forceinline__ Range own_range(const AttnArgs& a, int kv, int q_len, int shared) {
+// Own keys of a sequence: what its group does not share; under a window, from the first key that the first of the n
+// tokens that the call computes sees to the last one's own.  Their places go by the sequence's real length, q_end - t0
+// tokens from t0 on, of which n may be fewer.  None where it ends within the shared ones.  A length out of bounds gives no
+// keys (and NaN, see `broken`).
+__device__ __forceinline__ Range own_range(const AttnArgs& a, int kv, int q_end, int t0, int n, int shared) {
   if (broken(a, kv)) return Range{0, 0};
-  int first = shared;
-  if (a.window > 0) first = max(first, kv - min(q_len, a.max_q) + 1 - a.window);
+  int first = shared, end = kv;
+  if (a.window > 0) {
+    const int64_t pos = (int64_t)kv - ((int64_t)q_end - t0);   // the first token's
+    first = (int)max((int64_t)first, min(pos + 1 - a.window, (int64_t)kv));
+    end = (int)max((int64_t)0, min(pos + n, (int64_t)kv));
+  }
   first &= ~(kHalf - 1);   // whole pages are shared: none of their keys
-  return first < kv ? Range{first, kv} : Range{0, 0};
+  return first < end ? Range{first, end} : Range{0, 0};
 }
 __device__ __forceinline__ int own_pieces(const AttnArgs& a, Range r) {
   return clamp_to((r.end - r.first + a.own.chunk - 1) / a.own.chunk, 1, max(a.own.chunks, 1));
@@ -193,10 +199,10 @@ struct Work {
   int slot;                     // of the partial result; -1: the result is whole and goes to the output
 };
 
-// Tokens of sequence s that the call computes, from t0 on.
-__device__ __forceinline__ int own_tokens(const AttnArgs& a, int s, int& t0) {
-  t0 = clamp_to(a.q_starts[s], 0, a.tokens);
-  return min(clamp_to(a.q_starts[s + 1], t0, a.tokens) - t0, a.max_q);
+// Tokens of sequence s that the call computes, from t0 on; q_end: where all of its tokens end.
+__device__ __forceinline__ int own_tokens(const AttnArgs& a, int s, int& t0, int& q_end) {
+  t0 = clamp_to(a.q_starts[s], 0, a.tokens), q_end = a.q_starts[s + 1];
+  return min(clamp_to(q_end, t0, a.tokens) - t0, a.max_q);
 }
 
 template <bool SHARED>
@@ -212,10 +218,11 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, int head,
     first = 0, end = shared, w.slot = piece;
   } else {
     w.seq = item;
-    n = own_tokens(a, item, w.t0);
+    int q_end;
+    n = own_tokens(a, item, w.t0, q_end);
     if (n * a.per_kv <= kFewRows) return false;   // few_rows'
     const int g = group_of(a, item), shared = g >= 0 ? shared_keys(a, g) : 0;
-    const Range own = own_range(a, a.kv_lens[item], n, shared);
+    const Range own = own_range(a, a.kv_lens[item], q_end, w.t0, n, shared);
     const int pieces = own_pieces(a, own);
     if (piece >= pieces) return false;
     first = own.first, end = own.end;
@@ -285,7 +292,7 @@ __device__ __forceinline__ Pairs pairs_of(const AttnArgs& a, int s) {
     const int g = lane_find(a.group_starts, a.groups + 1, s);
     if (g >= 0 && g < a.groups) p.shared = shared_keys(a, g);
   }
-  p.keys = own_range(a, p.kv, n, p.shared);
+  p.keys = own_range(a, p.kv, p.q_end, p.t0, n, p.shared);
   p.units = max(1, (p.keys.end - p.keys.first + kUnit - 1) / kUnit);
   return p;
 }
@@ -963,7 +970,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   __shared__ float lds_o[kWaves][D], lds_ml[kWaves][2];
   const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t all = (int64_t)a.tokens * q_heads;
-  int s, t, h, t0;
+  int s, t, h, t0, q_end;
   int4 taken = {0, 0, 0, 0};
   if constexpr (MANY) {
     const int64_t mine = (int64_t)blockIdx.x * kWaves + wave;
@@ -980,7 +987,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     taken.x = clamp_to(taken.x, 0, a.shares - 1), taken.y = clamp_to(taken.y, 1, a.shares - taken.x);
     taken.z = clamp_to(taken.z, 0, a.shared.chunks);
   }
-  const int n = own_tokens(a, s, t0);
+  const int n = own_tokens(a, s, t0, q_end);
   if constexpr (!MANY) t += t0;
   if (t - t0 >= n || n * a.per_kv > kFewRows != MANY) return;
   const int64_t row = (int64_t)t * q_heads + h;
@@ -993,7 +1000,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
       const int g = group_of(a, s);
       shared = g >= 0 ? shared_keys(a, g) : 0, before = shared_pieces(a, shared);
     }
-    own = own_pieces(a, own_range(a, a.kv_lens[s], n, shared));
+    own = own_pieces(a, own_range(a, a.kv_lens[s], q_end, t0, n, shared));
   } else {
     before = taken.z, own = taken.y, pieces = own > 1;
     at = (2 * taken.x + 1) * a.piece_rows + ((t - t0) * a.per_kv + h % a.per_kv) % (16 * R);
