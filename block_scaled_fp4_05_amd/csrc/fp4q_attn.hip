@@ -190,6 +190,11 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 // tokens 215 -> 205 us).  Where they do not, m is the largest, whose p = 1 is exact in bf16 (on few keys out is
 // 1.9e-3 of its norm off instead of 2.3e-3).
 constexpr float kLag = 8.0f;
+// There p = 2^(s c - m), c = scale log2(e), with the product inside the fma: exact, while m is a rounded one.  Any m does as
+// long as p stays in range, but past 2^24 m's rounding counts in whole powers of two (at 2^36 p was infinite or zero for
+// every row).  From there on the product is rounded first, as m's was, so that the largest score gives p = 1; few_rows
+// always does so.  Looked at where m changes, it costs 0.2 % (prompts 204.7 us without, 205.1 with; in every tile 205.8).
+constexpr float kFar = 0x1p24f;
 
 // What a workgroup works on: the rows of an item (a sequence's query tokens, or in the shared pass a group's, times the
 // query heads of one key/value head) and a piece of its keys.
@@ -795,6 +800,7 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D>&
   float m = -kInf, l = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) acc[i] = zeros16();
+  bool far = false;   // some row's m is past kFar
   const bool idle = row0 + 32 * wave >= rows;
 
   auto compute = [&](int key0, int buf) {
@@ -834,18 +840,24 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D>&
     if (__any(mt > m + kLag)) {
       const float keep = mt == -kInf ? 1.0f : exp2_of(m - mt);
       m = mt, l *= keep;
+      far = __any(__builtin_fabsf(m) > kFar && m != -kInf);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) acc[i] *= keep;
     }
-    const float base = m == -kInf ? 0.0f : m;
+    float base = m == -kInf ? 0.0f : m, factor = a.scale_log2;
+    if (__builtin_expect(far, 0)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sc[i >> 4][i & 15] = sc[i >> 4][i & 15] * a.scale_log2 - base;
+      base = 0.0f, factor = 1.0f;
+    }
     v8b_a p[4];   // 16 keys each
 #pragma unroll
     for (int step = 0; step < 4; ++step) {
       u32x4_m words;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float x = exp2_of(__builtin_fmaf(sc[step >> 1][8 * (step & 1) + 2 * i], a.scale_log2, -base));
-        const float y = exp2_of(__builtin_fmaf(sc[step >> 1][8 * (step & 1) + 2 * i + 1], a.scale_log2, -base));
+        const float x = exp2_of(__builtin_fmaf(sc[step >> 1][8 * (step & 1) + 2 * i], factor, -base));
+        const float y = exp2_of(__builtin_fmaf(sc[step >> 1][8 * (step & 1) + 2 * i + 1], factor, -base));
         l += x + y;
         words[i] = bf16_pair(x, y);
       }
