@@ -8,8 +8,11 @@
 //
 // The queries of one key/value head (all of its query heads, of all the tokens of an item) are the
 // rows of one product.  S^T = K Q^T and O^T = V^T P^T run on the bf16 MFMA with fp32 sums: E4M3 times a power of two
-// is exact in bf16, so the codes are converted as they are used, the queries are bf16 already, and only P is rounded
-// to it (half a step, 2^-8 of each p_j at most; l sums the unrounded ones).  (S on the block-scaled MFMA, from the
+// is exact in bf16, so the codes are converted as they are used, the queries are bf16 already, and only P is rounded:
+// where rows are few to two bf16 parts, 2^-16 of each p_j at most, since their products cost next to nothing there (64 sequences
+// of up to 16384 keys 118.2 us, with one part 118.0; 8 tokens of 64 sequences 117.8, 116.0), where they are many to one,
+// 2^-8, since there the products count (two parts: prompts 264 us instead of 207, a prefix that 64 sequences share 50 instead of 47).
+// l sums the unrounded p_j.  (S on the block-scaled MFMA, from the
 // codes as they lie and the queries split into two E4M3 parts, needs no conversion of keys and as many MFMA cycles, but
 // its cut of the products left 1e-6 to 5e-6 of lse against 1e-7.)  S^T leaves a lane the scores of one row
 // and four neighbouring keys per 16, which is the layout that P^T's operand needs, given that V^T's takes its keys
@@ -187,8 +190,7 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 
 // Where the products count (many_rows) a row's m need not be its largest score so far: it follows only where that
 // is more than 2^kLag times larger, so that l and o, which have fp32's range, are rarely multiplied (prompts of 1021 to 4096
-// tokens 215 -> 205 us).  Where they do not, m is the largest, whose p = 1 is exact in bf16 (on few keys out is
-// 1.9e-3 of its norm off instead of 2.3e-3).
+// tokens 215 -> 205 us).
 constexpr float kLag = 8.0f;
 // There p = 2^(s c - m), c = scale log2(e), with the product inside the fma: exact, while m is a rounded one.  Any m does as
 // long as p stays in range, but past 2^24 m's rounding counts in whole powers of two (at 2^36 p was infinite or zero for
@@ -541,7 +543,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
       }
     }
     if (key0 + kUnit < stop) fetch(key0 + kUnit, f);
-    v8b_a p[R];
+    v8b_a p[R][2];   // in two parts, the second what the first's rounding left
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float sc[8];
@@ -569,22 +571,31 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
         for (int i = 0; i < D / 16; ++i) acc[r][i] *= keep;
       }
       const float base = m[r] == -kInf ? 0.0f : m[r];
-      uint32_t w[4];
+      u32x4_m w[2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float x = exp2_of(sc[2 * i] - base), y = exp2_of(sc[2 * i + 1] - base);
         l[r] += x + y;
-        w[i] = bf16_pair(x, y);
+        w[0][i] = bf16_pair(x, y);
+        w[1][i] = bf16_pair(x - bf16_lo(w[0][i]), y - bf16_hi(w[0][i]));
       }
-      p[r] = __builtin_bit_cast(v8b_a, u32x4_m{w[0], w[1], w[2], w[3]});
+      p[r][0] = __builtin_bit_cast(v8b_a, w[0]), p[r][1] = __builtin_bit_cast(v8b_a, w[1]);
     }
-    // O^T += V^T P^T, 16 elements of the head at a time.
+    // O^T += V^T P^T, 32 elements of the head at a time.
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const v4s_a x = read_transposed(tr + 32 * i), y = read_transposed(tr + 16 * W::ROW + 32 * i);
-      const v8b_a v = __builtin_bit_cast(v8b_a, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    for (int i = 0; i < D / 16; i += 2) {
+      v8b_a v[2];
 #pragma unroll
-      for (int r = 0; r < R; ++r) acc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[r], acc[r][i], 0, 0, 0);
+      for (int u = 0; u < 2; ++u) {
+        const v4s_a x = read_transposed(tr + 32 * (i + u)), y = read_transposed(tr + 16 * W::ROW + 32 * (i + u));
+        v[u] = __builtin_bit_cast(v8b_a, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < R; ++r) acc[r][i + u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[u], p[r][j], acc[r][i + u], 0, 0, 0);
     }
   };
   {

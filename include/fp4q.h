@@ -609,8 +609,10 @@ fp4q_status fp4q_kv_append(const void* k, const void* v, fp4q_dtype dt, int64_t 
  *   out    bf16 [tokens][q_heads][head_dim];  lse  float [tokens][q_heads] or NULL.
  *   scratch  device memory of at least fp4q_attention_paged_scratch bytes, 16-byte aligned; its contents before
  *            and after the call mean nothing.  Calls that may run at the same time need their own.
- * Scores, sums and the output are fp32 (in a fixed order: the same inputs give the same bits), probabilities are rounded to
- * bf16 for their product with the values: out is within 2e-3 of its norm of the exact value before its own rounding.
+ * Scores, sums and the output are fp32 (in a fixed order: the same inputs give the same bits).  In their product with the
+ * values the probabilities p_j = exp(s_j - lse) have 16 bits in sequences of up to 32 rows (tokens x q_heads / kv_heads); with more rows,
+ * and for the keys that a group shares, 8 bits (bf16).  Beside what fp32 leaves, an element of out is so at most
+ * 2^-16 or 2^-8 times sum_j p_j |v_j| off before its own rounding; on Gaussian values the 8 bits come to some 1.3e-3 to 1.6e-3 of out's norm.
  * A token that sees no key gets out = 0 and lse = -infinity; one that sees only scores of -infinity, NaN.
  * What a token does not see has no effect, whatever its codes.  A value that is not finite makes the elements
  * of out of the tokens that see it NaN or infinite, a key that is none makes their whole rows NaN.  A page outside the cache counts as
