@@ -987,22 +987,24 @@ __global__ __launch_bounds__(256, kManyPerCu<D>) void k_attn_all(AttnArgs a) {
 // rows of every pair that few_rows took, a workgroup for each: wave w takes every fourth piece in rounds of eight
 // with their loads in flight, then the waves are added in their order.  2048 rows 6 to 8 us (11 MB), 32 rows
 // 3.5 to 4.5: two trips to memory, one after the other, what each row has and then its pieces.
+// first: workgroups of the launches before.
 template <int D, int R, bool MANY>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, uint32_t first) {
   constexpr int PER = D / 64, AHEAD = MANY ? 4 : 8, WAVES = MANY ? 1 : kWaves;   // WAVES: that share a row
   __shared__ float lds_o[kWaves][D], lds_ml[kWaves][2];
   const int q_heads = a.kv_heads * a.per_kv, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t all = (int64_t)a.tokens * q_heads;
+  const uint32_t id = first + blockIdx.x;
   int s, t, h, t0, q_end;
   int4 taken = {0, 0, 0, 0};
   if constexpr (MANY) {
-    const int64_t mine = (int64_t)blockIdx.x * kWaves + wave;
+    const int64_t mine = (int64_t)id * kWaves + wave;
     if (mine >= all) return;
     t = (int)mine / q_heads, h = (int)mine % q_heads;
     s = wave_sequence(a.q_starts, a.seqs, t);
     if (s < 0) return;
   } else {
-    const int in_pair = blockIdx.x % a.most_rows, pair = blockIdx.x / a.most_rows;
+    const int in_pair = id % a.most_rows, pair = id / a.most_rows;
     s = pair / a.kv_heads, t = in_pair / a.per_kv, h = pair % a.kv_heads * a.per_kv + in_pair % a.per_kv;
     // asked for along with the sequence's tokens; without any it means nothing
     taken = *reinterpret_cast<const int4*>(a.taken + 4 * ((int64_t)pair * 2 + in_pair / (16 * R)));
@@ -1160,12 +1162,20 @@ Plan plan(const KvCache& c, const KvBatch& b, const Attention& a) {
   return p;
 }
 
+// As many launches as `all` workgroups of 256 threads need: one takes no more than 2^32 - 1 threads.
+template <typename F>
+void in_launches(int64_t all, F launch) {
+  for (int64_t first = 0; first < all; first += kMaxGrid) launch((unsigned)std::min(all - first, kMaxGrid), (uint32_t)first);
+}
+
 template <int D, int R>
 void launch_all(const AttnArgs& a, const Plan& p, int64_t rows, hipStream_t st) {
   if (p.grid > p.few) k_attn_all<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
   else k_attn_few<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
-  if (p.join_few) k_attn_join<D, R, false><<<(unsigned)(a.seqs * a.kv_heads * a.most_rows), 256, 0, st>>>(a);
-  if (p.join_many) k_attn_join<D, 1, true><<<(unsigned)((rows + kWaves - 1) / kWaves), 256, 0, st>>>(a);
+  if (p.join_few)
+    in_launches((int64_t)a.seqs * a.kv_heads * a.most_rows, [&](unsigned grid, uint32_t first) { k_attn_join<D, R, false><<<grid, 256, 0, st>>>(a, first); });
+  if (p.join_many)
+    in_launches((rows + kWaves - 1) / kWaves, [&](unsigned grid, uint32_t first) { k_attn_join<D, 1, true><<<grid, 256, 0, st>>>(a, first); });
 }
 
 template <int D>
