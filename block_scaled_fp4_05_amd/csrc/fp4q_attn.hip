@@ -37,11 +37,13 @@ constexpr int kWaves = 4;
 constexpr int kHalf = 16;       // keys of one MFMA, from a multiple of 16 on: never in two pages, whose least size it is
 constexpr int kMaxPages = 1024; // page ids of a workgroup of many_rows
 constexpr int kFewRows = 32;    // rows of a sequence and key/value head up to which few_rows takes it
+constexpr int kRowTile = 128;   // rows of a workgroup of many_rows
 
 // A pass of many_rows over its items' row tiles: pieces of `chunk` keys.
 struct Pass {
-  int items, row_tiles, chunk, chunks;   // chunks: the most pieces of a row tile; 0: no such pass
-  int grid;                              // workgroups
+  int items, row_tiles, chunk, chunks;   // row_tiles: the most that an item has; chunks: the most pieces of one; 0: no such pass
+  uint32_t grid;                         // workgroups: one for each key/value head, piece and place of a row tile
+  bool line;                             // places are those of `tiles_before`; else row_tiles for each item
 };
 
 struct AttnArgs {
@@ -55,7 +57,7 @@ struct AttnArgs {
   float scale_log2;                         // scale log2(e)
   uint16_t* out;
   float* lse;
-  int shares;                               // workgroups of few_rows
+  int shares, unit_shift;                   // workgroups of few_rows, whose units have 2^unit_shift keys
   // many_rows, two passes: groups with the keys that they share, sequences with their own
   Pass shared, own;
   // Partial results, each with its m and l: of the shared pass [piece][token][head][head_dim], behind them many_rows'
@@ -202,6 +204,7 @@ constexpr float kFar = 0x1p24f;
 // query heads of one key/value head) and a piece of its keys.
 struct Work {
   int head, seq, t0, rows;      // the item's first sequence and token, its rows
+  int kv, q_end;                // of a sequence
   int c0, c1;                   // keys
   int slot;                     // of the partial result; -1: the result is whole and goes to the output
 };
@@ -212,10 +215,33 @@ __device__ __forceinline__ int own_tokens(const AttnArgs& a, int s, int& t0, int
   return min(clamp_to(q_end, t0, a.tokens) - t0, a.max_q);
 }
 
+// Row tiles of a pass in a line, item after item, of which the host knows the sum of the lengths only.  Item i, whose rows
+// are those from row r on, has the places from min(i row_tiles, r / 128 + min(i, r / least)) on, least being the fewest rows
+// that an item with a tile has: both grow by its tiles at least, so no two tiles share a place, a search in the
+// starts finds a place's item without any sum over the items, and the line is no longer than what the host takes for r and i (`cut`).
 template <bool SHARED>
-__device__ __forceinline__ bool find_work(const AttnArgs& a, int item, int head, int piece, Work& w) {
-  const int chunk = SHARED ? a.shared.chunk : a.own.chunk;
+__device__ __forceinline__ int first_token(const AttnArgs& a, int i) {
+  return clamp_to(a.q_starts[SHARED ? clamp_to(a.group_starts[i], 0, a.seqs) : i], 0, a.tokens);
+}
+template <bool SHARED>
+__device__ __forceinline__ int tiles_before(const AttnArgs& a, int i) {
+  const int start = first_token<SHARED>(a, i), rows = start * a.per_kv;
+  const int places = rows / kRowTile + min(i, SHARED ? start : rows / (kFewRows + 1));
+  return (int)min((int64_t)i * (SHARED ? a.shared : a.own).row_tiles, (int64_t)places);
+}
+
+template <bool SHARED>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int place, int head, int piece, Work& w, int& row0) {
+  const Pass& pass = SHARED ? a.shared : a.own;
   w.head = head;
+  int item, tile;   // of the item's tiles from the last on, which under a causal mask has the most keys
+  if (__builtin_expect(pass.line, 0)) {
+    item = __builtin_amdgcn_readfirstlane(wave_last(pass.items, [&](int i) { return tiles_before<SHARED>(a, i) <= place; }));
+    if (item < 0) return false;
+    tile = place - tiles_before<SHARED>(a, item);
+  } else {
+    item = place % pass.items, tile = place / pass.items;
+  }
   int n, first, end;
   if constexpr (SHARED) {
     w.seq = clamp_to(a.group_starts[item], 0, a.seqs);
@@ -225,18 +251,20 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int item, int head,
     first = 0, end = shared, w.slot = piece;
   } else {
     w.seq = item;
-    int q_end;
-    n = own_tokens(a, item, w.t0, q_end);
+    n = own_tokens(a, item, w.t0, w.q_end), w.kv = a.kv_lens[item];
     if (n * a.per_kv <= kFewRows) return false;   // few_rows'
     const int g = group_of(a, item), shared = g >= 0 ? shared_keys(a, g) : 0;
-    const Range own = own_range(a, a.kv_lens[item], q_end, w.t0, n, shared);
+    const Range own = own_range(a, w.kv, w.q_end, w.t0, n, shared);
     const int pieces = own_pieces(a, own);
     if (piece >= pieces) return false;
     first = own.first, end = own.end;
     w.slot = pieces + shared_pieces(a, shared) == 1 ? -1 : a.shared.chunks + piece;
   }
   w.rows = n * a.per_kv;
-  w.c0 = min(first + piece * chunk, end), w.c1 = min(w.c0 + chunk, end);
+  const int last = pass.line ? (w.rows - 1) / kRowTile : pass.row_tiles - 1;
+  if (tile > last || (last - tile) * kRowTile >= w.rows) return false;
+  row0 = (last - tile) * kRowTile;
+  w.c0 = min(first + piece * pass.chunk, end), w.c1 = min(w.c0 + pass.chunk, end);
   return true;
 }
 
@@ -262,7 +290,7 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int seq, int t, float
 }
 
 // -----------------------------------------------------------------------------------------
-// Few rows per key/value head: the keys' bytes are what counts.  The work is a line of units, 128 keys of a pair
+// Few rows per key/value head: the keys' bytes are what counts.  The work is a line of units, 128 keys (more where they would pass 2^30) of a pair
 // (sequence and key/value head) with all of its 16 R rows, sequence by sequence, and every workgroup takes the same
 // number of units in a row, so that lengths, which the host does not know, balance.  It finds its place by a
 // prefix sum over the sequences, takes pair after pair, and writes what it has of each: the output where it took a pair
@@ -277,6 +305,8 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int seq, int t, float
 // tokens of 7 sequences with windows of 1000 keys as many.
 // -----------------------------------------------------------------------------------------
 constexpr int kUnit = kTile * kWaves;
+constexpr int kUnitShift = 7;
+static_assert(kUnit == 1 << kUnitShift, "");
 
 // Units and row tiles of a sequence's pairs.
 struct Pairs {
@@ -300,7 +330,7 @@ __device__ __forceinline__ Pairs pairs_of(const AttnArgs& a, int s) {
     if (g >= 0 && g < a.groups) p.shared = shared_keys(a, g);
   }
   p.keys = own_range(a, p.kv, p.q_end, p.t0, n, p.shared);
-  p.units = max(1, (p.keys.end - p.keys.first + kUnit - 1) / kUnit);
+  p.units = max(1, ((p.keys.end - p.keys.first - 1) >> a.unit_shift) + 1);
   return p;
 }
 
@@ -399,7 +429,8 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
   const int pair = (unit - seq_unit) / pairs.units, pair_unit = seq_unit + pair * pairs.units, k0 = unit - pair_unit;
   const int units = min(pairs.units - k0, unit_end - unit);
   const int head = pair % a.kv_heads, row_tile = pair / a.kv_heads, rows = pairs.rows, row0 = row_tile * 16 * R, t0 = pairs.t0;
-  const int c0 = pairs.keys.first + k0 * kUnit, c1 = min(c0 + units * kUnit, pairs.keys.end);
+  const int c0 = pairs.keys.first + (k0 << a.unit_shift);
+  const int c1 = k0 + units == pairs.units ? pairs.keys.end : c0 + (units << a.unit_shift);
   const bool whole = units == pairs.units;
   if (k0 == 0 && threadIdx.x == 0) {   // who has the pair: for k_attn_join
     int* at = a.taken + 4 * (((int64_t)seq * a.kv_heads + head) * 2 + row_tile);
@@ -705,7 +736,7 @@ struct ManyLds {
 };
 
 template <int D, bool SHARED>
-__device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D>& shared_lds) {
+__device__ __forceinline__ void many_rows(const AttnArgs& a, uint32_t id, ManyLds<D>& shared_lds) {
   using T = Tile<D>;
   uint8_t* lds = shared_lds.tile;
   auto& lds_bounds = shared_lds.bounds;
@@ -714,15 +745,12 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D>&
   const Pass& pass = SHARED ? a.shared : a.own;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = lane & 31, half = lane >> 5;
-  // Heads first, since workgroups go to the eight XCDs in turn and those of one head read the same keys; row tiles from the
-  // last on, which under a causal mask has the most keys.
+  // Heads first, since workgroups go to the eight XCDs in turn and those of one head read the same keys.
   const int head = id % a.kv_heads, piece = id / a.kv_heads % pass.chunks;
-  id /= pass.chunks * a.kv_heads;
-  const int item = id % pass.items, row_tile = pass.row_tiles - 1 - id / pass.items;
   Work w;
-  if (!find_work<SHARED>(a, item, head, piece, w)) return;
-  const int rows = w.rows, row0 = row_tile * 128, c1 = w.c1;
-  if (row0 >= rows) return;
+  int row0;
+  if (!find_work<SHARED>(a, id / (pass.chunks * a.kv_heads), head, piece, w, row0)) return;
+  const int rows = w.rows, c1 = w.c1;
   const int np = load_pages(a, w, lds_page), p0 = w.c0 >> a.page_shift;
 
   // Queries: lane (n, half) holds elements 32 i + 16 half .. + 15 of row n, as it does of the keys.
@@ -731,8 +759,12 @@ __device__ __forceinline__ void many_rows(const AttnArgs& a, int id, ManyLds<D>&
   {
     const int row = min(row0 + 32 * wave + n, rows - 1);   // behind the last row: that one again, not stored
     const int t = w.t0 + row / a.per_kv, h = head * a.per_kv + row % a.per_kv;
-    const int s = SHARED ? clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1) : w.seq;
-    const Range seen = visible_to(a, a.kv_lens[s], a.q_starts[s + 1], t, c1);
+    int kv = w.kv, q_end = w.q_end;
+    if constexpr (SHARED) {
+      const int s = clamp_to(lane_find(a.q_starts, a.seqs, t), 0, a.seqs - 1);
+      kv = a.kv_lens[s], q_end = a.q_starts[s + 1];
+    }
+    const Range seen = visible_to(a, kv, q_end, t, c1);
     lo = seen.first, hi = seen.end;
     const uint16_t* x = a.q + t * a.q_token + h * a.q_head;
 #pragma unroll
@@ -968,14 +1000,14 @@ __global__ __launch_bounds__(256, (kFewPerCu<D, R>)) void k_attn_few(AttnArgs a)
 }
 
 // One launch for all: the shared pass, the sequences with many rows, and those with few, which wait for memory while
-// the others multiply.
+// the others multiply.  first: workgroups of the launches before.
 template <int D, int R>
-__global__ __launch_bounds__(256, kManyPerCu<D>) void k_attn_all(AttnArgs a) {
+__global__ __launch_bounds__(256, kManyPerCu<D>) void k_attn_all(AttnArgs a, uint32_t first) {
   __shared__ union {
     FewLds<D, R> few;
     ManyLds<D> many;
   } lds;
-  const int id = blockIdx.x;
+  const uint32_t id = first + blockIdx.x;
   if (id < a.shared.grid) many_rows<D, true>(a, id, lds.many);
   else if (id < a.shared.grid + a.own.grid) many_rows<D, false>(a, id - a.shared.grid, lds.many);
   else few_rows<D, R>(a, id - a.shared.grid - a.own.grid, lds.few);
@@ -1105,16 +1137,24 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, uint32_t first) {
 }
 
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;   // workgroups of 256 threads in one launch
+constexpr int64_t kMaxScratch = (int64_t)1 << 38;
 constexpr int kCus = 256;
 
-// `rows` and `keys`: the most that one of the `items` has.  Keys are split until every CU has a workgroup, and where the
-// pieces stay long, until it has the two that it holds and that hide each other's waits; more and smaller pieces cost
-// more in joining them.  One against two workgroups on a CU, 64 queries of 32 heads on a prefix of 16384 keys 42 and 50 us,
+// `rows` and `keys`: the most that one of the `items` has, of `all` rows; least: the fewest that one with a tile has.  Where
+// places for every item's most tiles are more than three times what the rows can need, the tiles go in a line: such places
+// and a line, 255 single tokens and a chunk of 2048 on 8192 keys (50 times) 1790 and 1066 us, 16 groups of 16 tokens on
+// prefixes of 16384 (5.6 times) 505 and 275, 32 sequences of 1 to 600 tokens (5 times) 298 and 235, a prompt of 4096 with four
+// of 512 (3.2 times) 168 and 168, with four of 1024 (2.5 times) 193 and 198, three prompts of 1021 to 4096 (1.7 times) 199 and
+// 209: in a line the longest tiles do not all come first.
+// Keys are split until every CU has a workgroup, and where the pieces stay long, until it has the two that it holds and that
+// hide each other's waits; more and smaller pieces cost more in joining them.  One against two workgroups on a CU, 64 queries of 32 heads on a prefix of 16384 keys 42 and 50 us,
 // of 32768 64 and 67, of 65536 109 and 100 (pieces of 2048), of 131072 194 and 171; the last 512 tokens of 8192 112 and 97;
 // 1024 of 4096, of which the one has no pieces to join, 99 and 102, of 8192 187 and 173.
 constexpr int kLongPiece = 2048;
-Pass cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys, int64_t& grid) {
-  const int64_t row_tiles = (rows + 127) / 128, units = items * cache.heads * row_tiles;
+Pass cut(int64_t items, const KvCache& cache, int64_t rows, int64_t all, int64_t least, int64_t keys, int64_t& grid) {
+  const int64_t row_tiles = (rows + kRowTile - 1) / kRowTile, tiles = (all + kRowTile - 1) / kRowTile + std::min(items, all / least) - 1;
+  const bool line = items * row_tiles > 3 * tiles;
+  const int64_t units = cache.heads * (line ? tiles : items * row_tiles);
   const int64_t want = std::max<int64_t>(1, kCus / units);
   int64_t chunk = (keys + want - 1) / want;
   if (const int64_t two = 2 * kCus / units; cache.head_dim <= 128 && two > want && keys >= two * kLongPiece) chunk = (keys + two - 1) / two;
@@ -1122,12 +1162,13 @@ Pass cut(int64_t items, const KvCache& cache, int64_t rows, int64_t keys, int64_
   chunk = std::min<int64_t>(chunk, (int64_t)kMaxPages << cache.page_shift);
   const int64_t chunks = (keys + chunk - 1) / chunk;
   grid += units * chunks;
-  return Pass{(int)items, (int)row_tiles, (int)chunk, (int)chunks, (int)std::min<int64_t>(units * chunks, kMaxGrid)};
+  return Pass{(int)items, (int)row_tiles, (int)chunk, (int)chunks, (uint32_t)(units * chunks), line};
 }
 
 struct Plan {
   int r;                    // row tiles of few_rows' workgroups
-  int64_t few, grid, units; // its workgroups; all; most units of all pairs
+  int64_t few, grid;        // its workgroups; all
+  int unit_shift;
   int64_t most_rows, piece_rows;   // of a pair, and in one of its row tiles
   Pass own, shared;
   bool join_few, join_many;
@@ -1144,12 +1185,15 @@ Plan plan(const KvCache& c, const KvBatch& b, const Attention& a) {
   p.r = p.most_rows <= 16 || c.head_dim > 128 ? 1 : 2;   // (two 16-row tiles of 256 elements spill registers)
   p.piece_rows = std::min<int64_t>(p.most_rows, 16 * p.r);
   const int per_cu = c.head_dim == 64 ? (p.r == 1 ? kFewPerCu<64, 1> : kFewPerCu<64, 2>) : c.head_dim == 128 ? kFewPerCu<128, 1> : kFewPerCu<256, 1>;
-  const int64_t pair_units = (keys + kUnit - 1) / kUnit;
-  p.units = b.seqs * c.heads * ((p.most_rows + 16 * p.r - 1) / (16 * p.r)) * pair_units;
-  p.few = p.grid = std::min<int64_t>(kCus * per_cu, p.units);
+  const int64_t pairs = b.seqs * c.heads * ((p.most_rows + 16 * p.r - 1) / (16 * p.r));   // up to 2^27
+  p.unit_shift = kUnitShift;
+  while (pairs * (((keys - 1) >> p.unit_shift) + 1) > ((int64_t)1 << 30)) ++p.unit_shift;   // they are counted in 32 bits
+  const int64_t pair_units = ((keys - 1) >> p.unit_shift) + 1;
+  p.few = p.grid = std::min<int64_t>(kCus * per_cu, pairs * pair_units);
   const bool many = max_q * per_kv > kFewRows, shares = b.groups > 0 && b.max_shared_len > 0;
-  p.own = many ? cut(b.seqs, c, max_q * per_kv, keys, p.grid) : Pass{0, 0, kUnit, 0, 0};
-  p.shared = shares ? cut(b.groups, c, a.tokens * per_kv, b.max_shared_len, p.grid) : Pass{0, 0, kUnit, 0, 0};
+  const int64_t most = a.tokens * per_kv;
+  p.own = many ? cut(b.seqs, c, max_q * per_kv, most, kFewRows + 1, keys, p.grid) : Pass{0, 0, kUnit, 0, 0, false};
+  p.shared = shares ? cut(b.groups, c, most, most, per_kv, b.max_shared_len, p.grid) : Pass{0, 0, kUnit, 0, 0, false};
   p.join_few = pair_units > 1 || shares, p.join_many = many && (p.own.chunks > 1 || shares);
   p.slots = p.shared.chunks + std::max(p.own.chunks > 1 || shares ? p.own.chunks : 0, shares ? 1 : 0);
   auto put = [&](int64_t& at, int64_t bytes) { at = p.scratch, p.scratch += (bytes + 15) / 16 * 16; };
@@ -1170,7 +1214,8 @@ void in_launches(int64_t all, F launch) {
 
 template <int D, int R>
 void launch_all(const AttnArgs& a, const Plan& p, int64_t rows, hipStream_t st) {
-  if (p.grid > p.few) k_attn_all<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
+  if (p.grid > p.few)
+    in_launches(p.grid, [&](unsigned grid, uint32_t first) { k_attn_all<D, R><<<grid, 256, 0, st>>>(a, first); });
   else k_attn_few<D, R><<<(unsigned)p.grid, 256, 0, st>>>(a);
   if (p.join_few)
     in_launches((int64_t)a.seqs * a.kv_heads * a.most_rows, [&](unsigned grid, uint32_t first) { k_attn_join<D, R, false><<<grid, 256, 0, st>>>(a, first); });
@@ -1193,7 +1238,7 @@ void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t 
   a.max_pages = (int)b.max_pages, a.window = (int)std::min<int64_t>(t.window, 1 << 30), a.causal = t.causal;
   a.scale_log2 = t.scale * 1.4426950408889634f;
   a.out = static_cast<uint16_t*>(t.out), a.lse = t.lse;
-  a.shares = (int)p.few, a.shared = p.shared, a.own = p.own;
+  a.shares = (int)p.few, a.unit_shift = p.unit_shift, a.shared = p.shared, a.own = p.own;
   a.piece_rows = (int)p.piece_rows, a.most_rows = (int)p.most_rows;
   char* s = static_cast<char*>(t.scratch);
   a.part_o = reinterpret_cast<float*>(s), a.part_ml = reinterpret_cast<float*>(s + p.part_ml);
@@ -1207,11 +1252,9 @@ void launch(const KvCache& c, const KvBatch& b, const Attention& t, hipStream_t 
 
 }  // namespace
 
-bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) {
-  const Plan p = plan(c, b, a);
-  return p.grid <= kMaxGrid && p.units <= ((int64_t)1 << 30) &&
-         (!p.join_few || b.seqs * c.heads * p.most_rows <= kMaxGrid);
-}
+// Workgroups fit in 32 bits, too, where the scratch does: a pass has at most 3 (1 + 1/128) for each row and piece of it, which
+// take at least 256 bytes.
+bool attention_fits(const KvCache& c, const KvBatch& b, const Attention& a) { return plan(c, b, a).scratch <= kMaxScratch; }
 
 int64_t attention_scratch(const KvCache& c, const KvBatch& b, const Attention& a) { return plan(c, b, a).scratch; }
 

@@ -12,15 +12,16 @@
 namespace fp4q {
 namespace {
 
-// The last i in 0 .. n-1 with starts[i] <= t, or -1: 64 places at a time by the whole wave (t the same
+// The last i in 0 .. n-1 for which holds(i), or -1: 64 places at a time by the whole wave (holds the same
 // in all of its lanes), so one trip to memory for up to 64 sequences and two for 4096, where halving takes
-// six and twelve.  Starts do not fall; where they do, some place in range comes back.
-__device__ __forceinline__ int wave_find(const int32_t* __restrict__ starts, int n, int t) {
+// six and twelve.  It holds up to some place and not behind it; where that is not so, some place in range comes back.
+template <typename F>
+__device__ __forceinline__ int wave_last(int n, F holds) {
   const int lane = threadIdx.x & 63;
   int lo = 0;
   for (;;) {
     const int step = (n + 63) >> 6, at = lane * step;
-    const bool below = at < n && starts[lo + min(at, n - 1)] <= t;
+    const bool below = at < n && holds(lo + min(at, n - 1));
     const int count = __popcll(__ballot(below));
     if (count == 0) return lo - 1;
     const int skip = min((count - 1) * step, n - 1);
@@ -30,7 +31,7 @@ __device__ __forceinline__ int wave_find(const int32_t* __restrict__ starts, int
   }
 }
 
-// The same by one lane for its own t.
+// The last i in 0 .. n-1 with starts[i] <= t, which do not fall, or -1, by one lane for its own t.
 __device__ __forceinline__ int lane_find(const int32_t* __restrict__ starts, int n, int t) {
   int lo = -1, hi = n;   // starts[lo] <= t < starts[hi]
   while (hi - lo > 1) {
@@ -43,7 +44,7 @@ __device__ __forceinline__ int lane_find(const int32_t* __restrict__ starts, int
 
 // The sequence of token t (the same in the whole wave), or -1: t is behind the last or before the first.
 __device__ __forceinline__ int wave_sequence(const int32_t* __restrict__ q_starts, int seqs, int t) {
-  const int s = wave_find(q_starts, seqs + 1, t);
+  const int s = wave_last(seqs + 1, [&](int i) { return q_starts[i] <= t; });
   return s < seqs ? s : -1;
 }
 

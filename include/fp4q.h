@@ -589,7 +589,7 @@ typedef struct {
  *              A position that the table has no row for gives a key of NaN codes.
  * A token of no sequence is skipped, and so is one whose place is outside the page table or whose page is
  * outside the cache.  No two tokens of a call may have the same place: their bytes would mix.
- * max_q_len, max_kv_len and the groups are not used.  Shapes: 1 <= tokens < 2^24, table_rows < 2^31, rot_dim even, 2 .. head_dim;
+ * max_q_len, max_kv_len and the groups are looked at as everywhere, but not used.  Shapes: 1 <= tokens < 2^24, table_rows < 2^31, rot_dim even, 2 .. head_dim;
  * strides whole multiples of 16 bytes (FP4Q_E_ALIGN).  Alignment: 16 bytes (positions 4).
  */
 fp4q_status fp4q_kv_append(const void* k, const void* v, fp4q_dtype dt, int64_t tokens, int64_t k_token_stride,
@@ -618,8 +618,10 @@ fp4q_status fp4q_kv_append(const void* k, const void* v, fp4q_dtype dt, int64_t 
  * of out of the tokens that see it NaN or infinite, a key that is none makes their whole rows NaN.  A page outside the cache counts as
  * NaN keys, a kv_len outside 0 .. max_kv_len makes the sequence's rows NaN.  Query tokens past a sequence's first max_q_len,
  * and tokens of no sequence, are left as they were.
- * Shapes: head_dim 64, 128 or 256, q_heads a multiple of kv_heads up to 4096, 1 <= tokens < 2^24, tokens * q_heads < 2^26, 0 <= window < 2^31;
- * strides whole multiples of 16 bytes (FP4Q_E_ALIGN).  Alignment: 16 bytes (lse 4).
+ * Shapes: head_dim 64, 128 or 256, q_heads a multiple of kv_heads up to 4096, 1 <= tokens < 2^24, tokens * q_heads < 2^26, 0 <= window < 2^31,
+ * and a scratch of at most 2^38 bytes, which only prompts on contexts of many times 1024 pages pass (they take
+ * 4 (head_dim + 2) bytes for each query head of a token and 1024 pages); strides whole multiples of 16 bytes (FP4Q_E_ALIGN).
+ * Alignment: 16 bytes (lse 4).  out and lse overlap no input.
  */
 #define FP4Q_ATTN_CAUSAL 0u
 #define FP4Q_ATTN_ALL 1u

@@ -5,7 +5,7 @@ import torch
 
 import attention_ref as ref
 from block_scaled_fp4_05_amd import binding as B
-from test_gpu_attention import LEFT, _compare, _scale
+from test_gpu_attention import LEFT, _compare, _queries, _scale
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -45,3 +45,100 @@ def test_most_rows():
     want = _some_rows(case, q, some, window)
     for h in (0, 1, 1365, 2729, 2730):
         _compare((out[some, h:h + 1], lse[some, h:h + 1]), want)
+
+
+def _mixed(seqs, long, seed=0):
+    """Mostly single tokens, some drafts and some without tokens, and a prompt or a chunk behind every `long`."""
+    rng = np.random.default_rng(seed)
+    lens = []
+    for i in range(seqs):
+        n = int(rng.integers(33, 200)) if i % long == long - 1 else int(rng.integers(0, 4))
+        lens.append((n, n + int(rng.integers(0, 60))))
+    return lens
+
+
+@pytest.mark.parametrize("seqs,long", [(9, 4), (63, 31), (64, 20), (65, 64), (300, 50)])
+@pytest.mark.parametrize("window", [0, 25], ids=["all", "window"])
+def test_prompts_among_tokens(seqs, long, window):
+    case = ref.Case(_mixed(seqs, long, seqs), 1, 64, 16, seed=seqs, extra_tokens=3)
+    cache, batch = case.tensors(DEV)
+    q = _queries(case, 4)
+    got = B.attention_paged(q, cache, batch, scale=_scale(case), window=window, with_lse=True)
+    n = int(case.q_starts[-1])
+    want = ref.attention(case, q.float().cpu().numpy(), _scale(case), window)
+    _compare(tuple(t[:n] for t in got), tuple(t[:n] for t in want))
+
+
+@pytest.mark.parametrize("groups", [2, 9, 63, 64, 70, 200])
+def test_many_groups(groups):
+    """Groups of one to four sequences, some of several tokens, some empty, their prefixes of one to four pages."""
+    rng = np.random.default_rng(groups)
+    lens, shared = [], []
+    for g in range(groups):
+        count, prefix = int(rng.integers(1, 5)), 16 * int(rng.integers(1, 5))
+        shared.append((count, prefix))
+        lens += [(q, prefix + q + int(kv)) for q, kv in zip(rng.choice([0, 1, 1, 1, 2, 9, 40], count).tolist(), rng.integers(0, 40, count))]
+    case = ref.Case(lens, 1, 64, 16, groups=shared, seed=groups)
+    cache, batch = case.tensors(DEV)
+    q = _queries(case, 4)
+    want = ref.attention(case, q.float().cpu().numpy(), _scale(case))
+    _compare(B.attention_paged(q, cache, batch, scale=_scale(case), with_lse=True), want)
+
+
+def test_thousands_of_sequences():
+    """More than two searches of 64 places in the starts, with prompts between them and groups of two at the end."""
+    seqs = 4400
+    lens = _mixed(seqs, 500)
+    for i in range(4300, seqs, 2):
+        lens[i], lens[i + 1] = (1, 40), (2, 50)
+    case = ref.Case(lens, 1, 64, 16, groups=[(1, 0)] * 4300 + [(2, 32)] * 50)
+    cache, batch = case.tensors(DEV)
+    q = _queries(case, 4)
+    got = B.attention_paged(q, cache, batch, scale=_scale(case), with_lse=True)
+    some = [0, 1, 700, case.tokens - 1, case.tokens - 2, case.tokens - 3, case.tokens - 75]
+    for i in range(499, seqs, 500):
+        some += [int(case.q_starts[i]), int(case.q_starts[i]) + 17, int(case.q_starts[i + 1]) - 1]
+    _compare(tuple(t[some] for t in got), _some_rows(case, q, some))
+
+
+@pytest.mark.parametrize("window", [0, 60])
+def test_prompts_among_tokens_with_more_tokens_than_the_bound(window):
+    lens = [(1, 50)] * 20 + [(300, 1000)] + [(1, 70)] * 20 + [(120, 130), (0, 5)]
+    case = ref.Case(lens, 1, 64, 16)
+    cache, batch = case.tensors(DEV)
+    q = _queries(case, 4)
+    o, lse = B.attention_paged(q, cache, dict(batch, max_q_len=100), scale=_scale(case), window=window, with_lse=True)
+    want = ref.attention(case, q.float().cpu().numpy(), _scale(case), window)
+    done = [t for a, b in zip(case.q_starts, case.q_starts[1:]) for t in range(int(a), min(int(b), int(a) + 100))]
+    _compare((o[done], lse[done]), tuple(v[done] for v in want))
+
+
+@pytest.mark.parametrize("groups", [(), [(20, 512)]], ids=["own", "shared"])
+def test_bounds_far_past_the_lengths(groups):
+    """max_kv_len of 2^30: the keys of all pairs that the bounds allow are more than 32 bits can count in units of 128."""
+    heads = 64
+    lens = [(1, 513 + 71 * i * i) for i in range(10)] + [(i, 600 + 16 * i) for i in range(10)]
+    case = ref.Case(lens, heads, 64, 1024 if not groups else 512, groups=groups)
+    cache, batch = case.tensors(DEV)
+    width = (1 << 30) // case.page
+    table = torch.full((len(lens), width), -7, dtype=torch.int32, device=DEV)
+    table[:, :case.page_table.shape[1]] = batch["page_table"]
+    q, some = _queries(case, 1), [0, 31, 63]
+    o, lse = B.attention_paged(q, cache, dict(batch, page_table=table, max_kv_len=1 << 30), scale=_scale(case), with_lse=True)
+    for n in cache:
+        setattr(case, n, getattr(case, n)[:, some])
+    case.heads = len(some)
+    _compare((o[:, some], lse[:, some]), ref.attention(case, q[:, some].float().cpu().numpy(), _scale(case)))
+
+
+def test_a_chunk_among_many_sequences_in_small_pages():
+    """1023 single tokens and a chunk of 8192 tokens, where contexts may have 131072 positions in pages of 16."""
+    lens = [(1, 40)] * 1023 + [(8192, 20000)]
+    case = ref.Case(lens, 1, 64, 16)
+    cache, batch = case.tensors(DEV)
+    table = torch.full((len(lens), 8192), -7, dtype=torch.int32, device=DEV)
+    table[:, :case.page_table.shape[1]] = batch["page_table"]
+    q = _queries(case, 4)
+    got = B.attention_paged(q, cache, dict(batch, page_table=table, max_kv_len=131072), scale=_scale(case), with_lse=True)
+    some = [0, 500, 1022, 1023, 1024, 5000, 9213, 9214]
+    _compare(tuple(t[some] for t in got), _some_rows(case, q, some))
