@@ -61,10 +61,8 @@ struct RotaryArgs {
   const int32_t* positions;
   const f32x2* table;
   int64_t table_rows, x_token, x_head, y_token, y_head;   // strides in elements
-  int64_t tokens;
   int heads, head_dim, half;
   float sign;   // 1, or -1 for the gradient
-  bool interleaved;
 };
 
 __device__ __forceinline__ void turn(float a, float b, f32x2 cs, float& ya, float& yb) {
@@ -390,8 +388,7 @@ void launch_rotary_table(int64_t positions, int rot, double base, double factor,
 
 void launch_rotary(const Rotary& r, hipStream_t st) {
   const RotaryArgs a{r.x, r.y, r.positions, reinterpret_cast<const f32x2*>(r.table), r.table_rows, r.x_token, r.x_head,
-                     r.y_token, r.y_head, r.tokens, r.heads, r.head_dim, r.rot / 2, r.backward ? -1.0f : 1.0f,
-                     r.interleaved};
+                     r.y_token, r.y_head, r.heads, r.head_dim, r.rot / 2, r.backward ? -1.0f : 1.0f};
   const unsigned grid = (unsigned)r.tokens, lds = (unsigned)a.half * 8u;
   const int n = r.dtype ? 8 : 4;
   if (r.interleaved) {
