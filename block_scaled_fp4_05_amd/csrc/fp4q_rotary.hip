@@ -197,7 +197,8 @@ struct AppendArgs {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
 };
 
-// fp32 next to r towards zero with its last bit set where r is no fp32 number: rounds to fewer bits as r does.
+// fp32 next to r towards zero with its last bit set where r is no fp32 number: rounds to fewer bits as r does (past fp32's
+// range its largest number).
 __device__ __forceinline__ float to_odd(double r) {
   const float f = (float)r;
   const double back = (double)f;

@@ -581,8 +581,8 @@ typedef struct {
 
 /*
  * Keys and values of a call's tokens into the cache, the keys rotated on the way (fp4q_rotary's forward
- * formula) and both rounded to MXFP8.  A rotated key is rounded once, from the formula's value; without a table (NULL)
- * keys are stored as they come.
+ * formula) and both rounded to MXFP8.  A rotated key is rounded once, from the formula's value (one past fp32's range
+ * counts as fp32's largest number); without a table (NULL) keys are stored as they come.
  *   k, v       [tokens][kv_heads][head_dim] of type dt at the given strides (elements; heads dense inside).
  *   table      as fp4q_rotary, or NULL; rot_dim and mode (without FP4Q_ROTARY_BACKWARD) are read only with it.
  *   positions  device int32 [tokens]: the rows of the table; NULL: each token's place in its sequence.
