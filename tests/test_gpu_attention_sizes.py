@@ -142,3 +142,38 @@ def test_a_chunk_among_many_sequences_in_small_pages():
     got = B.attention_paged(q, cache, dict(batch, page_table=table, max_kv_len=131072), scale=_scale(case), with_lse=True)
     some = [0, 500, 1022, 1023, 1024, 5000, 9213, 9214]
     _compare(tuple(t[some] for t in got), _some_rows(case, q, some))
+
+
+def test_captured_and_replayed_while_the_prompts_move():
+    """Most tokens are a prompt's, of another sequence in each replay; the bounds and the number of tokens stay."""
+    seqs, tokens = 40, 400
+    g = np.random.default_rng(0)
+    case = ref.Case([(1, 420)] * seqs, 2, 64, 16)
+    cache, batch = case.tensors(DEV)
+    batch.update(max_q_len=300, group_starts=torch.tensor([0, 3, 40], dtype=torch.int32, device=DEV),
+                 shared_lens=torch.zeros(2, dtype=torch.int32, device=DEV), max_shared_len=64)
+    q = torch.randn(tokens, 8, 64, device=DEV).to(torch.bfloat16)
+    batch["page_table"][1:3, :4] = batch["page_table"][:1, :4]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        B.attention_paged(q, cache, batch, with_lse=True)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = B.attention_paged(q, cache, batch, with_lse=True)
+    for i in range(12):
+        n = g.integers(0, 3, seqs)
+        n[(7 * i) % seqs] = 300 if i % 3 else 0
+        n[(7 * i + 5) % seqs] = g.integers(9, 40)
+        starts = np.minimum(np.concatenate([[0], np.cumsum(n)]), tokens)
+        batch["q_starts"].copy_(torch.from_numpy(starts.astype(np.int32)))
+        batch["shared_lens"][0] = 64 * (i % 2)
+        q.copy_(torch.randn(q.shape, device=DEV))
+        out.fill_(LEFT), lse.fill_(LEFT)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = B.attention_paged(q, cache, batch, with_lse=True)
+        end = int(starts[-1])
+        assert torch.equal(out[:end], want[0][:end]) and torch.equal(lse[:end], want[1][:end]), i
+        assert (out[end:] == LEFT).all() and not (lse[:end] == LEFT).any(), i
