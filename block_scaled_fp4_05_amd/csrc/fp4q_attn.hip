@@ -698,7 +698,7 @@ __device__ __forceinline__ void few_rows(const AttnArgs& a, int me, FewLds<D, R>
 // two, so one barrier per tile.
 //
 // Prompts of 1021 to 4096 tokens, 32 query and 8 key/value heads of 128, causal (180 GFLOP): 204 us, 880 TFLOP/s.
-// The MFMA pipe is busy for 40 % of it, and the vector instructions (exponentials, conversions of codes, P to
+// The MFMA pipe is busy for 36 % of it, and the vector instructions (exponentials, conversions of codes, P to
 // bf16) take about as long, so no one part bounds it: without the exponentials 196, without any of the softmax 186, without
 // the loads 196.  Alternatives: 64 rows to a wave (spills) 482; the next tile's scores during this one's exponentials,
 // with two sets of scores (spills), 224; two tiles of loads in flight 225.
