@@ -47,6 +47,30 @@ def test_most_rows():
         _compare((out[some, h:h + 1], lse[some, h:h + 1]), want)
 
 
+def test_more_workgroups_than_a_launch_takes():
+    """16500 groups of one token on 1023 heads: a row tile and a joined row for each, all on the same pages.  Every 16th token sees the same."""
+    seqs, heads, page = 16500, 1023, 16
+    case = ref.Case([(1, 17 + i) for i in range(16)], heads, 64, page, groups=[(16, 16)])
+    cache, batch = case.tensors(DEV)
+    again = torch.arange(seqs, device=DEV) % 16
+    i32 = dict(dtype=torch.int32, device=DEV)
+    batch = {"q_starts": torch.arange(seqs + 1, **i32), "kv_lens": batch["kv_lens"][again], "page_table": batch["page_table"][again].contiguous(),
+             "max_q_len": 1, "max_kv_len": case.max_kv_len, "group_starts": torch.arange(seqs + 1, **i32),
+             "shared_lens": torch.full((seqs,), 16, **i32), "max_shared_len": 16}
+    one = torch.randn(1, 1, 64, generator=torch.Generator(device=DEV).manual_seed(0), device=DEV).to(torch.bfloat16)
+    o, lse = B.attention_paged(one.expand(seqs, heads, 64), cache, batch, scale=_scale(case), with_lse=True)
+    first = o[:16].clone(), lse[:16].clone()
+    for at in range(16, seqs, 16):
+        n = min(16, seqs - at)
+        assert torch.equal(o[at:at + n], first[0][:n]) and torch.equal(lse[at:at + n], first[1][:n]), at
+    some = [0, 500, 1022]
+    for n in cache:
+        setattr(case, n, getattr(case, n)[:, some])
+    case.heads = len(some)
+    q = one.expand(16, len(some), 64).float().cpu().numpy()
+    _compare((first[0][:, some], first[1][:, some]), ref.attention(case, q, _scale(case)))
+
+
 def _mixed(seqs, long, seed=0):
     """Mostly single tokens, some drafts and some without tokens, and a prompt or a chunk behind every `long`."""
     rng = np.random.default_rng(seed)
