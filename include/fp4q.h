@@ -566,7 +566,8 @@ typedef struct {
  *               sequences group_starts[g] .. group_starts[g+1]-1 ([groups+1], not falling) have the same
  *               first shared_lens[g] / page_size pages (rounded down), or as many of them as their own
  *               length reaches.  Those that the group's first sequence reaches, fp4q_attention_paged then reads
- *               once for all of a group's queries; what is computed is the same.  fp4q_kv_append ignores it.
+ *               once for all of a group's queries; what is computed is the same, but for the bits of the
+ *               probabilities (see there).  fp4q_kv_append ignores it.
  *   max_shared_len          at least the largest shared_lens; 0 <= max_shared_len <= max_kv_len.
  * Shapes: 1 <= seqs <= 65536, groups <= seqs, max_pages >= 1, max_q_len >= 1, max_kv_len >= 1, all < 2^31
  * (fp4q_attention_paged: max_kv_len <= 2^30).
